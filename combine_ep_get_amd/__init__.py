@@ -10,6 +10,14 @@ raises -- there is no fallback of any kind.
     recv_x, recv_scales, recv_src_idx, recv_w = dispatch(x, topk_weights, lay, use_fp8)
     y = combine(expert_out, lay, topk_weights)
 
+Around them: ``route`` decides ``topk_idx`` and ``topk_weights`` from gate
+logits; ``moe_layer`` is the whole expert layer for a few tokens (up to 256),
+without dispatch and combine, on bf16 or 4-bit expert weights
+(``QuantWeight``); ``quant_linear`` multiplies a few rows with a 4-bit weight.
+
+    topk_idx, topk_weights = route(logits, num_topk, bias=b, num_groups=8, topk_groups=4)
+    y = moe_layer(x, topk_idx, topk_weights, w13, w2)
+
 Options (same kernels): ``topk_idx`` int32 or int64; ``dispatch(...,
 x_scales=sf)`` for pre-quantised e4m3 input, ``zero_padding=True``,
 ``cumulative_stats=t``; ``cu_budget=n`` on dispatch and combine;
@@ -20,6 +28,7 @@ boundaries", sec. 1.1 and 1.4): num_tokens_per_rank, num_tokens_per_expert,
 is_token_in_rank, expert_alignment, num_experts.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -69,9 +78,39 @@ class LLArgs(ctypes.Structure):
                 ("recv_topk_weights", ctypes.c_void_p), ("cumulative_recv_stats", ctypes.c_void_p)]
 
 
+class RouteArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("topk_idx", ctypes.c_void_p), ("topk_weights", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("num_topk", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("logits_bytes", ctypes.c_int32), ("topk_idx_bytes", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class WeightDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("group", ctypes.c_int32)]
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p),
+                ("topk_weights", ctypes.c_void_p), ("w13", WeightDesc), ("w2", WeightDesc),
+                ("y", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("inter", ctypes.c_int32)]
+
+
+EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX = 0, 1
+EP_WEIGHT_BF16, EP_WEIGHT_INT4, EP_WEIGHT_MXFP4 = 0, 1, 2
+EP_MAX_FEW_TOKENS = 256
+EP_MAX_CONTRACTION = 65536
+
 EXPORTS = ("ep_recv_capacity", "ep_workspace_bytes", "ep_get_layout", "ep_dispatch",
            "ep_dispatch_ex", "ep_combine", "ep_layout_error", "ep_status_str", "ep_ll_capacity",
-           "ep_ll_dispatch", "ep_ll_dispatch_ex", "ep_get_layout_noalloc")
+           "ep_ll_dispatch", "ep_ll_dispatch_ex", "ep_get_layout_noalloc",
+           "ep_route", "ep_moe_workspace_bytes", "ep_moe_layer", "ep_quant_linear")
 EP_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 2 << 20
 EP_LAYOUT_ERR_OVERFLOW = 2
@@ -124,6 +163,14 @@ def load(path):
     L.ep_ll_dispatch.argtypes = [P, ctypes.c_int32] + [vp] * 10 + [vp]
     L.ep_ll_dispatch_ex.restype = ctypes.c_int
     L.ep_ll_dispatch_ex.argtypes = [P, ctypes.c_int32, ctypes.POINTER(LLArgs), vp]
+    L.ep_route.restype = ctypes.c_int
+    L.ep_route.argtypes = [ctypes.POINTER(RouteArgs), vp]
+    L.ep_moe_workspace_bytes.restype = i64
+    L.ep_moe_workspace_bytes.argtypes = [P, ctypes.c_int32]
+    L.ep_moe_layer.restype = ctypes.c_int
+    L.ep_moe_layer.argtypes = [P, ctypes.POINTER(MoeArgs), vp]
+    L.ep_quant_linear.restype = ctypes.c_int
+    L.ep_quant_linear.argtypes = [ctypes.c_int32] * 3 + [vp, ctypes.POINTER(WeightDesc), vp, vp]
     return L
 
 
@@ -493,6 +540,200 @@ def ep_ll_dispatch_ex(p, max_tokens_per_rank, args, stream=None):
                                                         ctypes.byref(args), st))
 
 
+# ------------------------------------------------- router and experts' products
+def _on(t, call):
+    """call(stream) with t's device current; its current stream there."""
+    import torch
+    if t.device.index == torch.cuda.current_device():
+        return call(_stream())
+    with torch.cuda.device(t.device):
+        return call(_stream())
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def route(logits, num_topk, bias=None, scoring="sigmoid", num_groups=1, topk_groups=1,
+          group_top=1, renormalize=True, scale=1.0, idx_dtype=None, out=None):
+    """Gate logits [N, E] (float32 or bf16) to (topk_idx [N, K], topk_weights
+    [N, K] float32), the inputs of get_layout, ll_dispatch and moe_layer; see
+    ep_route.  ``bias`` [E] float32 shifts the selection only; ``scoring`` is
+    "sigmoid" or "softmax"; ``idx_dtype`` int32 (default) or int64; ``out`` a
+    pair of preallocated outputs."""
+    import torch
+    N, E = logits.shape
+    K = int(num_topk)
+    size = {torch.float32: 4, torch.bfloat16: 2}.get(logits.dtype)
+    if size is None:
+        raise ValueError(f"logits: need float32 or bfloat16, got {logits.dtype}")
+    _need(logits, logits.dtype, (N, E), "logits")
+    if scoring not in ("sigmoid", "softmax"):
+        raise ValueError(f"scoring: need 'sigmoid' or 'softmax', got {scoring!r}")
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    if K < 1:
+        raise ValueError(f"num_topk: need at least 1, got {K}")
+    if out is None:
+        idx = torch.empty((N, K), dtype=idx_dtype or torch.int32, device=logits.device)
+        w = torch.empty((N, K), dtype=torch.float32, device=logits.device)
+    else:
+        idx, w = out
+        if idx_dtype is not None and idx.dtype != idx_dtype:
+            raise ValueError(f"topk_idx: need {idx_dtype}, got {idx.dtype}")
+        _need(idx, idx.dtype, (N, K), "topk_idx")
+        _need(w, torch.float32, (N, K), "topk_weights")
+    _same_device(logits, bias=bias, topk_idx=idx, topk_weights=w)
+    a = RouteArgs(logits.data_ptr(), None if bias is None else bias.data_ptr(), idx.data_ptr(),
+                  w.data_ptr(), N, E, K, num_groups, topk_groups, group_top,
+                  EP_SCORE_SOFTMAX if scoring == "softmax" else EP_SCORE_SIGMOID,
+                  int(bool(renormalize)), size, _idx_bytes(idx), scale)
+    _check("ep_route", _on(logits, lambda st: lib().ep_route(ctypes.byref(a), st)))
+    return idx, w
+
+
+class QuantWeight:
+    """A 4-bit weight [..., rows, cols] on the GPU (ep_weight_t): ``codes`` uint8
+    [..., rows, cols/2] as pack_codes lays them out, and
+    ``fmt`` "int4": ``scales`` bf16 [..., rows, cols/group], optional ``zeros``
+    uint8 of that shape (8 without), group 32, 64 or 128;
+    ``fmt`` "mxfp4": ``scales`` uint8 (E8M0) [..., rows, cols/32], group 32."""
+
+    def __init__(self, codes, scales, zeros=None, group=None, fmt="int4"):
+        import torch
+        if fmt not in ("int4", "mxfp4"):
+            raise ValueError(f"fmt: need 'int4' or 'mxfp4', got {fmt!r}")
+        group = (128 if fmt == "int4" else 32) if group is None else int(group)
+        if group not in ((32, 64, 128) if fmt == "int4" else (32,)):
+            raise ValueError(f"group: {group} is not a group size of {fmt}")
+        if codes.dim() < 2:
+            raise ValueError("codes: need [..., rows, cols/2]")
+        self.shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+        if self.shape[-1] % group != 0:
+            raise ValueError(f"cols {self.shape[-1]} is no multiple of the group {group}")
+        per = (*codes.shape[:-1], self.shape[-1] // group)
+        _need(codes, torch.uint8, codes.shape, "codes")
+        _need(scales, torch.bfloat16 if fmt == "int4" else torch.uint8, per, "scales")
+        if zeros is not None:
+            if fmt != "int4":
+                raise ValueError("zeros: only int4 has zero points")
+            _need(zeros, torch.uint8, per, "zeros")
+        _same_device(codes, scales=scales, zeros=zeros)
+        self.codes, self.scales, self.zeros, self.group, self.fmt = codes, scales, zeros, group, fmt
+        self.device = codes.device
+
+    def desc(self):
+        return WeightDesc(self.codes.data_ptr(), self.scales.data_ptr(),
+                          None if self.zeros is None else self.zeros.data_ptr(),
+                          EP_WEIGHT_INT4 if self.fmt == "int4" else EP_WEIGHT_MXFP4, self.group)
+
+
+def pack_codes(codes, fmt="int4"):
+    """4-bit codes, one per byte in column order [..., cols] (uint8, 0..15,
+    cols % 8 == 0), as the bytes [..., cols/2] that QuantWeight takes.  Done
+    once when a model is loaded, in torch, on any device."""
+    import torch
+    order = (0, 2, 4, 6, 1, 3, 5, 7) if fmt == "int4" else (0, 1, 2, 3, 4, 5, 6, 7)
+    if fmt not in ("int4", "mxfp4") or codes.dtype != torch.uint8 or codes.shape[-1] % 8 != 0:
+        raise ValueError("pack_codes: need uint8 codes, cols % 8 == 0, fmt 'int4' or 'mxfp4'")
+    c = codes.reshape(*codes.shape[:-1], -1, 8)
+    c = torch.stack([c[..., j] for j in order], dim=-1) & 15
+    return (c[..., 0::2] | (c[..., 1::2] << 4)).reshape(*codes.shape[:-1], -1)
+
+
+def _weight_desc(w, shape, name):
+    import torch
+    if isinstance(w, QuantWeight):
+        if w.shape != shape:
+            raise ValueError(f"{name}: need {shape}, got {w.shape}")
+        return w.desc()
+    _need(w, torch.bfloat16, shape, name)
+    return WeightDesc(w.data_ptr(), None, None, EP_WEIGHT_BF16, 0)
+
+
+@functools.lru_cache(maxsize=256)
+def moe_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter):
+    p = problem(num_tokens, hidden, num_topk, num_experts, 1)
+    v = lib().ep_moe_workspace_bytes(ctypes.byref(p), int(inter))
+    if v < 0:
+        raise ValueError("invalid problem sizes")
+    return int(v)
+
+
+def alloc_moe_workspace(num_tokens, num_topk, num_experts, hidden, inter, device="cuda"):
+    """The workspace of moe_layer calls of up to these sizes (one per stream)."""
+    import torch
+    return torch.empty((moe_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter),),
+                       dtype=torch.uint8, device=device)
+
+
+def moe_layer(x, topk_idx, topk_weights, w13, w2, out=None, workspace=None):
+    """The whole expert layer for a few tokens (at most 256), in two launches:
+    y[t] = sum_k topk_weights[t, k] * W2_e (silu(Wg_e x_t) * (Wu_e x_t)) with
+    e = topk_idx[t, k] (see ep_moe_layer).  ``x`` [N, H] bf16, ``w13``
+    [E, 2*I, H] (gate rows first) and ``w2`` [E, H, I], both bf16 tensors or
+    both QuantWeight of one format.  ``out`` [N, H] and ``workspace`` (from
+    alloc_moe_workspace) make the call allocation-free."""
+    import torch
+    N, H = x.shape
+    K = topk_idx.shape[1]
+    E, H2, I = w2.shape
+    _need(x, torch.bfloat16, (N, H), "x")
+    nb = _idx_bytes(topk_idx)
+    _need(topk_idx, topk_idx.dtype, (N, K), "topk_idx")
+    _need(topk_weights, torch.float32, (N, K), "topk_weights")
+    d13, d2 = _weight_desc(w13, (E, 2 * I, H), "w13"), _weight_desc(w2, (E, H, I), "w2")
+    need = moe_workspace_bytes(N, K, E, H, I)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    elif workspace.dtype != torch.uint8 or workspace.numel() < need \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace: need {need} contiguous uint8")
+    if out is None:
+        out = torch.empty((N, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, (N, H), "y")
+    _same_device(x, topk_idx=topk_idx, topk_weights=topk_weights, w13=w13, w2=w2, y=out,
+                 workspace=workspace)
+    p = Problem(N, H, K, E, 1, 1, 0, nb, 0)
+    a = MoeArgs(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), d13, d2,
+                out.data_ptr(), workspace.data_ptr(), I)
+    _check("ep_moe_layer", _on(x, lambda st: lib().ep_moe_layer(ctypes.byref(p), ctypes.byref(a),
+                                                                st)))
+    return out
+
+
+def moe_error(workspace):
+    """Synchronous: error flags (EP_LAYOUT_ERR_INDEX) of the last moe_layer that
+    used ``workspace``."""
+    v = ctypes.c_int32(0)
+    _check("ep_layout_error", _on(workspace, lambda st: lib().ep_layout_error(
+        _ptr(workspace), ctypes.byref(v), st)))
+    return int(v.value)
+
+
+def quant_linear(x, w, out=None):
+    """y [N, rows] bf16 = x [N, cols] bf16 times the transpose of the 4-bit
+    weight ``w`` (QuantWeight [rows, cols]), N <= 256 (see ep_quant_linear)."""
+    import torch
+    if not isinstance(w, QuantWeight) or len(w.shape) != 2:
+        raise ValueError("w: need a QuantWeight [rows, cols]")
+    rows, cols = w.shape
+    N = x.shape[0]
+    _need(x, torch.bfloat16, (N, cols), "x")
+    if out is None:
+        out = torch.empty((N, rows), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(out, torch.bfloat16, (N, rows), "y")
+    _same_device(x, w=w, y=out)
+    d = w.desc()
+    _check("ep_quant_linear", _on(x, lambda st: lib().ep_quant_linear(
+        N, cols, rows, x.data_ptr(), ctypes.byref(d), out.data_ptr(), st)))
+    return out
+
+
 # The other C entry points under their own names, for callers who read
 # include/ep_get.h: each is the function above that marshals that entry
 # point's arguments from tensors.
@@ -505,3 +746,7 @@ ep_combine = combine
 ep_layout_error = layout_error
 ep_ll_capacity = ll_capacity
 ep_ll_dispatch = ll_dispatch
+ep_route = route
+ep_moe_workspace_bytes = moe_workspace_bytes
+ep_moe_layer = moe_layer
+ep_quant_linear = quant_linear

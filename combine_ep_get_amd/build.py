@@ -7,10 +7,13 @@ packed-fp32 instruction selection is disabled for all device code.
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ep_get.hip")
+# the rest of libepget: the router, and the experts' products
+MORE_SRC = [os.path.join(HERE, "csrc", n) for n in ("ep_route.hip", "ep_moe.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libepget.so")
@@ -26,14 +29,29 @@ HIPFLAGS = [
 ]
 
 
-def build(verbose: bool = False, defines=(), out: str = LIB, src: str = SRC) -> str:
-    """Compile ``src`` into ``out``; ``defines`` are extra -D flags."""
-    os.makedirs(os.path.dirname(out), exist_ok=True)
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *HIPFLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, src, "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+
+
+def build(verbose: bool = False, defines=(), out: str = LIB, src: str = SRC) -> str:
+    """Compile ``src`` into ``out``; ``defines`` are extra -D flags.  The EP
+    library has several sources, compiled side by side and linked."""
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    tmp = out + ".tmp"
+    base = [HIPCC, *HIPFLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE]
+    if src != SRC:
+        _run([*base, src, "-o", tmp], verbose)
+    else:
+        objs = [(s, f"{out}.{os.path.basename(s)}.o") for s in (SRC, *MORE_SRC)]
+        with ThreadPoolExecutor(len(objs)) as pool:
+            list(pool.map(lambda so: _run([*[f for f in base if f != "-shared"], "-c", so[0],
+                                           "-o", so[1]], verbose), objs))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", *[o for _, o in objs], "-o", tmp],
+             verbose)
+        for _, o in objs:
+            os.remove(o)
     os.replace(tmp, out)
     return out
 

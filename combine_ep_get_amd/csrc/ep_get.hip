@@ -42,15 +42,7 @@
 // Build: hipcc --offload-arch=gfx950 -O3 -ffp-contract=off (products and sums
 // in combine are rounded separately, matching the contract bit for bit).
 
-#include <hip/hip_runtime.h>
-
-#include <atomic>
-#include <climits>
-#include <cstdio>
-#include <cstdlib>
-#include <cstring>
-
-#include "ep_get.h"
+#include "ep_host.h"
 
 // Cache policy of the streaming accesses (measured on MI355X): token rows
 // read by dispatch use ordinary loads, expert rows read by combine use
@@ -1451,37 +1443,6 @@ void launch_combine_persist_tok(int grid, size_t lds, hipStream_t st, const void
 }
 
 // ---------------------------------------------------------------- host side
-bool log_on() {
-  static int v = -1;
-  if (v < 0) {
-    const char* e = getenv("EP_GET_LOG");
-    v = (e && *e && *e != '0') ? 1 : 0;
-  }
-  return v == 1;
-}
-
-#define EP_LOG(...)                          \
-  do {                                       \
-    if (log_on()) {                          \
-      fprintf(stderr, "[ep_get] " __VA_ARGS__); \
-      fputc('\n', stderr);                   \
-    }                                        \
-  } while (0)
-
-int check_device() {
-  static std::atomic<int> cache[64];  // 0 unknown, 1 gfx950, 2 other
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return EP_ERR_HIP;
-  int c = (dev >= 0 && dev < 64) ? cache[dev].load() : 0;
-  if (c == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return EP_ERR_HIP;
-    c = (strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
-    if (dev >= 0 && dev < 64) cache[dev].store(c);
-  }
-  return c == 1 ? EP_OK : EP_ERR_UNSUPPORTED;
-}
-
 // LDS a persistent workgroup reserves: the whole per-workgroup maximum of
 // the current device (cached per device; 0 if it cannot be read).
 size_t persist_lds() {
@@ -1496,34 +1457,6 @@ size_t persist_lds() {
     if (dev >= 0 && dev < 64) cache[dev].store(v);
   }
   return (size_t)v;
-}
-
-int check_launch(const char* what) {
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) {
-    EP_LOG("%s: %s", what, hipGetErrorString(e));
-    return EP_ERR_HIP;
-  }
-  return EP_OK;
-}
-
-int64_t bound_of(const ep_problem_t* p) {
-  return (int64_t)p->num_tokens * p->num_topk + (int64_t)p->num_experts * (p->expert_alignment - 1);
-}
-
-int validate_layout(const ep_problem_t* p) {
-  if (!p) return EP_ERR_INVALID_ARG;
-  const int N = p->num_tokens, K = p->num_topk, E = p->num_experts, R = p->num_ranks,
-            A = p->expert_alignment;
-  if (N < 0 || K < 1 || K > EP_MAX_TOPK || E < 1 || E > EP_MAX_EXPERTS || R < 1 ||
-      R > EP_MAX_RANKS || R > E || A < 1)
-    return EP_ERR_INVALID_ARG;
-  if (E % R != 0 || N % R != 0) return EP_ERR_INVALID_ARG;
-  if (p->topk_idx_bytes != 0 && p->topk_idx_bytes != 4 && p->topk_idx_bytes != 8)
-    return EP_ERR_INVALID_ARG;
-  if (p->cu_budget < 0) return EP_ERR_INVALID_ARG;
-  if (bound_of(p) > INT32_MAX) return EP_ERR_INVALID_ARG;
-  return EP_OK;
 }
 
 int validate_payload(const ep_problem_t* p) {

@@ -303,6 +303,126 @@ typedef struct ep_ll_args {
 int ep_ll_dispatch_ex(const ep_problem_t* p, int32_t max_tokens_per_rank, const ep_ll_args_t* args,
                       void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around dispatch and combine: the router that decides the
+ * expert ids, and the experts' products for batches too small to be worth
+ * dispatching.  Same conventions as above: device pointers, caller-owned
+ * buffers, enqueue only, host-side checks. */
+
+/* Router: gate logits to expert ids and weights, the inputs of every call above.
+ *   s_e = sigmoid(logit_e) or softmax(logits)_e          (the score)
+ *   v_e = s_e + bias_e, or s_e without a bias            (decides, weighs nothing)
+ *   group score = sum of the group_top largest v of the group's E/num_groups
+ *   consecutive experts; the topk_groups best groups stay; of their experts
+ *   the num_topk largest v are chosen, in descending order.
+ *   weight_k = scale * s_k, divided by the sum of the chosen s if renormalize.
+ * Equal values go to the lowest expert (and group).  Scores are computed in 64
+ * bits, so that neighbours at the border are ordered as the formula orders
+ * them; without a bias the experts are ordered by their logits themselves.
+ * A logit of -inf or NaN masks its expert: it is never chosen, and a group with
+ * fewer than group_top unmasked experts comes after all others.  Where fewer
+ * than num_topk experts are left, the remaining entries are -1 with weight 0.
+ * +inf counts as the largest finite float.  Where the chosen scores sum to 0
+ * the weights are 0.
+ *   logits        [N][E] float32 (logits_bytes 4) or bf16 (2)
+ *   bias          [E] float32, finite, or NULL
+ *   num_groups    1..64, divides E; 1 <= topk_groups <= num_groups;
+ *                 group_top 1 or 2, at most E/num_groups;
+ *                 num_topk <= topk_groups * E/num_groups
+ *   topk_idx      [N][K] out, int32 (topk_idx_bytes 0 or 4) or int64 (8)
+ *   topk_weights  [N][K] float32 out */
+#define EP_MAX_GROUPS 64
+enum { EP_SCORE_SIGMOID = 0, EP_SCORE_SOFTMAX = 1 };
+typedef struct ep_route_args {
+  const void* logits;
+  const float* bias;
+  void* topk_idx;
+  float* topk_weights;
+  int32_t num_tokens;
+  int32_t num_experts;
+  int32_t num_topk;
+  int32_t num_groups;
+  int32_t topk_groups;
+  int32_t group_top;
+  int32_t scoring;
+  int32_t renormalize;
+  int32_t logits_bytes;
+  int32_t topk_idx_bytes;
+  float scale;
+} ep_route_args_t;
+int ep_route(const ep_route_args_t* args, void* stream);
+
+/* A weight matrix [rows][cols], or a stack of them [experts][rows][cols].
+ *   EP_WEIGHT_BF16   data bf16; cols % 8 == 0; scales, zeros and group ignored
+ *   EP_WEIGHT_INT4   data [rows][cols/2] bytes; value = scale * (code - zero).
+ *                    Nibble j (lowest first) of each little-endian 32-bit word
+ *                    holds column (0,2,4,6,1,3,5,7)[j] of its block of eight.
+ *                    scales [rows][cols/group] bf16; zeros [rows][cols/group]
+ *                    bytes or NULL (8); group 32, 64 or 128, cols % group == 0
+ *   EP_WEIGHT_MXFP4  OCP MXFP4: data [rows][cols/2] bytes of E2M1 codes, lower
+ *                    nibble first; scales [rows][cols/32] E8M0 bytes; group 32,
+ *                    cols % 32 == 0
+ * data is 16-byte aligned, bf16 scales 2-byte aligned. */
+enum { EP_WEIGHT_BF16 = 0, EP_WEIGHT_INT4 = 1, EP_WEIGHT_MXFP4 = 2 };
+typedef struct ep_weight {
+  const void* data;
+  const void* scales;
+  const uint8_t* zeros;
+  int32_t format;
+  int32_t group;
+} ep_weight_t;
+
+/* Most rows (tokens) of one ep_moe_layer or ep_quant_linear call, and the
+ * longest contraction (hidden, inter, cols): above that a batch is worth
+ * dispatching to a grouped GEMM. */
+#define EP_MAX_FEW_TOKENS 256
+#define EP_MAX_CONTRACTION 65536
+
+/* A whole expert layer for a few tokens, in two kernels and without dispatch
+ * and combine:
+ *   y[t] = sum over k with 0 <= topk_idx[t][k] < E of topk_weights[t][k] *
+ *          W2_e ( silu(Wg_e x[t]) * (Wu_e x[t]) ),  e = topk_idx[t][k]
+ * Only the experts that some token names are read, each once per 64 of its
+ * tokens.  Products accumulate in float32; weight * silu * up is rounded to bf16
+ * once, as the input of the second product, and y once.  A token without
+ * experts gets zeros; an expert named twice by one token counts with the sum
+ * of its weights.  Ids outside [-1, E) are skipped and flagged as by
+ * ep_get_layout (ep_layout_error on `workspace`).  Deterministic.
+ * x, weights and topk_weights are finite, |x| and the values before the second
+ * product below 2^119 with EP_WEIGHT_INT4.
+ *   p          num_tokens 0..EP_MAX_FEW_TOKENS, hidden, num_topk, num_experts,
+ *              topk_idx_bytes; num_ranks, expert_alignment, use_fp8 and
+ *              cu_budget are only checked
+ *   x          [N][hidden] bf16, 16-byte aligned
+ *   w13        [E][2*inter][hidden]: rows 0..inter-1 are Wg, the rest Wu
+ *   w2         [E][hidden][inter], in the same format and group as w13
+ *   inter      % 8 == 0 (bf16) or % group == 0; hidden and inter at most
+ *              EP_MAX_CONTRACTION
+ *   y          [N][hidden] bf16 out
+ *   workspace  ep_moe_workspace_bytes, 256-byte aligned; no initialisation;
+ *              calls that overlap need their own */
+typedef struct ep_moe_args {
+  const void* x;
+  const void* topk_idx;
+  const float* topk_weights;
+  ep_weight_t w13;
+  ep_weight_t w2;
+  void* y;
+  void* workspace;
+  int32_t inter;
+} ep_moe_args_t;
+int64_t ep_moe_workspace_bytes(const ep_problem_t* p, int32_t inter);
+int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* args, void* stream);
+
+/* y = x W^T for a few rows and a 4-bit weight (EP_WEIGHT_INT4, EP_WEIGHT_MXFP4):
+ *   x [num_rows][cols] bf16 (16-byte aligned), w [out_rows][cols],
+ *   y [num_rows][out_rows] bf16; num_rows 0..EP_MAX_FEW_TOKENS, cols at most
+ *   EP_MAX_CONTRACTION, out_rows 1..EP_MAX_HIDDEN.
+ * float32 accumulation, one rounding.  x finite, below 2^119 with
+ * EP_WEIGHT_INT4.  Deterministic. */
+int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void* x,
+                    const ep_weight_t* w, void* y, void* stream);
+
 /* SYNCHRONOUS debug query: waits for `stream`, then stores the error word of
  * the last ep_get_layout that used `workspace` into *flags (host pointer).
  * Bits: EP_LAYOUT_ERR_INDEX. */

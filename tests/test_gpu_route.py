@@ -1,0 +1,111 @@
+"""The router on the GPU against a plain implementation in Python floats: ids equal,
+weights within the roundings of a 64-bit computation stored as float32."""
+import math
+
+import pytest
+import torch
+
+import combine_ep_get_amd as ep
+from tests import product_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def check(logits, K, bias=None, **kw):
+    idx, w = ep.route(logits.cuda(), K, bias=None if bias is None else bias.cuda(), **kw)
+    kw.pop("idx_dtype", None)
+    want_idx, want_w = ref.route(logits, K, bias, **kw)
+    assert torch.equal(idx.cpu().long(), want_idx)
+    # one float32 rounding (2^-24) of a value computed in 64 bits
+    w, want = w.double().cpu(), want_w
+    assert ((w - want).abs() <= 1.001 * 2.0 ** -24 * want.abs() + 2.0 ** -149).all()
+    return idx, w
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,E,K,G,keep,top", [
+    (1, 256, 8, 8, 4, 2), (70, 256, 8, 1, 1, 1), (9, 1, 1, 1, 1, 1), (33, 64, 6, 8, 3, 1),
+    (5, 65, 7, 1, 1, 1), (6, 160, 6, 8, 3, 2), (4, 1024, 32, 64, 7, 2), (13, 100, 10, 4, 4, 1),
+    (3, 7, 7, 7, 7, 1), (8, 129, 32, 3, 1, 2)])
+def test_route(scoring, with_bias, dtype, N, E, K, G, keep, top):
+    gen = torch.Generator().manual_seed(N * E)
+    logits = (2 * torch.randn((N, E), generator=gen)).to(dtype)
+    bias = 0.2 * torch.randn((E,), generator=gen) if with_bias else None
+    check(logits, K, bias, scoring=scoring, num_groups=G, topk_groups=keep, group_top=top,
+          renormalize=N % 2 == 0, scale=2.5 if N % 3 else 1.0,
+          idx_dtype=torch.int64 if N % 2 else torch.int32)
+
+
+def test_ties_go_to_the_lowest():
+    logits = torch.zeros((3, 300))
+    logits[1] = torch.arange(300) % 3
+    logits[2, 5:] = -0.0
+    check(logits, 32)
+    check(logits, 9, num_groups=10, topk_groups=3, group_top=2)
+    check(logits, 4, bias=torch.zeros(300), scoring="softmax", num_groups=10, topk_groups=2)
+
+
+def test_neighbours_that_float32_cannot_tell_apart():
+    """Scores that differ by less than a float32 step are ordered as the formula says."""
+    gen = torch.Generator().manual_seed(1)
+    logits = 8 + 1e-4 * torch.randn((50, 64), generator=gen)
+    bias = 1e-3 * torch.randn((64,), generator=gen)
+    check(logits, 8, bias)
+    check(logits, 8, bias, num_groups=8, topk_groups=4, group_top=2)
+    check(20 + torch.randn((50, 64), generator=gen), 8)      # sigmoid is 1 in float32
+    check(logits, 8, num_groups=8, topk_groups=4, group_top=2, scoring="softmax")
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masked_and_extreme_logits(scoring, with_bias):
+    gen = torch.Generator().manual_seed(2)
+    inf, low = math.inf, torch.finfo(torch.float32).min
+    logits = torch.randn((9, 40), generator=gen)
+    logits[0] = -inf                              # no expert at all
+    logits[1] = float("nan")
+    logits[2, 3:] = -inf                          # fewer than K
+    logits[3, ::2] = float("nan")
+    logits[4] = low                               # the lowest number is a number
+    logits[5, 1:] = low
+    logits[6, 7] = inf
+    logits[6, 9] = inf
+    logits[7] = -600 + logits[7]                  # scores near the end of float64's range
+    logits[8, :39] = -inf
+    bias = 0.1 * torch.randn((40,), generator=gen) if with_bias else None
+    for kw in (dict(), dict(num_groups=4, topk_groups=2, group_top=1),
+               dict(num_groups=4, topk_groups=3, group_top=2), dict(renormalize=False)):
+        check(logits, 6, bias, scoring=scoring, **kw)
+
+
+def test_no_tokens_and_preallocated_outputs():
+    idx, w = ep.route(torch.empty((0, 16), device="cuda"), 4)
+    assert idx.shape == w.shape == (0, 4)
+    logits = torch.randn((5, 16), generator=torch.Generator().manual_seed(3)).cuda()
+    out = (torch.full((7, 4), 9, dtype=torch.int64, device="cuda"),
+           torch.full((7, 4), 9.0, device="cuda"))
+    got = ep.route(logits, 4, out=(out[0][1:6], out[1][1:6]))
+    a, b = ep.route(logits, 4)
+    assert torch.equal(got[0], a.long()) and torch.equal(got[1], b)
+    for t in out:
+        assert (t[0] == 9).all() and (t[6] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens(dtype):
+    gen = torch.Generator().manual_seed(4)
+    logits = (1.5 * torch.randn((2000, 256), generator=gen)).to(dtype)
+    bias = 0.1 * torch.randn((256,), generator=gen)
+    check(logits, 8, bias, num_groups=8, topk_groups=4, group_top=2, scale=2.5)
+    check(logits, 8, scoring="softmax", renormalize=False)
+
+
+def test_routes_feed_the_layout():
+    logits = torch.randn((64, 32), generator=torch.Generator().manual_seed(5)).cuda()
+    logits[3] = -math.inf                          # a token without experts: -1, no slots
+    idx, w = ep.route(logits, 4)
+    lay = ep.get_layout(idx, 32, 4, 8)
+    assert ep.layout_error(lay) == 0
+    assert (lay.slot_of[3] == -1).all() and int(lay.num_recv_per_expert.sum()) == 63 * 4
