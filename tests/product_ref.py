@@ -132,9 +132,14 @@ def route(logits, K, bias=None, scoring="sigmoid", num_groups=1, topk_groups=1, 
         can = [e for e in range(E) if live[e] and e // per in kept]
         best = sorted(can, key=lambda e: (-order[e], e))[:K]
         w = [s[e] for e in best]
-        if renormalize:
-            total = math.fsum(w)
-            w = [a / total if total > 0 else 0.0 for a in w]
+        if renormalize and best:
+            # quotients of scores from their logarithms: the scores themselves may underflow
+            if scoring == "softmax":
+                logs = [l[e] for e in best]
+            else:
+                logs = [min(l[e], 0.0) - math.log1p(math.exp(-abs(l[e]))) for e in best]
+            ratio = [math.exp(a - max(logs)) for a in logs]
+            w = [a / math.fsum(ratio) for a in ratio]
         ids.append(best + [-1] * (K - len(best)))
         weights.append([a * scale for a in w] + [0.0] * (K - len(best)))
     return torch.tensor(ids, dtype=torch.int64).view(-1, K), \
