@@ -30,6 +30,7 @@ is_token_in_rank, expert_alignment, num_experts.
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,6 +103,13 @@ class MoeArgs(ctypes.Structure):
                 ("inter", ctypes.c_int32)]
 
 
+# The same structs as bytes, for calls whose time is the host's: packing them is
+# several times quicker than filling a ctypes structure.
+_PROBLEM = struct.Struct("@9i").pack
+_ROUTE_ARGS = struct.Struct("@4P10if4x").pack
+_WEIGHT_DESC = struct.Struct("@3P2i").pack
+_MOE_ARGS = struct.Struct("@3P3P2i3P2i2Pi4x").pack
+
 EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX = 0, 1
 EP_WEIGHT_BF16, EP_WEIGHT_INT4, EP_WEIGHT_MXFP4 = 0, 1, 2
 EP_MAX_FEW_TOKENS = 256
@@ -164,13 +172,13 @@ def load(path):
     L.ep_ll_dispatch_ex.restype = ctypes.c_int
     L.ep_ll_dispatch_ex.argtypes = [P, ctypes.c_int32, ctypes.POINTER(LLArgs), vp]
     L.ep_route.restype = ctypes.c_int
-    L.ep_route.argtypes = [ctypes.POINTER(RouteArgs), vp]
+    L.ep_route.argtypes = [vp, vp]
     L.ep_moe_workspace_bytes.restype = i64
     L.ep_moe_workspace_bytes.argtypes = [P, ctypes.c_int32]
     L.ep_moe_layer.restype = ctypes.c_int
-    L.ep_moe_layer.argtypes = [P, ctypes.POINTER(MoeArgs), vp]
+    L.ep_moe_layer.argtypes = [vp, vp, vp]
     L.ep_quant_linear.restype = ctypes.c_int
-    L.ep_quant_linear.argtypes = [ctypes.c_int32] * 3 + [vp, ctypes.POINTER(WeightDesc), vp, vp]
+    L.ep_quant_linear.argtypes = [ctypes.c_int32] * 3 + [vp] * 4
     return L
 
 
@@ -541,19 +549,26 @@ def ep_ll_dispatch_ex(p, max_tokens_per_rank, args, stream=None):
 
 
 # ------------------------------------------------- router and experts' products
-def _on(t, call):
-    """call(stream) with t's device current; its current stream there."""
+def _call(fn, name, t, *args):
+    """fn(*args, stream) on t's device and its current stream there."""
     import torch
-    if t.device.index == torch.cuda.current_device():
-        return call(_stream())
-    with torch.cuda.device(t.device):
-        return call(_stream())
+    dev = t.get_device()
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != EP_OK:
+        raise EPError(name, rc)
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+def _arg(t, dtype, shape, name, ref):
+    """_need for arguments of small calls: the same check, the message made only
+    on failure; on ref's device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous() \
+            or t.get_device() != ref.get_device():
+        _need(t, dtype, shape, name)
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
 
 
 def route(logits, num_topk, bias=None, scoring="sigmoid", num_groups=1, topk_groups=1,
@@ -564,33 +579,34 @@ def route(logits, num_topk, bias=None, scoring="sigmoid", num_groups=1, topk_gro
     "sigmoid" or "softmax"; ``idx_dtype`` int32 (default) or int64; ``out`` a
     pair of preallocated outputs."""
     import torch
-    N, E = logits.shape
-    K = int(num_topk)
-    size = {torch.float32: 4, torch.bfloat16: 2}.get(logits.dtype)
-    if size is None:
+    N, E = shape = logits.shape
+    K = num_topk
+    size = 4 if logits.dtype is torch.float32 else 2
+    if size == 2 and logits.dtype is not torch.bfloat16:
         raise ValueError(f"logits: need float32 or bfloat16, got {logits.dtype}")
-    _need(logits, logits.dtype, (N, E), "logits")
+    _arg(logits, logits.dtype, shape, "logits", logits)
     if scoring not in ("sigmoid", "softmax"):
         raise ValueError(f"scoring: need 'sigmoid' or 'softmax', got {scoring!r}")
     if bias is not None:
-        _need(bias, torch.float32, (E,), "bias")
+        _arg(bias, torch.float32, (E,), "bias", logits)
     if K < 1:
         raise ValueError(f"num_topk: need at least 1, got {K}")
     if out is None:
-        idx = torch.empty((N, K), dtype=idx_dtype or torch.int32, device=logits.device)
-        w = torch.empty((N, K), dtype=torch.float32, device=logits.device)
+        idx = logits.new_empty((N, K), dtype=idx_dtype or torch.int32)
+        w = logits.new_empty((N, K), dtype=torch.float32)
+        nb = _idx_bytes(idx)
     else:
         idx, w = out
         if idx_dtype is not None and idx.dtype != idx_dtype:
             raise ValueError(f"topk_idx: need {idx_dtype}, got {idx.dtype}")
-        _need(idx, idx.dtype, (N, K), "topk_idx")
-        _need(w, torch.float32, (N, K), "topk_weights")
-    _same_device(logits, bias=bias, topk_idx=idx, topk_weights=w)
-    a = RouteArgs(logits.data_ptr(), None if bias is None else bias.data_ptr(), idx.data_ptr(),
-                  w.data_ptr(), N, E, K, num_groups, topk_groups, group_top,
-                  EP_SCORE_SOFTMAX if scoring == "softmax" else EP_SCORE_SIGMOID,
-                  int(bool(renormalize)), size, _idx_bytes(idx), scale)
-    _check("ep_route", _on(logits, lambda st: lib().ep_route(ctypes.byref(a), st)))
+        nb = _idx_bytes(idx)
+        _arg(idx, idx.dtype, (N, K), "topk_idx", logits)
+        _arg(w, torch.float32, (N, K), "topk_weights", logits)
+    a = _ROUTE_ARGS(logits.data_ptr(), 0 if bias is None else bias.data_ptr(), idx.data_ptr(),
+                    w.data_ptr(), N, E, K, num_groups, topk_groups, group_top,
+                    EP_SCORE_SOFTMAX if scoring == "softmax" else EP_SCORE_SIGMOID,
+                    1 if renormalize else 0, size, nb, scale)
+    _call(lib().ep_route, "ep_route", logits, a)
     return idx, w
 
 
@@ -614,20 +630,20 @@ class QuantWeight:
         if self.shape[-1] % group != 0:
             raise ValueError(f"cols {self.shape[-1]} is no multiple of the group {group}")
         per = (*codes.shape[:-1], self.shape[-1] // group)
-        _need(codes, torch.uint8, codes.shape, "codes")
-        _need(scales, torch.bfloat16 if fmt == "int4" else torch.uint8, per, "scales")
+        _arg(codes, torch.uint8, codes.shape, "codes", codes)
+        _arg(scales, torch.bfloat16 if fmt == "int4" else torch.uint8, per, "scales", codes)
         if zeros is not None:
             if fmt != "int4":
                 raise ValueError("zeros: only int4 has zero points")
-            _need(zeros, torch.uint8, per, "zeros")
-        _same_device(codes, scales=scales, zeros=zeros)
+            _arg(zeros, torch.uint8, per, "zeros", codes)
         self.codes, self.scales, self.zeros, self.group, self.fmt = codes, scales, zeros, group, fmt
         self.device = codes.device
+        # what the calls read; the tensors above keep the memory
+        self.desc = (codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(),
+                     EP_WEIGHT_INT4 if fmt == "int4" else EP_WEIGHT_MXFP4, group)
 
-    def desc(self):
-        return WeightDesc(self.codes.data_ptr(), self.scales.data_ptr(),
-                          None if self.zeros is None else self.zeros.data_ptr(),
-                          EP_WEIGHT_INT4 if self.fmt == "int4" else EP_WEIGHT_MXFP4, self.group)
+    def get_device(self):
+        return self.codes.get_device()
 
 
 def pack_codes(codes, fmt="int4"):
@@ -643,14 +659,16 @@ def pack_codes(codes, fmt="int4"):
     return (c[..., 0::2] | (c[..., 1::2] << 4)).reshape(*codes.shape[:-1], -1)
 
 
-def _weight_desc(w, shape, name):
+def _weight_desc(w, shape, name, ref):
     import torch
     if isinstance(w, QuantWeight):
         if w.shape != shape:
             raise ValueError(f"{name}: need {shape}, got {w.shape}")
-        return w.desc()
-    _need(w, torch.bfloat16, shape, name)
-    return WeightDesc(w.data_ptr(), None, None, EP_WEIGHT_BF16, 0)
+        if w.get_device() != ref.get_device():
+            raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
+        return w.desc
+    _arg(w, torch.bfloat16, shape, name, ref)
+    return w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0
 
 
 @functools.lru_cache(maxsize=256)
@@ -679,29 +697,27 @@ def moe_layer(x, topk_idx, topk_weights, w13, w2, out=None, workspace=None):
     import torch
     N, H = x.shape
     K = topk_idx.shape[1]
-    E, H2, I = w2.shape
-    _need(x, torch.bfloat16, (N, H), "x")
+    E, _, I = w2.shape
+    _arg(x, torch.bfloat16, (N, H), "x", x)
     nb = _idx_bytes(topk_idx)
-    _need(topk_idx, topk_idx.dtype, (N, K), "topk_idx")
-    _need(topk_weights, torch.float32, (N, K), "topk_weights")
-    d13, d2 = _weight_desc(w13, (E, 2 * I, H), "w13"), _weight_desc(w2, (E, H, I), "w2")
+    _arg(topk_idx, topk_idx.dtype, (N, K), "topk_idx", x)
+    _arg(topk_weights, torch.float32, (N, K), "topk_weights", x)
+    d13 = _weight_desc(w13, (E, 2 * I, H), "w13", x)
+    d2 = _weight_desc(w2, (E, H, I), "w2", x)
     need = moe_workspace_bytes(N, K, E, H, I)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
-    elif workspace.dtype != torch.uint8 or workspace.numel() < need \
-            or not workspace.is_contiguous():
-        raise ValueError(f"workspace: need {need} contiguous uint8")
-    if out is None:
-        out = torch.empty((N, H), dtype=torch.bfloat16, device=x.device)
+        workspace = x.new_empty((need,), dtype=torch.uint8)
+    elif workspace.numel() < need:
+        raise ValueError(f"workspace: need {need} bytes, got {workspace.numel()}")
     else:
-        _need(out, torch.bfloat16, (N, H), "y")
-    _same_device(x, topk_idx=topk_idx, topk_weights=topk_weights, w13=w13, w2=w2, y=out,
-                 workspace=workspace)
-    p = Problem(N, H, K, E, 1, 1, 0, nb, 0)
-    a = MoeArgs(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), d13, d2,
-                out.data_ptr(), workspace.data_ptr(), I)
-    _check("ep_moe_layer", _on(x, lambda st: lib().ep_moe_layer(ctypes.byref(p), ctypes.byref(a),
-                                                                st)))
+        _arg(workspace, torch.uint8, workspace.shape, "workspace", x)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _arg(out, torch.bfloat16, (N, H), "y", x)
+    _call(lib().ep_moe_layer, "ep_moe_layer", x, _PROBLEM(N, H, K, E, 1, 1, 0, nb, 0),
+          _MOE_ARGS(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), *d13, *d2,
+                    out.data_ptr(), workspace.data_ptr(), I))
     return out
 
 
@@ -709,8 +725,8 @@ def moe_error(workspace):
     """Synchronous: error flags (EP_LAYOUT_ERR_INDEX) of the last moe_layer that
     used ``workspace``."""
     v = ctypes.c_int32(0)
-    _check("ep_layout_error", _on(workspace, lambda st: lib().ep_layout_error(
-        _ptr(workspace), ctypes.byref(v), st)))
+    _call(lib().ep_layout_error, "ep_layout_error", workspace, workspace.data_ptr(),
+          ctypes.byref(v))
     return int(v.value)
 
 
@@ -722,15 +738,13 @@ def quant_linear(x, w, out=None):
         raise ValueError("w: need a QuantWeight [rows, cols]")
     rows, cols = w.shape
     N = x.shape[0]
-    _need(x, torch.bfloat16, (N, cols), "x")
+    _arg(x, torch.bfloat16, (N, cols), "x", w)
     if out is None:
-        out = torch.empty((N, rows), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((N, rows))
     else:
-        _need(out, torch.bfloat16, (N, rows), "y")
-    _same_device(x, w=w, y=out)
-    d = w.desc()
-    _check("ep_quant_linear", _on(x, lambda st: lib().ep_quant_linear(
-        N, cols, rows, x.data_ptr(), ctypes.byref(d), out.data_ptr(), st)))
+        _arg(out, torch.bfloat16, (N, rows), "y", w)
+    _call(lib().ep_quant_linear, "ep_quant_linear", x, N, cols, rows, x.data_ptr(),
+          _WEIGHT_DESC(*w.desc), out.data_ptr())
     return out
 
 

@@ -136,3 +136,23 @@ def test_pack_codes_layout():
     word = int.from_bytes(bytes(ep.pack_codes(codes)[0].tolist()), "little")
     assert [(word >> 4 * j) & 15 for j in range(8)] == [0, 2, 4, 6, 1, 3, 5, 7]
     assert ep.pack_codes(codes, "mxfp4")[0].tolist() == [0x10, 0x32, 0x54, 0x76]
+
+
+def test_packed_structs_are_the_structs():
+    """The binding packs the C structs into bytes: same sizes, same fields."""
+    a = ep.RouteArgs.from_buffer_copy(ep._ROUTE_ARGS(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14,
+                                                     0.5))
+    assert [getattr(a, f) for f, _ in a._fields_] == [*range(1, 15), 0.5]
+    d = ep.WeightDesc.from_buffer_copy(ep._WEIGHT_DESC(1, 2, 3, 4, 5))
+    assert [getattr(d, f) for f, _ in d._fields_] == [1, 2, 3, 4, 5]
+    m = ep.MoeArgs.from_buffer_copy(ep._MOE_ARGS(*range(1, 17)))
+    flat = [m.x, m.topk_idx, m.topk_weights]
+    flat += [getattr(w, f) for w in (m.w13, m.w2) for f, _ in w._fields_]
+    assert flat + [m.y, m.workspace, m.inter] == list(range(1, 17))
+    p = ep.Problem.from_buffer_copy(ep._PROBLEM(*range(1, 10)))
+    assert [getattr(p, f) for f, _ in p._fields_] == list(range(1, 10))
+    for packed, struct in ((ep._ROUTE_ARGS(*[0] * 14, 0.0), ep.RouteArgs),
+                           (ep._WEIGHT_DESC(*[0] * 5), ep.WeightDesc),
+                           (ep._MOE_ARGS(*[0] * 16), ep.MoeArgs),
+                           (ep._PROBLEM(*[0] * 9), ep.Problem)):
+        assert len(packed) == ctypes.sizeof(struct)
