@@ -3,41 +3,49 @@
 // rows with a 4-bit weight.
 //
 // All of it is one loop, `Stream`: 16-row tiles of a weight flow from HBM
-// through registers into v_mfma_f32_16x16x32_bf16, whose other operand is rows
-// of x.  The weights are the bytes that count (a decode batch has too few
-// tokens for the products to matter: 16 tokens are 16 flops per weight byte in
-// bf16, HBM's rate allows about 400), so every choice serves the stream:
-//   - a wavefront loads its tile straight into the operand layout (lane r + 16 g
-//     holds row r), with no LDS and no barrier on the way, several steps ahead;
+// into v_mfma_f32_16x16x32_bf16, whose other operand is rows of x.  The weights
+// are the bytes that count (a decode batch has too few tokens for the products to
+// matter: 16 tokens are 16 flops per weight byte in bf16, HBM's rate allows
+// about 400), so every choice serves the stream:
+//   - a load instruction reads whole 128-byte lines: 16 lanes 256 bytes of a bf16
+//     row, 8 lanes 128 bytes of a row of codes.  The MFMA wants lane r + 16 g
+//     to hold columns of row r; loading that directly touches 64 bytes of 16
+//     rows at a time, which reached 5.1 TB/s where whole lines reach 7.0 (493 MB,
+//     both as bare loads).  The loaded tile is turned through LDS, private to the
+//     wavefront, so there is no barrier;
+//   - loads run `depth` steps ahead in registers;
 //   - the wavefronts of a workgroup split the contraction and meet once, at the
-//     end, in LDS;
+//     end;
 //   - where an access falls outside (columns behind the end, rows behind the
 //     last, absent tokens) its buffer offset is out of range and the hardware
 //     returns zeros, so the loop has no branches.
 //
-// The contraction runs in steps of 128 columns, four MFMAs each.  Which eight
-// columns lane group g feeds to MFMA j is free as long as both operands agree;
-// it is chosen so that the weight's loads are as wide as its format allows
-// (`Fmt::col`).  A 4-bit weight is scaled per (row, group): lane r holds row r's
-// column of the 16x16 result, so one factor per lane does it, after the sum
-// over the group, in float32.  int4 codes become bf16 by putting the nibble
-// under the exponent of 128 (exact: 128 + code); the 128 and the zero point
-// leave again as (128 + zero) * sum(x), whose sum comes from an MFMA with ones.
-// E2M1 codes with their power-of-two scale are exact bf16 values already.
+// A step is 128 columns of bf16 or 256 of codes, four MFMAs per 128; MFMA j of a
+// half takes columns j*32 .. j*32+31, lane group g eight of them.  A 4-bit weight
+// is scaled per (row, group): lane r holds row r's column of the 16x16 result,
+// so one factor per lane does it, after the sum over the group, in float32.  int4
+// codes become bf16 by putting the nibble under the exponent of 128 (exact:
+// 128 + code); the 128 and the zero point leave again as (128 + zero) * sum(x),
+// whose sum comes from an MFMA with ones.  E2M1 codes with their power-of-two
+// scale are exact bf16 values already.
 //
 // Up to four tokens (`Quad`): rows t*4 + j of the MFMA's 16 hold the four
-// column pieces j of token t, so one load per step brings all of x and every
+// column pieces j of token t, so one load per half brings all of x and every
 // lane takes part; MFMA j's row t*4 + j is the product wanted, the other rows
 // are ignored.
+//
+// Weights are taken to be finite: a column or token that is not there is a zero
+// of x, and zero times an infinite weight would not be zero.
 #include "ep_host.h"
+
+#include <type_traits>
 
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format
 constexpr int kOutside = 0x7FFFFFFF;       // offset out of every buffer's range
@@ -46,49 +54,53 @@ constexpr int kNonTemporal = 2;            // NT in the cache-policy operand
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kBufferWord3);
+}
+
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-
-__device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // ---------------------------------------------------------------- formats
-// Weight format and group; Z: int4 with zero points.
 #ifndef EP_DQ
 #define EP_DQ 2
 #endif
 #ifndef EP_D1
 #define EP_D1 2
 #endif
+#ifndef EP_D2
+#define EP_D2 1
+#endif
 #ifndef EP_DB
 #define EP_DB 2
 #endif
-#ifndef EP_UPW
 #ifndef EP_W0
 #define EP_W0 3
 #endif
-#define EP_UPW(F, T) (T == 0 ? EP_W0 : 2)
+#ifndef EP_W1
+#define EP_W1 2
 #endif
-#ifndef EP_DNW
+#define EP_UPW(F, T) (T == 0 ? EP_W0 : T == 1 ? EP_W1 : 2)
 #define EP_DNW(F, T) 2
-#endif
 #ifndef EP_TWO
 #define EP_TWO 64
 #endif
 #ifndef EP_UT
 #define EP_UT 2
 #endif
-#ifndef EP_D2
-#define EP_D2 1
+#ifndef EP_URT
+#define EP_URT 2
 #endif
 #ifndef EP_DWAVES
 #define EP_DWAVES 8
 #endif
+// Weight format and group; Z: int4 with zero points.
 enum { kBf16, kMx, kInt128, kInt64, kInt32, kInt128Z, kInt64Z, kInt32Z };
 
 template <int F>
@@ -100,28 +112,20 @@ struct Fmt {
   static constexpr int halves = step / 128;          // of 128 columns, four MFMAs each
   static constexpr int chunks = quant ? 8 : 16;      // 16-byte chunks of a row per step
   static constexpr int loads = chunks / 4;           // 1 KiB loads per tile and step
-  // words of a row's codes that a lane feeds to MFMAs one after the other
-  static constexpr int words = integer ? group / 32 : 4;
-  static constexpr int groups = F == kMx ? 1 : quant ? 128 / group : 0;   // scales per half
-  // first of the eight columns (of a half) that lane group g feeds to MFMA j
-  static __device__ __forceinline__ int col(int g, int j) {
-    if constexpr (F == kMx || (integer && words == 4)) return g * 32 + j * 8;
-    else if constexpr (words == 2) return (j >> 1) * 64 + g * 16 + (j & 1) * 8;
-    else return j * 32 + g * 8;
-  }
+  static constexpr int groups = quant ? 128 / group : 1;    // scales per half
+  static constexpr int scales = quant ? step / group : 0;   // scales of a row per step
+  static constexpr int scale_bytes = F == kMx ? 1 : 2;
 };
 
-// ---------------------------------------------------------------- one weight tile
-// 16 rows of a weight as buffers; rows behind the last are out of range.
-struct Tile {
-  __amdgpu_buffer_rsrc_t data, scale, zero;
-};
-
-// Bytes of a row of codes (or bf16 values) and of its scales and zeros.
+// Bytes of a row of codes (or bf16 values), and its number of groups.
 template <int F>
 __device__ __forceinline__ int row_bytes(int cols) { return Fmt<F>::quant ? cols / 2 : cols * 2; }
 template <int F>
 __device__ __forceinline__ int row_groups(int cols) { return Fmt<F>::quant ? cols / Fmt<F>::group : 0; }
+template <int F>
+__device__ __forceinline__ int steps_of(int cols) {
+  return (cols + Fmt<F>::step - 1) / Fmt<F>::step;
+}
 
 struct Weight {           // kernel argument: ep_weight_t without what the kernel's type says
   const uint8_t* data;
@@ -129,51 +133,71 @@ struct Weight {           // kernel argument: ep_weight_t without what the kerne
   const uint8_t* zero;
 };
 
-template <int F>
-__device__ __forceinline__ Tile make_tile(const Weight& w, int64_t row, int rows, int cols) {
-  Tile t;
-  // in a scalar register: a buffer descriptor that is not costs every load a loop
-  const int n = uniform(max(0, min(16, rows)));
-  const int rb = row_bytes<F>(cols), rg = row_groups<F>(cols);
-  t.data = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w.data) + row * rb, 0, n * rb,
-                                             kBufferWord3);
-  if constexpr (Fmt<F>::quant) {
-    constexpr int size = F == kMx ? 1 : 2;
-    t.scale = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w.scale) + row * rg * size, 0,
-                                                n * rg * size, kBufferWord3);
-    if constexpr (Fmt<F>::zeros)
-      t.zero = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(w.zero) + row * rg, 0,
-                                                 n * rg, kBufferWord3);
+// ---------------------------------------------------------------- weight tiles
+// RT tiles of 16 rows: tile i starts at row `row` + i*16, or, where the tiles are
+// pairs of gate and up rows (`far` > 0), at row + (i/2)*16 + (i%2)*far.  `rows` is
+// how many rows there are from `row` on (for pairs: of each kind); those behind are
+// out of range.  The scales of all tiles share one buffer; what it returns for rows
+// that are not there only reaches results that nobody stores.
+template <int F, int RT>
+struct Tiles {
+  const uint8_t* data[RT];
+  const uint8_t *scale, *zero;
+  int bytes[RT], scale_end;
+  __device__ __forceinline__ void set(const Weight& w, int64_t row, int rows, int far, int cols) {
+    const int rb = row_bytes<F>(cols), rg = row_groups<F>(cols);
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+      const int at = far ? (i >> 1) * 16 : i * 16;
+      // in a scalar register: a descriptor that is not costs every load a loop
+      bytes[i] = uniform(max(0, min(16, rows - at))) * rb;
+      data[i] = w.data + (row + at + (far ? (i & 1) * far : 0)) * rb;
+    }
+    if constexpr (Fmt<F>::quant) {
+      const int span = uniform(far ? far + min(rows, RT * 8) : min(rows, RT * 16));
+      scale_end = span * rg;
+      scale = w.scale + row * rg * Fmt<F>::scale_bytes;
+      if constexpr (Fmt<F>::zeros) zero = w.zero + row * rg;
+    }
   }
-  return t;
-}
+};
 
 // ---------------------------------------------------------------- the stream
-// RT weight tiles times T token tiles of 16 (T == 0: Quad, up to 4 tokens).
+// RT weight tiles times T token tiles of 16 (T == 0: Quad, up to 4 tokens); PART: the
+// last step has fewer columns.
 //
-// Where the steps come from is the caller's cursor: `step` (which 128
-// columns), `live` (false: load nothing, which adds zeros), `tile[RT]`, `xoff[TT]`
-// (the lane's rows of x as byte offsets, kAbsent for none) and advance().
-template <int F, int RT, int T>
+// Where the steps come from is the caller's cursor: `step` (which columns),
+// `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT]` (the row of
+// x of token(k) in bytes, kAbsent for none) and advance().
+template <int F, int RT, int T, bool PART>
 struct Stream {
+  using M = Fmt<F>;
   static constexpr bool quad = T == 0;
   static constexpr int TT = quad ? 1 : T;
   static constexpr int tokens = quad ? 4 : 16 * TT;
+  static constexpr int values_per_row = RT * M::scales;           // scales of a step, all tiles
+  static constexpr int scale_loads = (values_per_row + 3) / 4;    // a value per lane group
   // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's
   // latency, as far as the registers go.
-  static constexpr int depth = Fmt<F>::quant ? (quad ? EP_DQ : TT <= 1 ? EP_D1 : EP_D2) : (quad ? EP_DB : 2);
+  static constexpr int depth = M::quant ? (quad ? EP_DQ : TT <= 1 ? EP_D1 : EP_D2)
+                                        : (quad ? EP_DB : 2);
+  // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros
+  static constexpr int tile_words = 16 * M::chunks;
+  static constexpr int buffer_words =
+      RT * tile_words + values_per_row * 4 * (M::zeros ? 2 : 1);
 
   struct Slot {
-    u32x4 w[RT][Fmt<F>::loads];                      // as loaded: see load()
-    uint32_t s[RT][Fmt<F>::halves][Fmt<F>::groups ? Fmt<F>::groups : 1];
-    uint32_t z[RT][Fmt<F>::halves][Fmt<F>::groups ? Fmt<F>::groups : 1];
-    u32x4 x[TT][Fmt<F>::halves][quad ? 1 : 4];
+    u32x4 w[RT][M::loads];                           // as loaded: see load()
+    uint32_t s[M::quant ? scale_loads : 1], z[M::zeros ? scale_loads : 1];
+    u32x4 x[TT][M::halves][quad ? 1 : 4];            // MFMA operands (Quad: one for all four)
   };
 
   // acc[i][j]: Quad: MFMA j's own rows (bf16, mxfp4), or [i][0] the whole sum
   // (int4); otherwise token tile j.  In the MFMA's result layout: lane r + 16 g
   // holds weight row r of tokens g*4 .. g*4+3.
   f32x4 acc[RT][quad ? 4 : TT];
+  // The lane's offsets: loads of the tiles, of the scales (in values), of x.
+  int woff[M::loads], soff[M::quant ? scale_loads : 1], xcol;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -182,184 +206,184 @@ struct Stream {
       for (int j = 0; j < (quad ? 4 : TT); j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // A step's loads.  One load instruction reads whole 128-byte lines: 16 lanes a
-  // row's 256 bytes (bf16 weights and x: four rows per load), 8 lanes 128 bytes
-  // (codes: eight rows).  xoff[k][j]: row j*4 + lane/16 of token tile k (Quad:
-  // the row that token() names), in bytes.
-  template <typename Cursor>
-  __device__ __forceinline__ void load(Slot& b, const Cursor& at, int cols,
-                                       __amdgpu_buffer_rsrc_t xr) {
-    using M = Fmt<F>;
+  // far: as in Tiles::set
+  __device__ __forceinline__ void init(int cols, int far) {
+    clear();
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int step = uniform(at.live ? at.step : 0);
-    const int c0 = step * M::step;
-    const int left = at.live ? cols - c0 : 0;              // columns left from here
-    const int rb = row_bytes<F>(cols);
-    {
-      const int chunk = lane & (M::chunks - 1), row = lane / M::chunks;
-      const bool in = chunk * (M::quant ? 32 : 8) < left;
+    const int rb = row_bytes<F>(cols), rg = row_groups<F>(cols);
 #pragma unroll
-      for (int q = 0; q < M::loads; q++) {
-        const int off = in ? (q * (64 / M::chunks) + row) * rb + chunk * 16 : kOutside;
+    for (int q = 0; q < M::loads; q++)
+      woff[q] = (q * (64 / M::chunks) + lane / M::chunks) * rb + (lane & (M::chunks - 1)) * 16;
+    if constexpr (M::quant) {
 #pragma unroll
-        for (int i = 0; i < RT; i++)
-          b.w[i][q] = __builtin_amdgcn_raw_buffer_load_b128(at.tile[i].data, off,
-                                                            step * (M::chunks * 16), kNonTemporal);
+      for (int q = 0; q < scale_loads; q++) {        // lane group g has value q*4 + g of its row
+        const int v = q * 4 + g, i = v / M::scales;
+        const int row = r + (far ? (i >> 1) * 16 + (i & 1) * far : i * 16);
+        soff[q] = v < values_per_row ? row * rg + v % M::scales : kOutside / 2;
       }
     }
-    if constexpr (M::quant) {
-      const int rg = row_groups<F>(cols);
-#pragma unroll
-      for (int m = 0; m < M::halves; m++)
-#pragma unroll
-        for (int q = 0; q < M::groups; q++) {
-          const int c = m * 128 + (F == kMx ? g * 32 : q * M::group);
-          const int n = r * rg + (c0 + c) / M::group;
-#pragma unroll
-          for (int i = 0; i < RT; i++) {
-            if constexpr (F == kMx)
-              b.s[i][m][q] = __builtin_amdgcn_raw_buffer_load_b8(at.tile[i].scale,
-                                                                 c < left ? n : kOutside, 0, 0);
-            else
-              b.s[i][m][q] = __builtin_amdgcn_raw_buffer_load_b16(at.tile[i].scale,
-                                                                  c < left ? n * 2 : kOutside, 0, 0);
-            if constexpr (M::zeros)
-              b.z[i][m][q] = __builtin_amdgcn_raw_buffer_load_b8(at.tile[i].zero,
-                                                                 c < left ? n : kOutside, 0, 0);
-          }
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < M::halves; m++) {
-      const int c = m * 128 + (quad ? M::col(g, lane & 3) : r * 8);
-#pragma unroll
-      for (int k = 0; k < TT; k++)
-#pragma unroll
-        for (int j = 0; j < (quad ? 1 : 4); j++)
-          b.x[k][m][j] = __builtin_amdgcn_raw_buffer_load_b128(
-              xr, c < left ? at.xoff[k][j] + c * 2 : kOutside, c0 * 2, 0);
-    }
+    xcol = g * 8 + (quad ? (lane & 3) * 32 : 0);
   }
 
-  // From loaded rows to MFMA operands, through 4 KiB of LDS that are the
-  // wavefront's own (its LDS accesses execute in order, so the fences only bind
-  // the compiler).  Chunk c of row r lies at slot c ^ r of its row: the 8 lanes
-  // of an access phase fall on different banks when they write (one row, 8
-  // chunks) and when they read (8 rows, one chunk).
+  // A step's loads.
+  template <typename Cursor>
+  __device__ __forceinline__ void load(Slot& b, const Cursor& at, int cols, const void* x,
+                                       int xbytes) {
+    const int step = uniform(at.live ? at.step : 0);
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+      const auto rs = buffer(at.tiles.data[i], at.live ? at.tiles.bytes[i] : 0);
+#pragma unroll
+      for (int q = 0; q < M::loads; q++)
+        b.w[i][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, woff[q], step * (M::chunks * 16),
+                                                          kNonTemporal);
+    }
+    if constexpr (M::quant) {
+      const int n = at.live ? at.tiles.scale_end : 0;
+      const auto ss = buffer(at.tiles.scale, n * M::scale_bytes);
+#pragma unroll
+      for (int q = 0; q < scale_loads; q++) {
+        if constexpr (M::scale_bytes == 1)
+          b.s[q] = __builtin_amdgcn_raw_buffer_load_b8(ss, soff[q], step * M::scales, 0);
+        else
+          b.s[q] = __builtin_amdgcn_raw_buffer_load_b16(ss, soff[q] * 2, step * (M::scales * 2), 0);
+      }
+      if constexpr (M::zeros) {
+        const auto zs = buffer(at.tiles.zero, n);
+#pragma unroll
+        for (int q = 0; q < scale_loads; q++)
+          b.z[q] = __builtin_amdgcn_raw_buffer_load_b8(zs, soff[q], step * M::scales, 0);
+      }
+    }
+    const auto xr = buffer(x, at.live ? xbytes : 0);
+    const int left = cols - step * M::step;          // columns left from here
+#pragma unroll
+    for (int m = 0; m < M::halves; m++)
+#pragma unroll
+      for (int j = 0; j < (quad ? 1 : 4); j++) {
+        const int c = m * 128 + j * 32;
+        const bool in = !PART || c + xcol < left;
+#pragma unroll
+        for (int k = 0; k < TT; k++)
+          b.x[k][m][j] = __builtin_amdgcn_raw_buffer_load_b128(
+              xr, in ? at.xoff[k] + (xcol + c) * 2 : kOutside, step * (M::step * 2), 0);
+      }
+  }
+
+  // The wavefront's LDS accesses execute in order; the fences bind the compiler.
   static __device__ __forceinline__ void fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  template <int CHUNKS>
-  static __device__ __forceinline__ int place(int row, int chunk) {
-    return row * CHUNKS + (chunk ^ (row & (CHUNKS - 1)));
+
+  // Where chunk c of row r lies in its tile: permuted so that the lanes that access
+  // LDS together, writing (a row's chunks) or reading (16 rows, one chunk of 16
+  // bytes or four of its words), fall on different banks.
+  static __device__ __forceinline__ int place(int r, int c) {
+    return r * M::chunks + (c ^ (M::quant ? (r >> 1) & 7 : r));
   }
-  template <int CHUNKS>
-  static __device__ __forceinline__ void put(u32x4* buf, const u32x4* v) {
-    const int lane = threadIdx.x & 63;
+
+  // Write the step's tiles and scales to LDS.
+  __device__ __forceinline__ void put(const Slot& b, u32x4* buf) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     fence();
 #pragma unroll
-    for (int q = 0; q < CHUNKS / 4; q++)
-      buf[place<CHUNKS>(q * (64 / CHUNKS) + lane / CHUNKS, lane & (CHUNKS - 1))] = v[q];
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+      for (int q = 0; q < M::loads; q++)
+        buf[i * tile_words +
+            place(q * (64 / M::chunks) + lane / M::chunks, lane & (M::chunks - 1))] = b.w[i][q];
+    if constexpr (M::quant) {
+      uint32_t* sb = reinterpret_cast<uint32_t*>(buf + RT * tile_words);
+      float* zb = reinterpret_cast<float*>(sb + values_per_row * 16);
+#pragma unroll
+      for (int q = 0; q < scale_loads; q++) {
+        const int v = q * 4 + g;
+        if (values_per_row % 4 == 0 || v < values_per_row) {
+          sb[r * values_per_row + v] = M::integer ? b.s[q] << 16 : b.s[q] << 23;
+          if constexpr (M::zeros) zb[r * values_per_row + v] = 128.f + (float)b.z[q];
+        }
+      }
+    }
     fence();
   }
 
-  // The four operands of x for a half that lies in buf.
-  static __device__ __forceinline__ void take_x(const u32x4* buf, u32x4* o) {
-    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  // The row's scales (or zeros: 128 + zero) of the step, by tile and group.
+  static __device__ __forceinline__ void take_scales(const u32x4* at, float* v) {
+    const int r = threadIdx.x & 15;
+    if constexpr (values_per_row % 4 == 0) {
+      const f32x4* from = reinterpret_cast<const f32x4*>(at) + r * (values_per_row / 4);
 #pragma unroll
-    for (int j = 0; j < 4; j++) o[j] = buf[place<16>(r, Fmt<F>::col(g, j) / 8)];
-  }
-
-  // Half m of a weight tile that lies in buf: bf16 the four operands, else the
-  // four words of codes.
-  static __device__ __forceinline__ void take_w(const u32x4* buf, int m, u32x4* o) {
-    using M = Fmt<F>;
-    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    if constexpr (!M::quant) {
+      for (int q = 0; q < values_per_row / 4; q++) {
+        const f32x4 t = from[q];
 #pragma unroll
-      for (int j = 0; j < 4; j++) o[j] = buf[place<16>(r, j * 4 + g)];
-    } else if constexpr (M::words == 4) {
-      o[0] = buf[place<8>(r, m * 4 + g)];
-    } else if constexpr (M::words == 2) {
-#pragma unroll
-      for (int q = 0; q < 2; q++) {
-        const u32x2 v = reinterpret_cast<const u32x2*>(
-            buf + place<8>(r, m * 4 + q * 2 + (g >> 1)))[g & 1];
-        o[0][q * 2] = v.x, o[0][q * 2 + 1] = v.y;
+        for (int e = 0; e < 4; e++) v[q * 4 + e] = t[e];
       }
     } else {
+      const f32x2* from = reinterpret_cast<const f32x2*>(at) + r * (values_per_row / 2);
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        o[0][q] = reinterpret_cast<const uint32_t*>(buf + place<8>(r, m * 4 + q))[g];
+      for (int q = 0; q < values_per_row / 2; q++) {
+        const f32x2 t = from[q];
+        v[q * 2] = t[0], v[q * 2 + 1] = t[1];
+      }
     }
   }
 
   // The eight bf16 weights of a word of codes (int4: 128 + code; mxfp4: scaled).
-  static __device__ __forceinline__ u32x4 operand(uint32_t w, uint32_t scale) {
+  static __device__ __forceinline__ u32x4 operand(uint32_t w, float scale) {
     u32x4 o;
-    if constexpr (Fmt<F>::integer) {
+    if constexpr (M::integer) {
 #pragma unroll
       for (int q = 0; q < 4; q++) o[q] = ((w >> (4 * q)) & 0x000F000Fu) | 0x43004300u;
     } else {
-      const float s = __uint_as_float(scale << 23);
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
     }
     return o;
   }
 
   // The products of a step.
   __device__ __forceinline__ void compute(const Slot& b, u32x4* buf) {
-    using M = Fmt<F>;
+    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     const f32x4 none{0.f, 0.f, 0.f, 0.f};
     constexpr uint32_t kOnes = 0x3F803F80u;
     const u32x4 ones{kOnes, kOnes, kOnes, kOnes};
-    constexpr int per = M::integer ? 4 / M::groups : 4;      // MFMAs per group
-    u32x4 w[RT][M::halves];                      // codes
-    if constexpr (M::quant) {
-#pragma unroll
-      for (int i = 0; i < RT; i++) {
-        put<M::chunks>(buf, b.w[i]);
-#pragma unroll
-        for (int m = 0; m < M::halves; m++) take_w(buf, m, &w[i][m]);
+    constexpr int per = 4 / M::groups;               // MFMAs per group
+    put(b, buf);
+    float sv[M::quant ? values_per_row : 1], zv[M::zeros ? values_per_row : 1];
+    if constexpr (M::quant) take_scales(buf + RT * tile_words, sv);
+    if constexpr (M::zeros) take_scales(buf + RT * tile_words + values_per_row * 4, zv);
+    const auto weight = [&](int i, int m, int j) {   // operand of MFMA j
+      if constexpr (!M::quant) {
+        return buf[i * tile_words + place(r, j * 4 + g)];
+      } else {
+        const uint32_t w =
+            reinterpret_cast<const uint32_t*>(buf + i * tile_words + place(r, m * 4 + j))[g];
+        return operand(w, M::integer ? 0.f : sv[i * M::scales + m * 4 + j]);
       }
-    }
+    };
+    const auto x = [&](int k, int m, int j) { return b.x[k][m][quad ? 0 : j]; };
+    const auto zero = [&](int i, int m, int q) {     // off the codes as the operand has them
+      return M::zeros ? zv[i * M::scales + m * M::groups + q] : 136.f;
+    };
 #pragma unroll
     for (int m = 0; m < M::halves; m++) {
-      u32x4 x[TT][4];
-#pragma unroll
-      for (int k = 0; k < TT; k++) {
-        if constexpr (quad) {
-          x[k][0] = x[k][1] = x[k][2] = x[k][3] = b.x[k][m][0];
-        } else {
-          put<16>(buf, b.x[k][m]);
-          take_x(buf, x[k]);
-        }
-      }
       if constexpr (!M::integer) {
 #pragma unroll
-        for (int i = 0; i < RT; i++) {
-          u32x4 o[4];
-          if constexpr (M::quant) {
+        for (int i = 0; i < RT; i++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) o[j] = operand(w[i][m][j], b.s[i][m][0]);
-          } else {
-            put<M::chunks>(buf, b.w[i]);
-            take_w(buf, 0, o);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; j++)
+          for (int j = 0; j < 4; j++) {
+            const u32x4 o = weight(i, m, j);
 #pragma unroll
             for (int k = 0; k < TT; k++) {
               f32x4& c = acc[i][quad ? j : k];
-              c = mfma(x[k][j], o[j], c);
+              c = mfma(x(k, m, j), o, c);
             }
-        }
+          }
       } else if constexpr (quad) {
-        const f32x4 sx = mfma(x[0][0], ones, none);      // register j: sum of piece j
+        const f32x4 sx = mfma(x(0, m, 0), ones, none);   // register j: sum of piece j
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
@@ -367,62 +391,55 @@ struct Stream {
             float sum = 0.f, xs = 0.f;
 #pragma unroll
             for (int j = q * per; j < (q + 1) * per; j++) {
-              const f32x4 d = mfma(x[0][0], operand(w[i][m][j], 0), none);
+              const f32x4 d = mfma(x(0, m, j), weight(i, m, j), none);
               sum += d[j];
               xs += sx[j];
             }
-            acc[i][0][0] = fmaf(bf16_value(b.s[i][m][q]), fmaf(-zero_of(b, i, m, q), xs, sum),
-                                acc[i][0][0]);
+            acc[i][0][0] = fmaf(sv[i * M::scales + m * M::groups + q],
+                                fmaf(-zero(i, m, q), xs, sum), acc[i][0][0]);
           }
       } else {
 #pragma unroll
         for (int q = 0; q < M::groups; q++) {
-          f32x4 xs[TT], d[RT][TT];
+          f32x4 xs[TT];
 #pragma unroll
           for (int k = 0; k < TT; k++) {
             xs[k] = none;
 #pragma unroll
-            for (int i = 0; i < RT; i++) d[i][k] = none;
-          }
-#pragma unroll
-          for (int j = q * per; j < (q + 1) * per; j++) {
-#pragma unroll
-            for (int k = 0; k < TT; k++) xs[k] = mfma(x[k][j], ones, xs[k]);
-#pragma unroll
-            for (int i = 0; i < RT; i++) {
-              const u32x4 o = operand(w[i][m][j], 0);
-#pragma unroll
-              for (int k = 0; k < TT; k++) d[i][k] = mfma(x[k][j], o, d[i][k]);
-            }
+            for (int j = q * per; j < (q + 1) * per; j++) xs[k] = mfma(x(k, m, j), ones, xs[k]);
           }
 #pragma unroll
           for (int i = 0; i < RT; i++) {
-            const float s = bf16_value(b.s[i][m][q]), z = zero_of(b, i, m, q);
+            f32x4 d[TT];
+#pragma unroll
+            for (int k = 0; k < TT; k++) d[k] = none;
+#pragma unroll
+            for (int j = q * per; j < (q + 1) * per; j++) {
+              const u32x4 o = weight(i, m, j);
+#pragma unroll
+              for (int k = 0; k < TT; k++) d[k] = mfma(x(k, m, j), o, d[k]);
+            }
+            const float s = sv[i * M::scales + m * M::groups + q], z = zero(i, m, q);
 #pragma unroll
             for (int k = 0; k < TT; k++)
 #pragma unroll
               for (int e = 0; e < 4; e++)
-                acc[i][k][e] = fmaf(s, fmaf(-z, xs[k][e], d[i][k][e]), acc[i][k][e]);
+                acc[i][k][e] = fmaf(s, fmaf(-z, xs[k][e], d[k][e]), acc[i][k][e]);
           }
         }
       }
     }
   }
 
-  // What is taken off the codes as the operand holds them (128 + code).
-  static __device__ __forceinline__ float zero_of(const Slot& b, int i, int m, int q) {
-    return Fmt<F>::zeros ? 128.f + (float)b.z[i][m][q] : 136.f;
-  }
-
   // Add `count` steps of the cursor to acc; after(i) follows step i's products.
   template <typename Cursor, typename After>
-  __device__ __forceinline__ void run(int count, Cursor& at, int cols, __amdgpu_buffer_rsrc_t xr,
+  __device__ __forceinline__ void run(int count, Cursor& at, int cols, const void* x, int xbytes,
                                       u32x4* buf, After&& after) {
     Slot slot[depth];
 #pragma unroll
     for (int d = 0; d < depth; d++) {
       at.live = d < count;
-      load(slot[d], at, cols, xr);
+      load(slot[d], at, cols, x, xbytes);
       at.advance();
     }
     for (int i = 0; i < count; i += depth) {
@@ -430,18 +447,17 @@ struct Stream {
       for (int d = 0; d < depth; d++) {
         compute(slot[d], buf);
         at.live = i + d + depth < count;
-        load(slot[d], at, cols, xr);
+        load(slot[d], at, cols, x, xbytes);
         at.advance();
         after(i + d);
       }
     }
   }
 
-  // Which token row the lane's load j of x is for in token tile k.
-  static constexpr int rows = quad ? 1 : 4;            // such loads per half
-  static __device__ __forceinline__ int token(int k, int j) {
+  // The token row that the lane loads of x in token tile k.
+  static __device__ __forceinline__ int token(int k) {
     const int lane = threadIdx.x & 63;
-    return quad ? (lane & 15) >> 2 : k * 16 + j * 4 + (lane >> 4);
+    return quad ? (lane & 15) >> 2 : k * 16 + (lane & 15);
   }
 
   // f(token, value) for every token row this lane holds of weight tile i (its
@@ -450,7 +466,7 @@ struct Stream {
   __device__ __forceinline__ void values(int i, Fn&& f) const {
     const int g = (threadIdx.x & 63) >> 4;
     if constexpr (quad) {
-      if constexpr (Fmt<F>::integer) f(g, acc[i][0][0]);
+      if constexpr (M::integer) f(g, acc[i][0][0]);
       else f(g, acc[i][0][0] + acc[i][1][1] + acc[i][2][2] + acc[i][3][3]);
     } else {
 #pragma unroll
@@ -461,22 +477,15 @@ struct Stream {
   }
 };
 
-constexpr int kBuffer = 256;               // 16-byte words of LDS per wavefront (Stream::put)
-
 // The cursor over every by-th step of the same tiles and rows.
-template <int RT, typename S>
+template <int F, int RT, int TT>
 struct Strided {
-  Tile tile[RT];
-  int xoff[S::TT][S::rows];
+  Tiles<F, RT> tiles;
+  int xoff[TT];
   int step, by;
   bool live;
   __device__ __forceinline__ void advance() { step += by; }
 };
-
-template <int F>
-__device__ __forceinline__ int steps_of(int cols) {
-  return (cols + Fmt<F>::step - 1) / Fmt<F>::step;
-}
 
 // How many of `steps` a wave takes that starts at `first` and goes on by `by`.
 __device__ __forceinline__ int share_of(int steps, int first, int by) {
@@ -488,33 +497,25 @@ constexpr int kLinWaves = 8;
 
 // One workgroup: RT*16 rows of the weight, all columns split over the waves, 16 T
 // rows of x (blockIdx.y).
-template <int F, int RT, int T>
+template <int F, int RT, int T, bool PART>
 __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
     const uint16_t* __restrict__ x, Weight w, uint16_t* __restrict__ y, int n, int cols, int rows) {
-  using S = Stream<F, RT, T>;
+  using S = Stream<F, RT, T, PART>;
   __shared__ float red[kLinWaves][RT][S::tokens][16];
-  __shared__ u32x4 buf[kLinWaves][kBuffer];
+  __shared__ u32x4 buf[kLinWaves][S::buffer_words];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int row0 = blockIdx.x * (RT * 16), t0 = blockIdx.y * S::tokens;
   const int nt = min(n - t0, S::tokens);
-  Strided<RT, S> at;
+  Strided<F, RT, S::TT> at;
+  at.tiles.set(w, row0, rows - row0, 0, cols);
 #pragma unroll
-  for (int i = 0; i < RT; i++)
-    at.tile[i] = make_tile<F>(w, min(row0 + i * 16, rows), rows - row0 - i * 16, cols);
-  const auto xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x) + (int64_t)t0 * cols,
-                                                    0, nt * cols * 2, kBufferWord3);
-#pragma unroll
-  for (int k = 0; k < S::TT; k++)
-#pragma unroll
-    for (int q = 0; q < S::rows; q++) {
-      const int t = S::token(k, q);
-      at.xoff[k][q] = t < nt ? t * cols * 2 : kAbsent;
-    }
+  for (int k = 0; k < S::TT; k++) at.xoff[k] = S::token(k) < nt ? S::token(k) * cols * 2 : kAbsent;
   at.step = wave;
   at.by = kLinWaves;
   S st;
-  st.clear();
-  st.run(share_of(steps_of<F>(cols), wave, kLinWaves), at, cols, xr, buf[wave], [](int) {});
+  st.init(cols, 0);
+  st.run(share_of(steps_of<F>(cols), wave, kLinWaves), at, cols, x + (int64_t)t0 * cols,
+         nt * cols * 2, buf[wave], [](int) {});
 #pragma unroll
   for (int i = 0; i < RT; i++)
     st.values(i, [&](int t, float v) { red[wave][i][t][lane & 15] = v; });
@@ -685,43 +686,40 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, Routing& r, int16_t
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// Entries pos0 .. of the expert's list through 16 gate and 16 up rows.
-template <int F, int T>
-__device__ __forceinline__ void up_tokens(const MoeArgs& a, const Routing& r,
-                                          float (*red)[16], u32x4 (*buf)[kBuffer],
-                                          const Tile* tile, int i0, int pos0, int n) {
-  using S = Stream<F, 2, T>;
+// Entries pos0 .. of the expert's list through RT/2 pairs of 16 gate and 16 up rows.
+// red[(wave * RT + tile) * tokens + token][row]
+template <int F, int RT, int T, bool PART>
+__device__ __forceinline__ void up_tokens(const MoeArgs& a, const Routing& r, float (*red)[16],
+                                          u32x4* buf, const Tiles<F, RT>& tiles, int i0, int pos0,
+                                          int n) {
+  using S = Stream<F, RT, T, PART>;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = min(n - pos0, S::tokens);
-  const auto xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.x), 0,
-                                                    a.N * a.H * 2, kBufferWord3);
-  Strided<2, S> at;
-  at.tile[0] = tile[0], at.tile[1] = tile[1];
+  Strided<F, RT, S::TT> at;
+  at.tiles = tiles;
 #pragma unroll
-  for (int k = 0; k < S::TT; k++)
-#pragma unroll
-    for (int q = 0; q < S::rows; q++) {
-      const int t = S::token(k, q), pair = t < nt ? r.pair[pos0 + t] : -1;
-      at.xoff[k][q] = pair >= 0 ? (pair >> kPairShift) * a.H * 2 : kAbsent;
-    }
+  for (int k = 0; k < S::TT; k++) {
+    const int t = S::token(k), pair = t < nt ? r.pair[pos0 + t] : -1;
+    at.xoff[k] = pair >= 0 ? (pair >> kPairShift) * a.H * 2 : kAbsent;
+  }
   at.step = wave;
   at.by = kUpWaves;
   S st;
-  st.clear();
-  st.run(share_of(steps_of<F>(a.H), wave, kUpWaves), at, a.H, xr, buf[wave], [](int) {});
+  st.init(a.H, a.I);
+  st.run(share_of(steps_of<F>(a.H), wave, kUpWaves), at, a.H, a.x, a.N * a.H * 2,
+         buf + wave * S::buffer_words, [](int) {});
   if (pos0 > 0) __syncthreads();              // red of the tokens before is consumed
-  // red[(wave * 2 + tile) * tokens + token][row]
 #pragma unroll
-  for (int i = 0; i < 2; i++)
-    st.values(i, [&](int t, float v) { red[(wave * 2 + i) * S::tokens + t][lane & 15] = v; });
+  for (int i = 0; i < RT; i++)
+    st.values(i, [&](int t, float v) { red[(wave * RT + i) * S::tokens + t][lane & 15] = v; });
   __syncthreads();
-  for (int q = threadIdx.x; q < nt * 16; q += kUpThreads) {
-    const int t = q >> 4, c = q & 15;
+  for (int q = threadIdx.x; q < nt * RT * 8; q += kUpThreads) {
+    const int t = q / (RT * 8), c = q % (RT * 8), i = c / 16 * 2;
     float g = 0.f, u = 0.f;
 #pragma unroll
     for (int v = 0; v < kUpWaves; v++) {
-      g += red[v * 2 * S::tokens + t][c];
-      u += red[(v * 2 + 1) * S::tokens + t][c];
+      g += red[(v * RT + i) * S::tokens + t][c & 15];
+      u += red[(v * RT + i + 1) * S::tokens + t][c & 15];
     }
     const int pair = r.pair[pos0 + t];
     // the one rounding between the products: the second one's operand is bf16
@@ -731,17 +729,18 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, const Routing& r,
   }
 }
 
-// First kernel: blockIdx.x the tile of 16 gate and up rows, blockIdx.y the
+// First kernel: blockIdx.x the RT/2 tiles of 16 gate and up rows, blockIdx.y the
 // expert among the active ones.  T: token tiles per pass; 0 and 1 without MANY:
 // few tokens.
-template <int F, int T, bool MANY>
+template <int F, int RT, int T, bool MANY, bool PART>
 __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArgs a) {
+  using S = Stream<F, RT, T, PART>;
   __shared__ Routing r;
-  __shared__ float red[kUpWaves * 2 * (T == 0 ? 4 : 16 * T)][16];
-  __shared__ u32x4 buf[kUpWaves][kBuffer];
+  __shared__ float red[kUpWaves * RT * S::tokens][16];
+  __shared__ u32x4 buf[kUpWaves * S::buffer_words];
   extern __shared__ int16_t ids[];            // [N*K]
   int n = 0, before = 0, total = 0;
-  const int j = blockIdx.y, i0 = blockIdx.x * 16;
+  const int j = blockIdx.y, i0 = blockIdx.x * (RT * 8);
   const int e = find_expert<MANY>(a, r, ids, j, n, before, total);
   if (blockIdx.x == 0 && j == 0 && threadIdx.x == 0) {
     a.words[0] = r.bad;
@@ -760,17 +759,15 @@ __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArg
           (uint8_t)(pair < 0 ? 0 : (pair & ((1 << kPairShift) - 1)) + 1);
     }
   }
-  Tile tile[2];
-  const int64_t row = (int64_t)e * 2 * a.I + i0;
-  tile[0] = make_tile<F>(a.w13, row, a.I - i0, a.H);
-  tile[1] = make_tile<F>(a.w13, row + a.I, a.I - i0, a.H);
+  Tiles<F, RT> tiles;
+  tiles.set(a.w13, (int64_t)e * 2 * a.I + i0, a.I - i0, a.I, a.H);
   if constexpr (!MANY) {
-    up_tokens<F, T>(a, r, red, buf, tile, i0, 0, n);
+    up_tokens<F, RT, T, PART>(a, r, red, buf, tiles, i0, 0, n);
   } else {
     if (T == 1 || n > 16)
-      for (int p = 0; p < n; p += 16 * T) up_tokens<F, T>(a, r, red, buf, tile, i0, p, n);
+      for (int p = 0; p < n; p += 16 * T) up_tokens<F, RT, T, PART>(a, r, red, buf, tiles, i0, p, n);
     else
-      up_tokens<F, 1>(a, r, red, buf, tile, i0, 0, n);
+      up_tokens<F, RT, 1, PART>(a, r, red, buf, tiles, i0, 0, n);
   }
 }
 
@@ -787,17 +784,14 @@ struct FewCursor {
   const uint8_t* map;                     // LDS [experts][16]
   int64_t row0;
   int rows, j, step, steps, n, rot;
-  Tile tile[1];
-  int xoff[1][S::rows];
+  Tiles<F, 1> tiles;
+  int xoff[1];
   bool live;
   __device__ __forceinline__ void enter() {
     const int at = min(j, a->experts - 1);
-    tile[0] = make_tile<F>(a->w2, (int64_t)uniform(expert[at]) * a->H + row0, rows, a->I);
-#pragma unroll
-    for (int q = 0; q < S::rows; q++) {
-      const int t = S::token(0, q), k1 = map[at * kFew + t];
-      xoff[0][q] = k1 ? (t * a->K + k1 - 1) * a->I * 2 : kAbsent;
-    }
+    tiles.set(a->w2, (int64_t)uniform(expert[at]) * a->H + row0, rows, 0, a->I);
+    const int t = S::token(0), k1 = map[at * kFew + t];
+    xoff[0] = k1 ? (t * a->K + k1 - 1) * a->I * 2 : kAbsent;
   }
   __device__ __forceinline__ void turn() {
     step = n + rot;
@@ -813,17 +807,17 @@ struct FewCursor {
   }
 };
 
-template <int F, int T>
+template <int F, int T, bool PART>
 __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs a) {
-  using S = Stream<F, 1, T>;
+  using S = Stream<F, 1, T, PART>;
   extern __shared__ u32x4 lds4[];
   int32_t* lds = reinterpret_cast<int32_t*>(lds4);
   const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  u32x4* buf = reinterpret_cast<u32x4*>(lds) + wave * kBuffer;
+  u32x4* buf = lds4 + wave * S::buffer_words;
   float(*red)[S::tokens][16] =
-      reinterpret_cast<float(*)[S::tokens][16]>(lds + waves * kBuffer * 4);
-  int32_t* expert = lds + waves * (kBuffer * 4 + S::tokens * 16);
+      reinterpret_cast<float(*)[S::tokens][16]>(lds + waves * S::buffer_words * 4);
+  int32_t* expert = lds + waves * (S::buffer_words * 4 + S::tokens * 16);
   uint8_t* map = reinterpret_cast<uint8_t*>(expert + a.experts);
   const int active = a.words[1];
   for (int q = threadIdx.x; q < a.experts; q += blockDim.x) expert[q] = a.expert[q];
@@ -840,12 +834,10 @@ __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs
   at.rot = blockIdx.x % steps;           // the same for all that share an expert's steps
   at.turn();
   S st;
-  st.clear();
+  st.init(a.I, 0);
   if (count > 0) {
     at.enter();
-    const auto hr = __builtin_amdgcn_make_buffer_rsrc(a.hidden, 0, a.N * a.K * a.I * 2,
-                                                      kBufferWord3);
-    st.run(count, at, a.I, hr, buf, [](int) {});
+    st.run(count, at, a.I, a.hidden, a.N * a.K * a.I * 2, buf, [](int) {});
   }
   st.values(0, [&](int t, float v) { red[wave][t][lane & 15] = v; });
   __syncthreads();
@@ -877,8 +869,8 @@ struct ManyCursor {
   int64_t row0;
   int rows, steps, item, last, tail, rot;   // tail: the last item's end
   int begin, end, left, step;
-  Tile tile[1];
-  int xoff[T][4];
+  Tiles<F, 1> tiles;
+  int xoff[T];
   bool live;
   __device__ __forceinline__ void enter(int from) {
     const uint32_t it = uniform(items[min(item, last)]);
@@ -889,17 +881,14 @@ struct ManyCursor {
     // wavefronts and workgroups start at different columns: rows of 4 KiB would
     // otherwise have them all in the same few memory channels
     step = begin + rot % left;
-    tile[0] = make_tile<F>(a->w2, (int64_t)e * a->H + row0, rows, a->I);
+    tiles.set(a->w2, (int64_t)e * a->H + row0, rows, 0, a->I);
 #pragma unroll
-    for (int k = 0; k < T; k++)
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int t = Stream<F, 1, T>::token(k, q);
-        const int pair = t < n ? pairs[first + t] : 0;
-        xoff[k][q] = t < n ? ((pair >> kPairShift) * a->K + (pair & ((1 << kPairShift) - 1))) *
-                                 a->I * 2
-                           : kAbsent;
-      }
+    for (int k = 0; k < T; k++) {
+      const int t = Stream<F, 1, T, false>::token(k);
+      const int pair = t < n ? pairs[first + t] : 0;
+      xoff[k] = t < n ? ((pair >> kPairShift) * a->K + (pair & ((1 << kPairShift) - 1))) * a->I * 2
+                      : kAbsent;
+    }
   }
   __device__ __forceinline__ void advance() {
     if (--left == 0) {
@@ -916,23 +905,22 @@ __host__ __device__ inline int most_items(int experts, int pairs, int T) {
   return experts + pairs / (16 * T);
 }
 __host__ __device__ inline int list_words(int pairs) { return (pairs + 1) / 2; }
-size_t many_lds(int N, int K, int experts, int T) {
-  return (size_t)kManyWaves * kBuffer * 16 + (kRows + 16 * T + kManyWaves * 16 * T) * 64 +
+size_t many_lds(int buffer_words, int N, int K, int experts, int T) {
+  return (size_t)kManyWaves * buffer_words * 16 + (kRows + 16 * T + kManyWaves * 16 * T) * 64 +
          4 * ((size_t)most_items(experts, N * K, T) + 2 * list_words(N * K));
 }
 
-template <int F, int T>
+template <int F, int T, bool PART>
 __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_kernel(MoeArgs a) {
-  using S = Stream<F, 1, T>;
+  using S = Stream<F, 1, T, PART>;
   constexpr int kOut = EP_MAX_FEW_TOKENS * 16 / (64 * kManyWaves);   // results per thread
   extern __shared__ u32x4 lds4[];       // (the type aligns it: behind the variables below)
-  int32_t* lds = reinterpret_cast<int32_t*>(lds4);
   __shared__ int n_items;
   __shared__ uint32_t extra_item[kManyWaves];        // item of the extra rows, 0: none
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int NK = a.N * a.K;
-  u32x4* buf = reinterpret_cast<u32x4*>(lds) + wave * kBuffer;
-  float(*own)[16] = reinterpret_cast<float(*)[16]>(lds + kManyWaves * kBuffer * 4);
+  u32x4* buf = lds4 + wave * S::buffer_words;
+  float(*own)[16] = reinterpret_cast<float(*)[16]>(lds4 + kManyWaves * S::buffer_words);
   float(*extra)[16] = own + kRows + 16 * T;          // [waves][16 T]
   uint32_t* items = reinterpret_cast<uint32_t*>(extra + kManyWaves * 16 * T);
   uint16_t* pairs = reinterpret_cast<uint16_t*>(items + most_items(a.experts, NK, T));
@@ -972,7 +960,6 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
     }
   }
   const int h0 = blockIdx.x * 16, steps = steps_of<F>(a.I);
-  const auto hr = __builtin_amdgcn_make_buffer_rsrc(a.hidden, 0, NK * a.I * 2, kBufferWord3);
   float out[kOut];
 #pragma unroll
   for (int i = 0; i < kOut; i++) out[i] = 0.f;
@@ -1002,8 +989,8 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
       int item = at.item, left = at.left;            // where the products are, behind the loads
       bool whole = at.begin == 0;
       S st;
-      st.clear();
-      st.run(s1 - s0, at, a.I, hr, buf, [&](int i) {
+      st.init(a.I, 0);
+      st.run(s1 - s0, at, a.I, a.hidden, NK * a.I * 2, buf, [&](int i) {
         if (i >= s1 - s0 || --left > 0) return;
         const uint32_t it = uniform(items[item]);
         const int n = it >> 23;
@@ -1080,20 +1067,34 @@ int validate_moe(const ep_problem_t* p, int inter) {
   return EP_OK;
 }
 
+// f(std::bool_constant<last step is a part>)
+template <int F, typename Fn>
+void with_part(int cols, Fn&& f) {
+  if (cols % Fmt<F>::step) f(std::true_type());
+  else f(std::false_type());
+}
+
 template <int F, int T, bool MANY>
 void launch_moe(const MoeArgs& a, hipStream_t st) {
-  const dim3 up((a.I + 15) / 16, a.experts);
+  constexpr int RT = T == 0 ? 2 : EP_URT, UT = MANY ? EP_UT : T;
+  const dim3 up((a.I + RT * 8 - 1) / (RT * 8), a.experts);
   const int down = (a.H + 15) / 16;
-  const size_t ids = sizeof(int16_t) * a.N * a.K;
-  moe_up_kernel<F, (MANY ? EP_UT : T), MANY><<<up, kUpThreads, ids, st>>>(a);
-  if constexpr (MANY) {
-    moe_down_many_kernel<F, T><<<down, 64 * kManyWaves, many_lds(a.N, a.K, a.experts, T), st>>>(a);
-  } else {
-    constexpr int waves = EP_DWAVES;
-    const size_t lds = sizeof(float) * waves * (kBuffer * 4 + Stream<F, 1, T>::tokens * 16) +
-                       (size_t)a.experts * (4 + kFew);
-    moe_down_few_kernel<F, T><<<down, 64 * waves, lds, st>>>(a);
-  }
+  with_part<F>(a.H, [&](auto part) {
+    moe_up_kernel<F, RT, UT, MANY, part.value>
+        <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
+  });
+  with_part<F>(a.I, [&](auto part) {
+    constexpr int words = Stream<F, 1, T, false>::buffer_words;
+    if constexpr (MANY) {
+      moe_down_many_kernel<F, T, part.value>
+          <<<down, 64 * kManyWaves, many_lds(words, a.N, a.K, a.experts, T), st>>>(a);
+    } else {
+      constexpr int waves = EP_DWAVES;
+      const size_t lds = sizeof(float) * waves * (words * 4 + Stream<F, 1, T, false>::tokens * 16) +
+                         (size_t)a.experts * (4 + kFew);
+      moe_down_few_kernel<F, T, part.value><<<down, 64 * waves, lds, st>>>(a);
+    }
+  });
 }
 
 template <int F>
@@ -1116,10 +1117,14 @@ int launch_linear(int n, int cols, int rows, const void* x, const Weight& w, voi
   uint16_t* yp = (uint16_t*)y;
   EP_LOG("quant_linear: n=%d cols=%d rows=%d grid=%d", n, cols, rows, gx);
   constexpr int B = 64 * kLinWaves;
-  if (n <= 4) linear_kernel<F, RT, 0><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
-  else if (n <= 16) linear_kernel<F, RT, 1><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
-  else
-    linear_kernel<F, RT, 2><<<dim3(gx, (n + 31) / 32), B, 0, st>>>(xp, w, yp, n, cols, rows);
+  with_part<F>(cols, [&](auto part) {
+    constexpr bool P = part.value;
+    if (n <= 4) linear_kernel<F, RT, 0, P><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
+    else if (n <= 16)
+      linear_kernel<F, RT, 1, P><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
+    else
+      linear_kernel<F, RT, 2, P><<<dim3(gx, (n + 31) / 32), B, 0, st>>>(xp, w, yp, n, cols, rows);
+  });
   return check_launch("quant_linear");
 }
 
