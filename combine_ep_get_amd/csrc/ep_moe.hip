@@ -20,9 +20,10 @@
 //     last, absent tokens) its buffer offset is out of range and the hardware
 //     returns zeros, so the loop has no branches.
 //
-// A step is 128 columns of bf16 or 256 of codes, four MFMAs per 128; MFMA j of a
-// half takes columns j*32 .. j*32+31, lane group g eight of them.  A 4-bit weight
-// is scaled per (row, group): lane r holds row r's column of the 16x16 result,
+// A step is 128 columns of bf16 or 256 of codes, four MFMAs per 128.  Which eight
+// columns of these 128 lane group g feeds to MFMA j is free as long as both operands
+// agree (Fmt::col): it is what a lane reads from LDS at once.  A 4-bit weight is
+// scaled per (row, group): lane r holds row r's column of the 16x16 result,
 // so one factor per lane does it, after the sum over the group, in float32.  int4
 // codes become bf16 by putting the nibble under the exponent of 128 (exact:
 // 128 + code); the 128 and the zero point leave again as (128 + zero) * sum(x),
@@ -44,7 +45,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format
@@ -95,7 +96,13 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 #define EP_UT 2
 #endif
 #ifndef EP_URT
-#define EP_URT 2
+#define EP_URT 4
+#endif
+#ifndef EP_DRT
+#define EP_DRT 2
+#endif
+#ifndef EP_KS
+#define EP_KS 4
 #endif
 #ifndef EP_DWAVES
 #define EP_DWAVES 8
@@ -112,6 +119,16 @@ struct Fmt {
   static constexpr int halves = step / 128;          // of 128 columns, four MFMAs each
   static constexpr int chunks = quant ? 8 : 16;      // 16-byte chunks of a row per step
   static constexpr int loads = chunks / 4;           // 1 KiB loads per tile and step
+  // words of a row's codes that a lane reads together and feeds to MFMAs one after
+  // the other: as many as stay inside a group, so that an MFMA's 32 columns are of
+  // one group (mxfp4 scales each lane's codes by themselves)
+  static constexpr int words = integer ? group / 32 : 4;
+  // first of the eight columns (of a half) that lane group g feeds to MFMA j
+  static __device__ __forceinline__ int col(int g, int j) {
+    if constexpr (quant && words == 4) return g * 32 + j * 8;
+    else if constexpr (words == 2) return (j >> 1) * 64 + g * 16 + (j & 1) * 8;
+    else return j * 32 + g * 8;
+  }
   static constexpr int groups = quant ? 128 / group : 1;    // scales per half
   static constexpr int scales = quant ? step / group : 0;   // scales of a row per step
   static constexpr int scale_bytes = F == kMx ? 1 : 2;
@@ -167,14 +184,15 @@ struct Tiles {
 // last step has fewer columns.
 //
 // Where the steps come from is the caller's cursor: `step` (which columns),
-// `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT]` (the row of
-// x of token(k) in bytes, kAbsent for none) and advance().
+// `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row
+// of x of token(k, j) in bytes, kAbsent for none) and advance().
 template <int F, int RT, int T, bool PART>
 struct Stream {
   using M = Fmt<F>;
   static constexpr bool quad = T == 0;
   static constexpr int TT = quad ? 1 : T;
   static constexpr int tokens = quad ? 4 : 16 * TT;
+  static constexpr int rows = quad ? 1 : 4;                       // loads of x per tile and half
   static constexpr int values_per_row = RT * M::scales;           // scales of a step, all tiles
   static constexpr int scale_loads = (values_per_row + 3) / 4;    // a value per lane group
   // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's
@@ -183,13 +201,14 @@ struct Stream {
                                         : (quad ? EP_DB : 2);
   // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros
   static constexpr int tile_words = 16 * M::chunks;
-  static constexpr int buffer_words =
-      RT * tile_words + values_per_row * 4 * (M::zeros ? 2 : 1);
+  static constexpr int scale_words = M::integer ? 16 * scale_loads : 0;
+  static constexpr int x_at = RT * tile_words + scale_words * (M::zeros ? 2 : 1);
+  static constexpr int buffer_words = x_at + (quad ? 0 : 256);
 
   struct Slot {
     u32x4 w[RT][M::loads];                           // as loaded: see load()
     uint32_t s[M::quant ? scale_loads : 1], z[M::zeros ? scale_loads : 1];
-    u32x4 x[TT][M::halves][quad ? 1 : 4];            // MFMA operands (Quad: one for all four)
+    u32x4 x[TT][M::halves][quad ? 1 : 4];            // as loaded (Quad: the MFMA operand)
   };
 
   // acc[i][j]: Quad: MFMA j's own rows (bf16, mxfp4), or [i][0] the whole sum
@@ -222,10 +241,11 @@ struct Stream {
         soff[q] = v < values_per_row ? row * rg + v % M::scales : kOutside / 2;
       }
     }
-    xcol = g * 8 + (quad ? (lane & 3) * 32 : 0);
+    xcol = quad ? M::col(g, lane & 3) : r * 8;
   }
 
-  // A step's loads.
+  // A step's loads.  x comes as the weights do: 256 bytes of four rows per load (a load
+  // in the MFMA's layout, 64 bytes of 16 rows, takes four times as long in L1).
   template <typename Cursor>
   __device__ __forceinline__ void load(Slot& b, const Cursor& at, int cols, const void* x,
                                        int xbytes) {
@@ -258,16 +278,16 @@ struct Stream {
     const auto xr = buffer(x, at.live ? xbytes : 0);
     const int left = cols - step * M::step;          // columns left from here
 #pragma unroll
-    for (int m = 0; m < M::halves; m++)
+    for (int m = 0; m < M::halves; m++) {
+      const int c = m * 128 + xcol;
+      const bool in = !PART || c < left;
 #pragma unroll
-      for (int j = 0; j < (quad ? 1 : 4); j++) {
-        const int c = m * 128 + j * 32;
-        const bool in = !PART || c + xcol < left;
+      for (int k = 0; k < TT; k++)
 #pragma unroll
-        for (int k = 0; k < TT; k++)
+        for (int j = 0; j < rows; j++)
           b.x[k][m][j] = __builtin_amdgcn_raw_buffer_load_b128(
-              xr, in ? at.xoff[k] + (xcol + c) * 2 : kOutside, step * (M::step * 2), 0);
-      }
+              xr, in ? at.xoff[k][j] + c * 2 : kOutside, step * (M::step * 2), 0);
+    }
   }
 
   // The wavefront's LDS accesses execute in order; the fences bind the compiler.
@@ -276,11 +296,11 @@ struct Stream {
     __builtin_amdgcn_wave_barrier();
   }
 
-  // Where chunk c of row r lies in its tile: permuted so that the lanes that access
-  // LDS together, writing (a row's chunks) or reading (16 rows, one chunk of 16
-  // bytes or four of its words), fall on different banks.
+  // Where chunk c of row r lies in its tile: permuted so that the 8 lanes of an
+  // access phase fall on different banks when they write (a row's chunks) and when
+  // they read (8 rows, one chunk).
   static __device__ __forceinline__ int place(int r, int c) {
-    return r * M::chunks + (c ^ (M::quant ? (r >> 1) & 7 : r));
+    return r * M::chunks + (c ^ (r & (M::chunks - 1)));
   }
 
   // Write the step's tiles and scales to LDS.
@@ -293,40 +313,44 @@ struct Stream {
       for (int q = 0; q < M::loads; q++)
         buf[i * tile_words +
             place(q * (64 / M::chunks) + lane / M::chunks, lane & (M::chunks - 1))] = b.w[i][q];
-    if constexpr (M::quant) {
-      uint32_t* sb = reinterpret_cast<uint32_t*>(buf + RT * tile_words);
-      float* zb = reinterpret_cast<float*>(sb + values_per_row * 16);
+    if constexpr (M::integer) {
+      // [load][row][lane group]
+      float* sb = reinterpret_cast<float*>(buf + RT * tile_words);
 #pragma unroll
       for (int q = 0; q < scale_loads; q++) {
-        const int v = q * 4 + g;
-        if (values_per_row % 4 == 0 || v < values_per_row) {
-          sb[r * values_per_row + v] = M::integer ? b.s[q] << 16 : b.s[q] << 23;
-          if constexpr (M::zeros) zb[r * values_per_row + v] = 128.f + (float)b.z[q];
-        }
+        sb[q * 64 + r * 4 + g] = __uint_as_float(b.s[q] << 16);
+        if constexpr (M::zeros) sb[(scale_loads + q) * 64 + r * 4 + g] = 128.f + (float)b.z[q];
       }
     }
     fence();
   }
 
   // The row's scales (or zeros: 128 + zero) of the step, by tile and group.
-  static __device__ __forceinline__ void take_scales(const u32x4* at, float* v) {
+  static __device__ __forceinline__ void take_scales(const u32x4* at, f32x4* v) {
     const int r = threadIdx.x & 15;
-    if constexpr (values_per_row % 4 == 0) {
-      const f32x4* from = reinterpret_cast<const f32x4*>(at) + r * (values_per_row / 4);
 #pragma unroll
-      for (int q = 0; q < values_per_row / 4; q++) {
-        const f32x4 t = from[q];
+    for (int q = 0; q < scale_loads; q++) v[q] = reinterpret_cast<const f32x4*>(at)[q * 16 + r];
+  }
+
+  // Half m of tile i: the four words of codes for the MFMAs.
+  static __device__ __forceinline__ u32x4 take_codes(const u32x4* buf, int i, int m) {
+    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    buf += i * tile_words;
+    u32x4 v;
+    if constexpr (M::words == 4) {
+      v = buf[place(r, m * 4 + g)];
+    } else if constexpr (M::words == 2) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[q * 4 + e] = t[e];
+      for (int q = 0; q < 2; q++) {
+        const u32x2 t = reinterpret_cast<const u32x2*>(buf + place(r, m * 4 + q * 2 + (g >> 1)))[g & 1];
+        v[q * 2] = t.x, v[q * 2 + 1] = t.y;
       }
     } else {
-      const f32x2* from = reinterpret_cast<const f32x2*>(at) + r * (values_per_row / 2);
 #pragma unroll
-      for (int q = 0; q < values_per_row / 2; q++) {
-        const f32x2 t = from[q];
-        v[q * 2] = t[0], v[q * 2 + 1] = t[1];
-      }
+      for (int q = 0; q < 4; q++)
+        v[q] = reinterpret_cast<const uint32_t*>(buf + place(r, m * 4 + q))[g];
     }
+    return v;
   }
 
   // The eight bf16 weights of a word of codes (int4: 128 + code; mxfp4: scaled).
@@ -352,24 +376,51 @@ struct Stream {
     const u32x4 ones{kOnes, kOnes, kOnes, kOnes};
     constexpr int per = 4 / M::groups;               // MFMAs per group
     put(b, buf);
-    float sv[M::quant ? values_per_row : 1], zv[M::zeros ? values_per_row : 1];
-    if constexpr (M::quant) take_scales(buf + RT * tile_words, sv);
-    if constexpr (M::zeros) take_scales(buf + RT * tile_words + values_per_row * 4, zv);
+    f32x4 sv[M::integer ? scale_loads : 1], zv[M::zeros ? scale_loads : 1];
+    if constexpr (M::integer) take_scales(buf + RT * tile_words, sv);
+    if constexpr (M::zeros) take_scales(buf + RT * tile_words + scale_words, zv);
+    u32x4 codes[RT][M::halves];
+    if constexpr (M::quant) {
+#pragma unroll
+      for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int m = 0; m < M::halves; m++) codes[i][m] = take_codes(buf, i, m);
+    }
     const auto weight = [&](int i, int m, int j) {   // operand of MFMA j
-      if constexpr (!M::quant) {
-        return buf[i * tile_words + place(r, j * 4 + g)];
-      } else {
-        const uint32_t w =
-            reinterpret_cast<const uint32_t*>(buf + i * tile_words + place(r, m * 4 + j))[g];
-        return operand(w, M::integer ? 0.f : sv[i * M::scales + m * 4 + j]);
-      }
+      if constexpr (!M::quant) return buf[i * tile_words + place(r, j * 4 + g)];
+      // mxfp4: the lane group that loaded a scale is the one whose codes it scales
+      else return operand(codes[i][m][j],
+                          M::integer ? 0.f : __uint_as_float(b.s[i * M::halves + m] << 23));
     };
-    const auto x = [&](int k, int m, int j) { return b.x[k][m][quad ? 0 : j]; };
+    const auto scale = [&](int i, int m, int q) {
+      const int v = i * M::scales + m * M::groups + q;
+      return sv[v / 4][v % 4];
+    };
     const auto zero = [&](int i, int m, int q) {     // off the codes as the operand has them
-      return M::zeros ? zv[i * M::scales + m * M::groups + q] : 136.f;
+      const int v = i * M::scales + m * M::groups + q;
+      return M::zeros ? zv[v / 4][v % 4] : 136.f;
     };
 #pragma unroll
     for (int m = 0; m < M::halves; m++) {
+      u32x4 xo[TT][4];
+#pragma unroll
+      for (int k = 0; k < TT; k++) {
+        if constexpr (quad) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) xo[k][j] = b.x[k][m][0];
+        } else {
+          const int lane = threadIdx.x & 63;
+          u32x4* xb = buf + x_at;
+          fence();
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            xb[(j * 4 + (lane >> 4)) * 16 + ((lane & 15) ^ (j * 4 + (lane >> 4)))] = b.x[k][m][j];
+          fence();
+#pragma unroll
+          for (int j = 0; j < 4; j++) xo[k][j] = xb[r * 16 + ((M::col(g, j) / 8) ^ r)];
+        }
+      }
+      const auto x = [&](int k, int, int j) { return xo[k][j]; };
       if constexpr (!M::integer) {
 #pragma unroll
         for (int i = 0; i < RT; i++)
@@ -395,7 +446,7 @@ struct Stream {
               sum += d[j];
               xs += sx[j];
             }
-            acc[i][0][0] = fmaf(sv[i * M::scales + m * M::groups + q],
+            acc[i][0][0] = fmaf(scale(i, m, q),
                                 fmaf(-zero(i, m, q), xs, sum), acc[i][0][0]);
           }
       } else {
@@ -419,7 +470,7 @@ struct Stream {
 #pragma unroll
               for (int k = 0; k < TT; k++) d[k] = mfma(x(k, m, j), o, d[k]);
             }
-            const float s = sv[i * M::scales + m * M::groups + q], z = zero(i, m, q);
+            const float s = scale(i, m, q), z = zero(i, m, q);
 #pragma unroll
             for (int k = 0; k < TT; k++)
 #pragma unroll
@@ -445,6 +496,7 @@ struct Stream {
     for (int i = 0; i < count; i += depth) {
 #pragma unroll
       for (int d = 0; d < depth; d++) {
+        if (d > 0 && i + d >= count) break;
         compute(slot[d], buf);
         at.live = i + d + depth < count;
         load(slot[d], at, cols, x, xbytes);
@@ -454,10 +506,10 @@ struct Stream {
     }
   }
 
-  // The token row that the lane loads of x in token tile k.
-  static __device__ __forceinline__ int token(int k) {
+  // The token row that the lane's load j of x is of in token tile k.
+  static __device__ __forceinline__ int token(int k, int j) {
     const int lane = threadIdx.x & 63;
-    return quad ? (lane & 15) >> 2 : k * 16 + (lane & 15);
+    return quad ? (lane & 15) >> 2 : k * 16 + j * 4 + (lane >> 4);
   }
 
   // f(token, value) for every token row this lane holds of weight tile i (its
@@ -478,10 +530,10 @@ struct Stream {
 };
 
 // The cursor over every by-th step of the same tiles and rows.
-template <int F, int RT, int TT>
+template <int F, int RT, typename S>
 struct Strided {
   Tiles<F, RT> tiles;
-  int xoff[TT];
+  int xoff[S::TT][S::rows];
   int step, by;
   bool live;
   __device__ __forceinline__ void advance() { step += by; }
@@ -506,10 +558,15 @@ __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int row0 = blockIdx.x * (RT * 16), t0 = blockIdx.y * S::tokens;
   const int nt = min(n - t0, S::tokens);
-  Strided<F, RT, S::TT> at;
+  Strided<F, RT, S> at;
   at.tiles.set(w, row0, rows - row0, 0, cols);
 #pragma unroll
-  for (int k = 0; k < S::TT; k++) at.xoff[k] = S::token(k) < nt ? S::token(k) * cols * 2 : kAbsent;
+  for (int k = 0; k < S::TT; k++)
+#pragma unroll
+    for (int q = 0; q < S::rows; q++) {
+      const int t = S::token(k, q);
+      at.xoff[k][q] = t < nt ? t * cols * 2 : kAbsent;
+    }
   at.step = wave;
   at.by = kLinWaves;
   S st;
@@ -577,6 +634,7 @@ struct MoeArgs {
   uint16_t* hidden;                       // [N*K][I] bf16: weight * silu(gate) * up
   int N, H, K, E, I, wide;                // wide: 64-bit ids
   int experts;
+  int split;                              // first kernel: wavefronts per contraction
 };
 
 // A routing entry as an expert id; whatever is no expert becomes -1, and bad
@@ -623,12 +681,27 @@ struct Routing {
   int32_t bad;
 };
 
+// What thread `tid` keeps of token tid's weight until the products are there: the
+// load is on its way meanwhile.
+struct Gate {
+  uint32_t named;
+  int at;                                     // place in the expert's list, -1: not there
+  float weight;
+  __device__ __forceinline__ void put(const MoeArgs& a, Routing& r) const {
+    if (at < 0) return;
+    float w = weight;
+    for (uint32_t more = named & (named - 1); more; more &= more - 1)
+      w += a.weights[threadIdx.x * a.K + __ffs(more) - 1];   // named twice: the weights add up
+    r.weight[at] = w;
+  }
+};
+
 // Finds the j-th active expert, its tokens (in order) with their weights, and
 // how many pairs name lower experts.  ids: LDS for N*K entries.  Returns the
 // id, -1 if there are fewer.
 template <bool MANY>
 __device__ __forceinline__ int find_expert(const MoeArgs& a, Routing& r, int16_t* ids, int j,
-                                           int& n, int& before, int& total) {
+                                           Gate& gate, int& n, int& before, int& total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (tid < EP_MAX_EXPERTS / 32) r.bitmap[tid] = 0;
   if (tid == 0) r.bad = 0;
@@ -643,22 +716,21 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, Routing& r, int16_t
   __syncthreads();
   const int e = uniform(nth_active(r.bitmap, j, total));
   if (e < 0) return -1;
-  int k0 = -1, below = 0;
-  float w = 0.f;
+  int below = 0;
+  uint32_t named = 0;                         // the choices of token tid that are e
   if (tid < a.N)
     for (int k = 0; k < a.K; k++) {
       const int o = ids[tid * a.K + k];
-      if (o == e) {
-        if (k0 < 0) k0 = k;
-        w += a.weights[tid * a.K + k];        // an expert named twice: the weights add up
-      }
+      named |= o == e ? 1u << k : 0u;
       below += o >= 0 && o < e ? 1 : 0;
     }
+  const int k0 = __ffs(named) - 1;
+  gate.named = named;
+  gate.at = -1;
+  if (k0 >= 0) gate.weight = a.weights[tid * a.K + k0];   // waited for in Gate::put
   if constexpr (!MANY) {
-    if (tid < kFew) {
-      r.pair[tid] = k0 >= 0 ? tid << kPairShift | k0 : -1;
-      r.weight[tid] = w;
-    }
+    if (tid < kFew) r.pair[tid] = k0 >= 0 ? tid << kPairShift | k0 : -1;
+    if (k0 >= 0) gate.at = tid;
     n = a.N;
   } else {
     const uint64_t has = __ballot(k0 >= 0);
@@ -676,7 +748,7 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, Routing& r, int16_t
     }
     if (k0 >= 0) {
       r.pair[at] = tid << kPairShift | k0;
-      r.weight[at] = w;
+      gate.at = at;
     }
     n = uniform(n);
   }
@@ -686,38 +758,43 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, Routing& r, int16_t
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// Entries pos0 .. of the expert's list through RT/2 pairs of 16 gate and 16 up rows.
-// red[(wave * RT + tile) * tokens + token][row]
+// A workgroup's four wavefronts share 4/split groups of tiles (RT/2 pairs of 16 gate
+// and 16 up rows), split of them the contraction of each.
+// Entries pos0 .. of the expert's list; red[(wave * RT + tile) * tokens + token][row]
 template <int F, int RT, int T, bool PART>
-__device__ __forceinline__ void up_tokens(const MoeArgs& a, const Routing& r, float (*red)[16],
-                                          u32x4* buf, const Tiles<F, RT>& tiles, int i0, int pos0,
-                                          int n) {
+__device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Gate& gate,
+                                          float (*red)[16], u32x4* buf, const Tiles<F, RT>& tiles,
+                                          int i0, int pos0, int n) {
   using S = Stream<F, RT, T, PART>;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = min(n - pos0, S::tokens);
-  Strided<F, RT, S::TT> at;
+  Strided<F, RT, S> at;
   at.tiles = tiles;
 #pragma unroll
-  for (int k = 0; k < S::TT; k++) {
-    const int t = S::token(k), pair = t < nt ? r.pair[pos0 + t] : -1;
-    at.xoff[k] = pair >= 0 ? (pair >> kPairShift) * a.H * 2 : kAbsent;
-  }
-  at.step = wave;
-  at.by = kUpWaves;
+  for (int k = 0; k < S::TT; k++)
+#pragma unroll
+    for (int q = 0; q < S::rows; q++) {
+      const int t = S::token(k, q), pair = t < nt ? r.pair[pos0 + t] : -1;
+      at.xoff[k][q] = pair >= 0 ? (pair >> kPairShift) * a.H * 2 : kAbsent;
+    }
+  at.step = wave & (a.split - 1);
+  at.by = a.split;
   S st;
   st.init(a.H, a.I);
-  st.run(share_of(steps_of<F>(a.H), wave, kUpWaves), at, a.H, a.x, a.N * a.H * 2,
+  st.run(share_of(steps_of<F>(a.H), at.step, a.split), at, a.H, a.x, a.N * a.H * 2,
          buf + wave * S::buffer_words, [](int) {});
   if (pos0 > 0) __syncthreads();              // red of the tokens before is consumed
+  else gate.put(a, r);
 #pragma unroll
   for (int i = 0; i < RT; i++)
     st.values(i, [&](int t, float v) { red[(wave * RT + i) * S::tokens + t][lane & 15] = v; });
   __syncthreads();
-  for (int q = threadIdx.x; q < nt * RT * 8; q += kUpThreads) {
-    const int t = q / (RT * 8), c = q % (RT * 8), i = c / 16 * 2;
+  const int wide = kUpWaves / a.split * RT * 8;      // rows of hidden per workgroup
+  for (int q = threadIdx.x; q < nt * wide; q += kUpThreads) {
+    const int t = q / wide, c = q - t * wide;
+    const int w0 = c / (RT * 8) * a.split, i = c % (RT * 8) / 16 * 2;
     float g = 0.f, u = 0.f;
-#pragma unroll
-    for (int v = 0; v < kUpWaves; v++) {
+    for (int v = w0; v < w0 + a.split; v++) {
       g += red[(v * RT + i) * S::tokens + t][c & 15];
       u += red[(v * RT + i + 1) * S::tokens + t][c & 15];
     }
@@ -729,9 +806,8 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, const Routing& r, fl
   }
 }
 
-// First kernel: blockIdx.x the RT/2 tiles of 16 gate and up rows, blockIdx.y the
-// expert among the active ones.  T: token tiles per pass; 0 and 1 without MANY:
-// few tokens.
+// First kernel: blockIdx.x the groups of tiles, blockIdx.y the expert among the
+// active ones.  T: token tiles per pass; 0 and 1 without MANY: few tokens.
 template <int F, int RT, int T, bool MANY, bool PART>
 __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
@@ -740,8 +816,9 @@ __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArg
   __shared__ u32x4 buf[kUpWaves * S::buffer_words];
   extern __shared__ int16_t ids[];            // [N*K]
   int n = 0, before = 0, total = 0;
-  const int j = blockIdx.y, i0 = blockIdx.x * (RT * 8);
-  const int e = find_expert<MANY>(a, r, ids, j, n, before, total);
+  const int j = blockIdx.y, i0 = blockIdx.x * (kUpWaves / a.split * RT * 8);
+  Gate gate;
+  const int e = find_expert<MANY>(a, r, ids, j, gate, n, before, total);
   if (blockIdx.x == 0 && j == 0 && threadIdx.x == 0) {
     a.words[0] = r.bad;
     a.words[1] = total;
@@ -760,38 +837,43 @@ __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArg
     }
   }
   Tiles<F, RT> tiles;
-  tiles.set(a.w13, (int64_t)e * 2 * a.I + i0, a.I - i0, a.I, a.H);
+  const int own = i0 + uniform(threadIdx.x >> 6) / a.split * (RT * 8);
+  tiles.set(a.w13, (int64_t)e * 2 * a.I + min(own, a.I), a.I - own, a.I, a.H);
   if constexpr (!MANY) {
-    up_tokens<F, RT, T, PART>(a, r, red, buf, tiles, i0, 0, n);
+    up_tokens<F, RT, T, PART>(a, r, gate, red, buf, tiles, i0, 0, n);
   } else {
     if (T == 1 || n > 16)
-      for (int p = 0; p < n; p += 16 * T) up_tokens<F, RT, T, PART>(a, r, red, buf, tiles, i0, p, n);
+      for (int p = 0; p < n; p += 16 * T)
+        up_tokens<F, RT, T, PART>(a, r, gate, red, buf, tiles, i0, p, n);
     else
-      up_tokens<F, RT, 1, PART>(a, r, red, buf, tiles, i0, 0, n);
+      up_tokens<F, RT, 1, PART>(a, r, gate, red, buf, tiles, i0, 0, n);
   }
 }
 
-// ---- second product.  One workgroup owns 16 columns of y and walks the active
+// ---- second product.  One workgroup owns RT*16 columns of y and walks the active
 // experts; its wavefronts share the steps of all of them evenly, one stream of
 // loads each that does not stop between experts.  The parts meet in LDS and are
 // added in the wavefronts' order: no atomics, the same sums on every run.
 
 // Few: token rows are the same for every expert, the accumulators go through.
-template <int F, typename S>
+template <int F, int RT, typename S>
 struct FewCursor {
   const MoeArgs* a;
   const int32_t* expert;                  // LDS
   const uint8_t* map;                     // LDS [experts][16]
   int64_t row0;
   int rows, j, step, steps, n, rot;
-  Tiles<F, 1> tiles;
-  int xoff[1];
+  Tiles<F, RT> tiles;
+  int xoff[1][S::rows];
   bool live;
   __device__ __forceinline__ void enter() {
     const int at = min(j, a->experts - 1);
     tiles.set(a->w2, (int64_t)uniform(expert[at]) * a->H + row0, rows, 0, a->I);
-    const int t = S::token(0), k1 = map[at * kFew + t];
-    xoff[0] = k1 ? (t * a->K + k1 - 1) * a->I * 2 : kAbsent;
+#pragma unroll
+    for (int q = 0; q < S::rows; q++) {
+      const int t = S::token(0, q), k1 = map[at * kFew + t];
+      xoff[0][q] = k1 ? (t * a->K + k1 - 1) * a->I * 2 : kAbsent;
+    }
   }
   __device__ __forceinline__ void turn() {
     step = n + rot;
@@ -807,28 +889,29 @@ struct FewCursor {
   }
 };
 
-template <int F, int T, bool PART>
+template <int F, int RT, int T, bool PART>
 __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs a) {
-  using S = Stream<F, 1, T, PART>;
+  using S = Stream<F, RT, T, PART>;
+  constexpr int wide = RT * 16;               // columns of y per workgroup
   extern __shared__ u32x4 lds4[];
   int32_t* lds = reinterpret_cast<int32_t*>(lds4);
   const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   u32x4* buf = lds4 + wave * S::buffer_words;
-  float(*red)[S::tokens][16] =
-      reinterpret_cast<float(*)[S::tokens][16]>(lds + waves * S::buffer_words * 4);
-  int32_t* expert = lds + waves * (S::buffer_words * 4 + S::tokens * 16);
+  float(*red)[S::tokens][wide] =
+      reinterpret_cast<float(*)[S::tokens][wide]>(lds + waves * S::buffer_words * 4);
+  int32_t* expert = lds + waves * (S::buffer_words * 4 + S::tokens * wide);
   uint8_t* map = reinterpret_cast<uint8_t*>(expert + a.experts);
   const int active = a.words[1];
   for (int q = threadIdx.x; q < a.experts; q += blockDim.x) expert[q] = a.expert[q];
   for (int q = threadIdx.x; q < a.experts * (kFew / 4); q += blockDim.x)
     reinterpret_cast<uint32_t*>(map)[q] = ((const uint32_t*)a.pairs)[q];
   __syncthreads();
-  const int h0 = blockIdx.x * 16, steps = steps_of<F>(a.I);
+  const int h0 = blockIdx.x * wide, steps = steps_of<F>(a.I);
   const int total = uniform(active) * steps;
   const int first = (int)((int64_t)total * wave / waves);
   const int count = (int)((int64_t)total * (wave + 1) / waves) - first;
-  FewCursor<F, S> at;
+  FewCursor<F, RT, S> at;
   at.a = &a, at.expert = expert, at.map = map, at.row0 = h0, at.rows = a.H - h0;
   at.j = first / steps, at.n = first % steps, at.steps = steps;
   at.rot = blockIdx.x % steps;           // the same for all that share an expert's steps
@@ -839,10 +922,12 @@ __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs
     at.enter();
     st.run(count, at, a.I, a.hidden, a.N * a.K * a.I * 2, buf, [](int) {});
   }
-  st.values(0, [&](int t, float v) { red[wave][t][lane & 15] = v; });
+#pragma unroll
+  for (int i = 0; i < RT; i++)
+    st.values(i, [&](int t, float v) { red[wave][t][i * 16 + (lane & 15)] = v; });
   __syncthreads();
-  for (int q = threadIdx.x; q < a.N * 16; q += blockDim.x) {
-    const int t = q >> 4, c = q & 15;
+  for (int q = threadIdx.x; q < a.N * wide; q += blockDim.x) {
+    const int t = q / wide, c = q % wide;
     float v = 0.f;
     for (int u = 0; u < waves; u++) v += red[u][t][c];
     if (h0 + c < a.H) a.y[(int64_t)t * a.H + h0 + c] = bf16_bits(v);
@@ -855,13 +940,13 @@ __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs
 // writes: the item's own rows, by list position, if the segment begins the
 // item, else the wavefront's extra rows (only its first segment can begin
 // inside an item).  In the end every (token, column) sums up its own rows, in
-// a fixed order.  LDS holds kRows listed pairs at a time; longer lists take
+// a fixed order.  LDS holds rows_kept listed pairs at a time; longer lists take
 // several rounds.
 // item: expert | first pair << 10 | tokens << 23.
 constexpr int kManyWaves = 8;
-constexpr int kRows = 384;
+constexpr int rows_kept(int RT) { return 384 / RT; }
 
-template <int F, int T>
+template <int F, int RT, int T>
 struct ManyCursor {
   const MoeArgs* a;
   const uint32_t* items;                  // LDS
@@ -869,8 +954,8 @@ struct ManyCursor {
   int64_t row0;
   int rows, steps, item, last, tail, rot;   // tail: the last item's end
   int begin, end, left, step;
-  Tiles<F, 1> tiles;
-  int xoff[T];
+  Tiles<F, RT> tiles;
+  int xoff[T][4];
   bool live;
   __device__ __forceinline__ void enter(int from) {
     const uint32_t it = uniform(items[min(item, last)]);
@@ -883,12 +968,15 @@ struct ManyCursor {
     step = begin + rot % left;
     tiles.set(a->w2, (int64_t)e * a->H + row0, rows, 0, a->I);
 #pragma unroll
-    for (int k = 0; k < T; k++) {
-      const int t = Stream<F, 1, T, false>::token(k);
-      const int pair = t < n ? pairs[first + t] : 0;
-      xoff[k] = t < n ? ((pair >> kPairShift) * a->K + (pair & ((1 << kPairShift) - 1))) * a->I * 2
-                      : kAbsent;
-    }
+    for (int k = 0; k < T; k++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int t = Stream<F, RT, T, false>::token(k, q);
+        const int pair = t < n ? pairs[first + t] : 0;
+        xoff[k][q] = t < n ? ((pair >> kPairShift) * a->K + (pair & ((1 << kPairShift) - 1))) *
+                                 a->I * 2
+                           : kAbsent;
+      }
   }
   __device__ __forceinline__ void advance() {
     if (--left == 0) {
@@ -905,23 +993,25 @@ __host__ __device__ inline int most_items(int experts, int pairs, int T) {
   return experts + pairs / (16 * T);
 }
 __host__ __device__ inline int list_words(int pairs) { return (pairs + 1) / 2; }
-size_t many_lds(int buffer_words, int N, int K, int experts, int T) {
-  return (size_t)kManyWaves * buffer_words * 16 + (kRows + 16 * T + kManyWaves * 16 * T) * 64 +
+size_t many_lds(int buffer_words, int N, int K, int experts, int RT, int T) {
+  return (size_t)kManyWaves * buffer_words * 16 +
+         (size_t)(rows_kept(RT) + 16 * T + kManyWaves * 16 * T) * RT * 64 +
          4 * ((size_t)most_items(experts, N * K, T) + 2 * list_words(N * K));
 }
 
-template <int F, int T, bool PART>
+template <int F, int RT, int T, bool PART>
 __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_kernel(MoeArgs a) {
-  using S = Stream<F, 1, T, PART>;
-  constexpr int kOut = EP_MAX_FEW_TOKENS * 16 / (64 * kManyWaves);   // results per thread
+  using S = Stream<F, RT, T, PART>;
+  constexpr int wide = RT * 16, kRows = rows_kept(RT);     // columns of y; listed pairs at a time
+  constexpr int kOut = EP_MAX_FEW_TOKENS * wide / (64 * kManyWaves);   // results per thread
   extern __shared__ u32x4 lds4[];       // (the type aligns it: behind the variables below)
   __shared__ int n_items;
   __shared__ uint32_t extra_item[kManyWaves];        // item of the extra rows, 0: none
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int NK = a.N * a.K;
   u32x4* buf = lds4 + wave * S::buffer_words;
-  float(*own)[16] = reinterpret_cast<float(*)[16]>(lds4 + kManyWaves * S::buffer_words);
-  float(*extra)[16] = own + kRows + 16 * T;          // [waves][16 T]
+  float(*own)[wide] = reinterpret_cast<float(*)[wide]>(lds4 + kManyWaves * S::buffer_words);
+  float(*extra)[wide] = own + kRows + 16 * T;          // [waves][16 T]
   uint32_t* items = reinterpret_cast<uint32_t*>(extra + kManyWaves * 16 * T);
   uint16_t* pairs = reinterpret_cast<uint16_t*>(items + most_items(a.experts, NK, T));
   uint16_t* place = pairs + 2 * list_words(NK);      // where in the list (token, k) is
@@ -959,7 +1049,7 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
       place[(pair >> kPairShift) * a.K + (pair & ((1 << kPairShift) - 1))] = (uint16_t)at;
     }
   }
-  const int h0 = blockIdx.x * 16, steps = steps_of<F>(a.I);
+  const int h0 = blockIdx.x * wide, steps = steps_of<F>(a.I);
   float out[kOut];
 #pragma unroll
   for (int i = 0; i < kOut; i++) out[i] = 0.f;
@@ -978,7 +1068,7 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
     const int s1 = (int)((int64_t)total * (wave + 1) / kManyWaves);
     if (lane == 0) extra_item[wave] = 0;
     if (s1 > s0) {
-      ManyCursor<F, T> at;
+      ManyCursor<F, RT, T> at;
       at.a = &a, at.items = items, at.pairs = pairs, at.row0 = h0, at.rows = a.H - h0;
       at.steps = steps, at.rot = blockIdx.x + wave;
       at.item = i0 + s0 / steps;
@@ -991,13 +1081,15 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
       S st;
       st.init(a.I, 0);
       st.run(s1 - s0, at, a.I, a.hidden, NK * a.I * 2, buf, [&](int i) {
-        if (i >= s1 - s0 || --left > 0) return;
+        if (--left > 0) return;
         const uint32_t it = uniform(items[item]);
         const int n = it >> 23;
-        float(*to)[16] = whole ? own + ((it >> 10) & 8191) - from : extra + wave * 16 * T;
-        st.values(0, [&](int t, float v) {
-          if (t < n) to[t][lane & 15] = v;
-        });
+        float(*to)[wide] = whole ? own + ((it >> 10) & 8191) - from : extra + wave * 16 * T;
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+          st.values(i, [&](int t, float v) {
+            if (t < n) to[t][i * 16 + (lane & 15)] = v;
+          });
         st.clear();
         whole = true;
         left = ++item < at.last ? steps : at.tail;
@@ -1008,7 +1100,7 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
     const int lo = (items[i0] >> 10) & 8191, hi = ((last >> 10) & 8191) + (last >> 23);
 #pragma unroll
     for (int i = 0; i < kOut; i++) {
-      const int q = threadIdx.x + i * 64 * kManyWaves, t = q >> 4, c = q & 15;
+      const int q = threadIdx.x + i * 64 * kManyWaves, t = q / wide, c = q % wide;
       if (t >= a.N) break;
       for (int k = 0; k < a.K; k++) {
         const int p = place[t * a.K + k];
@@ -1025,7 +1117,7 @@ __global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_k
   }
 #pragma unroll
   for (int i = 0; i < kOut; i++) {
-    const int q = threadIdx.x + i * 64 * kManyWaves, t = q >> 4, c = q & 15;
+    const int q = threadIdx.x + i * 64 * kManyWaves, t = q / wide, c = q % wide;
     if (t < a.N && h0 + c < a.H) a.y[(int64_t)t * a.H + h0 + c] = bf16_bits(out[i]);
   }
 }
@@ -1075,24 +1167,27 @@ void with_part(int cols, Fn&& f) {
 }
 
 template <int F, int T, bool MANY>
-void launch_moe(const MoeArgs& a, hipStream_t st) {
-  constexpr int RT = T == 0 ? 2 : EP_URT, UT = MANY ? EP_UT : T;
-  const dim3 up((a.I + RT * 8 - 1) / (RT * 8), a.experts);
-  const int down = (a.H + 15) / 16;
+void launch_moe(MoeArgs a, hipStream_t st) {
+  constexpr int RT = T == 0 || !Fmt<F>::quant ? 2 : EP_URT, UT = MANY ? EP_UT : T;
+  a.split = EP_KS;
+  const int wide = kUpWaves / a.split * RT * 8;
+  const dim3 up((a.I + wide - 1) / wide, a.experts);
   with_part<F>(a.H, [&](auto part) {
     moe_up_kernel<F, RT, UT, MANY, part.value>
         <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
   });
+  constexpr int DRT = Fmt<F>::quant && T > 0 ? EP_DRT : 1;
+  const int down = (a.H + DRT * 16 - 1) / (DRT * 16);
   with_part<F>(a.I, [&](auto part) {
-    constexpr int words = Stream<F, 1, T, false>::buffer_words;
+    using S = Stream<F, DRT, T, part.value>;
     if constexpr (MANY) {
-      moe_down_many_kernel<F, T, part.value>
-          <<<down, 64 * kManyWaves, many_lds(words, a.N, a.K, a.experts, T), st>>>(a);
+      moe_down_many_kernel<F, DRT, T, part.value><<<
+          down, 64 * kManyWaves, many_lds(S::buffer_words, a.N, a.K, a.experts, DRT, T), st>>>(a);
     } else {
       constexpr int waves = EP_DWAVES;
-      const size_t lds = sizeof(float) * waves * (words * 4 + Stream<F, 1, T, false>::tokens * 16) +
+      const size_t lds = sizeof(float) * waves * (S::buffer_words * 4 + S::tokens * DRT * 16) +
                          (size_t)a.experts * (4 + kFew);
-      moe_down_few_kernel<F, T, part.value><<<down, 64 * waves, lds, st>>>(a);
+      moe_down_few_kernel<F, DRT, T, part.value><<<down, 64 * waves, lds, st>>>(a);
     }
   });
 }
@@ -1156,7 +1251,7 @@ int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* a, void* stream) {
                   (int32_t*)(ws + m.o_expert), (int32_t*)(ws + m.o_count),
                   (int32_t*)(ws + m.o_start), ws + m.o_pairs, (uint16_t*)(ws + m.o_hidden),
                   p->num_tokens, p->hidden, p->num_topk, p->num_experts, a->inter,
-                  p->topk_idx_bytes == 8, m.experts};
+                  p->topk_idx_bytes == 8, m.experts, 0};
   hipStream_t st = (hipStream_t)stream;
   switch (f) {
     case kBf16: return launch_moe<kBf16>(k, st);
