@@ -73,7 +73,13 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 #define EP_DQ 2
 #endif
 #ifndef EP_D1
-#define EP_D1 2
+#define EP_D1 1
+#endif
+#ifndef EP_D1R
+#define EP_D1R 2
+#endif
+#ifndef EP_DMIN
+#define EP_DMIN 192
 #endif
 #ifndef EP_D2
 #define EP_D2 1
@@ -88,7 +94,6 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 #define EP_W1 2
 #endif
 #define EP_UPW(F, T) (T == 0 ? EP_W0 : T == 1 ? EP_W1 : 2)
-#define EP_DNW(F, T) 2
 #ifndef EP_TWO
 #define EP_TWO 64
 #endif
@@ -197,13 +202,16 @@ struct Stream {
   static constexpr int scale_loads = (values_per_row + 3) / 4;    // a value per lane group
   // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's
   // latency, as far as the registers go.
-  static constexpr int depth = M::quant ? (quad ? EP_DQ : TT <= 1 ? EP_D1 : EP_D2)
+  static constexpr int depth = M::quant ? (quad ? EP_DQ : TT > 1 ? EP_D2 : RT == 1 ? EP_D1R : EP_D1)
                                         : (quad ? EP_DB : 2);
-  // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros
+  // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros.
+  // x passes through the same words, and in the end the sums.
   static constexpr int tile_words = 16 * M::chunks;
   static constexpr int scale_words = M::integer ? 16 * scale_loads : 0;
-  static constexpr int x_at = RT * tile_words + scale_words * (M::zeros ? 2 : 1);
-  static constexpr int buffer_words = x_at + (quad ? 0 : 256);
+  static constexpr int results = RT * tokens * 16;                // floats of a wavefront's sums
+  static constexpr int most(int a, int b) { return a > b ? a : b; }
+  static constexpr int buffer_words = most(
+      most(RT * tile_words + scale_words * (M::zeros ? 2 : 1), quad ? 0 : 256), results / 4);
 
   struct Slot {
     u32x4 w[RT][M::loads];                           // as loaded: see load()
@@ -375,7 +383,7 @@ struct Stream {
     constexpr uint32_t kOnes = 0x3F803F80u;
     const u32x4 ones{kOnes, kOnes, kOnes, kOnes};
     constexpr int per = 4 / M::groups;               // MFMAs per group
-    put(b, buf);
+    if constexpr (M::quant) put(b, buf);
     f32x4 sv[M::integer ? scale_loads : 1], zv[M::zeros ? scale_loads : 1];
     if constexpr (M::integer) take_scales(buf + RT * tile_words, sv);
     if constexpr (M::zeros) take_scales(buf + RT * tile_words + scale_words, zv);
@@ -410,16 +418,16 @@ struct Stream {
           for (int j = 0; j < 4; j++) xo[k][j] = b.x[k][m][0];
         } else {
           const int lane = threadIdx.x & 63;
-          u32x4* xb = buf + x_at;
           fence();
 #pragma unroll
           for (int j = 0; j < 4; j++)
-            xb[(j * 4 + (lane >> 4)) * 16 + ((lane & 15) ^ (j * 4 + (lane >> 4)))] = b.x[k][m][j];
+            buf[(j * 4 + (lane >> 4)) * 16 + ((lane & 15) ^ (j * 4 + (lane >> 4)))] = b.x[k][m][j];
           fence();
 #pragma unroll
-          for (int j = 0; j < 4; j++) xo[k][j] = xb[r * 16 + ((M::col(g, j) / 8) ^ r)];
+          for (int j = 0; j < 4; j++) xo[k][j] = buf[r * 16 + ((M::col(g, j) / 8) ^ r)];
         }
       }
+      if constexpr (!M::quant) put(b, buf);
       const auto x = [&](int k, int, int j) { return xo[k][j]; };
       if constexpr (!M::integer) {
 #pragma unroll
@@ -553,7 +561,6 @@ template <int F, int RT, int T, bool PART>
 __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
     const uint16_t* __restrict__ x, Weight w, uint16_t* __restrict__ y, int n, int cols, int rows) {
   using S = Stream<F, RT, T, PART>;
-  __shared__ float red[kLinWaves][RT][S::tokens][16];
   __shared__ u32x4 buf[kLinWaves][S::buffer_words];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int row0 = blockIdx.x * (RT * 16), t0 = blockIdx.y * S::tokens;
@@ -573,15 +580,18 @@ __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
   st.init(cols, 0);
   st.run(share_of(steps_of<F>(cols), wave, kLinWaves), at, cols, x + (int64_t)t0 * cols,
          nt * cols * 2, buf[wave], [](int) {});
+  float* sums = reinterpret_cast<float*>(buf[wave]);         // [RT][tokens][16]
+  S::fence();
 #pragma unroll
   for (int i = 0; i < RT; i++)
-    st.values(i, [&](int t, float v) { red[wave][i][t][lane & 15] = v; });
+    st.values(i, [&](int t, float v) { sums[(i * S::tokens + t) * 16 + (lane & 15)] = v; });
   __syncthreads();
   for (int q = threadIdx.x; q < nt * RT * 16; q += 64 * kLinWaves) {
     const int t = q / (RT * 16), c = q % (RT * 16);
     float v = 0.f;
 #pragma unroll
-    for (int u = 0; u < kLinWaves; u++) v += red[u][c >> 4][t][c & 15];
+    for (int u = 0; u < kLinWaves; u++)
+      v += reinterpret_cast<const float*>(buf[u])[((c >> 4) * S::tokens + t) * 16 + (c & 15)];
     if (row0 + c < rows) y[(int64_t)(t0 + t) * rows + row0 + c] = bf16_bits(v);
   }
 }
@@ -760,11 +770,11 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
 // A workgroup's four wavefronts share 4/split groups of tiles (RT/2 pairs of 16 gate
 // and 16 up rows), split of them the contraction of each.
-// Entries pos0 .. of the expert's list; red[(wave * RT + tile) * tokens + token][row]
+// Entries pos0 .. of the expert's list.
 template <int F, int RT, int T, bool PART>
 __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Gate& gate,
-                                          float (*red)[16], u32x4* buf, const Tiles<F, RT>& tiles,
-                                          int i0, int pos0, int n) {
+                                          u32x4* buf, const Tiles<F, RT>& tiles, int i0, int pos0,
+                                          int n) {
   using S = Stream<F, RT, T, PART>;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = min(n - pos0, S::tokens);
@@ -783,11 +793,12 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
   st.init(a.H, a.I);
   st.run(share_of(steps_of<F>(a.H), at.step, a.split), at, a.H, a.x, a.N * a.H * 2,
          buf + wave * S::buffer_words, [](int) {});
-  if (pos0 > 0) __syncthreads();              // red of the tokens before is consumed
-  else gate.put(a, r);
+  if (pos0 == 0) gate.put(a, r);
+  float* sums = reinterpret_cast<float*>(buf + wave * S::buffer_words);   // [RT][tokens][16]
+  S::fence();
 #pragma unroll
   for (int i = 0; i < RT; i++)
-    st.values(i, [&](int t, float v) { red[(wave * RT + i) * S::tokens + t][lane & 15] = v; });
+    st.values(i, [&](int t, float v) { sums[(i * S::tokens + t) * 16 + (lane & 15)] = v; });
   __syncthreads();
   const int wide = kUpWaves / a.split * RT * 8;      // rows of hidden per workgroup
   for (int q = threadIdx.x; q < nt * wide; q += kUpThreads) {
@@ -795,8 +806,9 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
     const int w0 = c / (RT * 8) * a.split, i = c % (RT * 8) / 16 * 2;
     float g = 0.f, u = 0.f;
     for (int v = w0; v < w0 + a.split; v++) {
-      g += red[(v * RT + i) * S::tokens + t][c & 15];
-      u += red[(v * RT + i + 1) * S::tokens + t][c & 15];
+      const float* part = reinterpret_cast<const float*>(buf + v * S::buffer_words);
+      g += part[(i * S::tokens + t) * 16 + (c & 15)];
+      u += part[((i + 1) * S::tokens + t) * 16 + (c & 15)];
     }
     const int pair = r.pair[pos0 + t];
     // the one rounding between the products: the second one's operand is bf16
@@ -804,6 +816,7 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
       a.hidden[(int64_t)((pair >> kPairShift) * a.K + (pair & ((1 << kPairShift) - 1))) * a.I +
                i0 + c] = bf16_bits(r.weight[pos0 + t] * (silu(g) * u));
   }
+  if (pos0 + S::tokens < n) __syncthreads();    // the next tokens' tiles go where the sums are
 }
 
 // First kernel: blockIdx.x the groups of tiles, blockIdx.y the expert among the
@@ -812,7 +825,6 @@ template <int F, int RT, int T, bool MANY, bool PART>
 __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   __shared__ Routing r;
-  __shared__ float red[kUpWaves * RT * S::tokens][16];
   __shared__ u32x4 buf[kUpWaves * S::buffer_words];
   extern __shared__ int16_t ids[];            // [N*K]
   int n = 0, before = 0, total = 0;
@@ -840,13 +852,13 @@ __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArg
   const int own = i0 + uniform(threadIdx.x >> 6) / a.split * (RT * 8);
   tiles.set(a.w13, (int64_t)e * 2 * a.I + min(own, a.I), a.I - own, a.I, a.H);
   if constexpr (!MANY) {
-    up_tokens<F, RT, T, PART>(a, r, gate, red, buf, tiles, i0, 0, n);
+    up_tokens<F, RT, T, PART>(a, r, gate, buf, tiles, i0, 0, n);
   } else {
     if (T == 1 || n > 16)
       for (int p = 0; p < n; p += 16 * T)
-        up_tokens<F, RT, T, PART>(a, r, gate, red, buf, tiles, i0, p, n);
+        up_tokens<F, RT, T, PART>(a, r, gate, buf, tiles, i0, p, n);
     else
-      up_tokens<F, RT, 1, PART>(a, r, gate, red, buf, tiles, i0, 0, n);
+      up_tokens<F, RT, 1, PART>(a, r, gate, buf, tiles, i0, 0, n);
   }
 }
 
@@ -890,7 +902,7 @@ struct FewCursor {
 };
 
 template <int F, int RT, int T, bool PART>
-__global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs a) {
+__global__ __launch_bounds__(512, 2) void moe_down_few_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   constexpr int wide = RT * 16;               // columns of y per workgroup
   extern __shared__ u32x4 lds4[];
@@ -898,9 +910,7 @@ __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs
   const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   u32x4* buf = lds4 + wave * S::buffer_words;
-  float(*red)[S::tokens][wide] =
-      reinterpret_cast<float(*)[S::tokens][wide]>(lds + waves * S::buffer_words * 4);
-  int32_t* expert = lds + waves * (S::buffer_words * 4 + S::tokens * wide);
+  int32_t* expert = lds + waves * S::buffer_words * 4;
   uint8_t* map = reinterpret_cast<uint8_t*>(expert + a.experts);
   const int active = a.words[1];
   for (int q = threadIdx.x; q < a.experts; q += blockDim.x) expert[q] = a.expert[q];
@@ -922,14 +932,17 @@ __global__ __launch_bounds__(512, EP_DNW(F, T)) void moe_down_few_kernel(MoeArgs
     at.enter();
     st.run(count, at, a.I, a.hidden, a.N * a.K * a.I * 2, buf, [](int) {});
   }
+  float* sums = reinterpret_cast<float*>(buf);               // [tokens][wide]
+  S::fence();
 #pragma unroll
   for (int i = 0; i < RT; i++)
-    st.values(i, [&](int t, float v) { red[wave][t][i * 16 + (lane & 15)] = v; });
+    st.values(i, [&](int t, float v) { sums[t * wide + i * 16 + (lane & 15)] = v; });
   __syncthreads();
   for (int q = threadIdx.x; q < a.N * wide; q += blockDim.x) {
     const int t = q / wide, c = q % wide;
     float v = 0.f;
-    for (int u = 0; u < waves; u++) v += red[u][t][c];
+    for (int u = 0; u < waves; u++)
+      v += reinterpret_cast<const float*>(lds4 + u * S::buffer_words)[t * wide + c];
     if (h0 + c < a.H) a.y[(int64_t)t * a.H + h0 + c] = bf16_bits(v);
   }
 }
@@ -1000,7 +1013,7 @@ size_t many_lds(int buffer_words, int N, int K, int experts, int RT, int T) {
 }
 
 template <int F, int RT, int T, bool PART>
-__global__ __launch_bounds__(64 * kManyWaves, EP_DNW(F, T)) void moe_down_many_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * kManyWaves, 2) void moe_down_many_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   constexpr int wide = RT * 16, kRows = rows_kept(RT);     // columns of y; listed pairs at a time
   constexpr int kOut = EP_MAX_FEW_TOKENS * wide / (64 * kManyWaves);   // results per thread
@@ -1166,9 +1179,26 @@ void with_part(int cols, Fn&& f) {
   else f(std::false_type());
 }
 
+template <int F, int RT, int T, bool MANY>
+void launch_down(const MoeArgs& a, hipStream_t st) {
+  const int grid = (a.H + RT * 16 - 1) / (RT * 16);
+  with_part<F>(a.I, [&](auto part) {
+    using S = Stream<F, RT, T, part.value>;
+    if constexpr (MANY) {
+      moe_down_many_kernel<F, RT, T, part.value><<<
+          grid, 64 * kManyWaves, many_lds(S::buffer_words, a.N, a.K, a.experts, RT, T), st>>>(a);
+    } else {
+      constexpr int waves = EP_DWAVES;
+      const size_t lds = (size_t)waves * S::buffer_words * 16 + (size_t)a.experts * (4 + kFew);
+      moe_down_few_kernel<F, RT, T, part.value><<<grid, 64 * waves, lds, st>>>(a);
+    }
+  });
+}
+
 template <int F, int T, bool MANY>
 void launch_moe(MoeArgs a, hipStream_t st) {
-  constexpr int RT = T == 0 || !Fmt<F>::quant ? 2 : EP_URT, UT = MANY ? EP_UT : T;
+  constexpr bool coarse = F == kMx || Fmt<F>::group == 128;
+  constexpr int RT = T > 0 && Fmt<F>::quant && coarse ? EP_URT : 2, UT = MANY ? EP_UT : T;
   a.split = EP_KS;
   const int wide = kUpWaves / a.split * RT * 8;
   const dim3 up((a.I + wide - 1) / wide, a.experts);
@@ -1176,20 +1206,12 @@ void launch_moe(MoeArgs a, hipStream_t st) {
     moe_up_kernel<F, RT, UT, MANY, part.value>
         <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
   });
-  constexpr int DRT = Fmt<F>::quant && T > 0 ? EP_DRT : 1;
-  const int down = (a.H + DRT * 16 - 1) / (DRT * 16);
-  with_part<F>(a.I, [&](auto part) {
-    using S = Stream<F, DRT, T, part.value>;
-    if constexpr (MANY) {
-      moe_down_many_kernel<F, DRT, T, part.value><<<
-          down, 64 * kManyWaves, many_lds(S::buffer_words, a.N, a.K, a.experts, DRT, T), st>>>(a);
-    } else {
-      constexpr int waves = EP_DWAVES;
-      const size_t lds = sizeof(float) * waves * (S::buffer_words * 4 + S::tokens * DRT * 16) +
-                         (size_t)a.experts * (4 + kFew);
-      moe_down_few_kernel<F, DRT, T, part.value><<<down, 64 * waves, lds, st>>>(a);
-    }
-  });
+  // Codes with one token tile: two row tiles per wavefront halve what x costs, if
+  // the workgroups still fill the GPU (64 tokens, 7168 columns: 115 us against 145;
+  // 13 tokens, 1952 columns: 22.7 against 15.0).
+  if constexpr (T == 1 && Fmt<F>::quant && coarse)
+    if (a.H >= 32 * EP_DMIN) return launch_down<F, 2, T, MANY>(a, st);
+  launch_down<F, 1, T, MANY>(a, st);
 }
 
 template <int F>
@@ -1214,11 +1236,14 @@ int launch_linear(int n, int cols, int rows, const void* x, const Weight& w, voi
   constexpr int B = 64 * kLinWaves;
   with_part<F>(cols, [&](auto part) {
     constexpr bool P = part.value;
+    // groups of 32 and two token tiles: one row tile, or the registers spill
+    constexpr int R2 = Fmt<F>::integer && Fmt<F>::group == 32 ? 1 : RT;
+    const int g2 = (rows + R2 * 16 - 1) / (R2 * 16);
     if (n <= 4) linear_kernel<F, RT, 0, P><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
     else if (n <= 16)
       linear_kernel<F, RT, 1, P><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
     else
-      linear_kernel<F, RT, 2, P><<<dim3(gx, (n + 31) / 32), B, 0, st>>>(xp, w, yp, n, cols, rows);
+      linear_kernel<F, R2, 2, P><<<dim3(g2, (n + 31) / 32), B, 0, st>>>(xp, w, yp, n, cols, rows);
   });
   return check_launch("quant_linear");
 }
