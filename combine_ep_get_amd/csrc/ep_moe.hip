@@ -365,8 +365,12 @@ struct Stream {
   static __device__ __forceinline__ u32x4 operand(uint32_t w, float scale) {
     u32x4 o;
     if constexpr (M::integer) {
+      // one v_and_or each: it takes no literals, and one scalar register at most
+      uint32_t mask = 0x000F000Fu, exponent = 0x43004300u;
+      asm("" : "+v"(mask));
+      asm("" : "+s"(exponent));
 #pragma unroll
-      for (int q = 0; q < 4; q++) o[q] = ((w >> (4 * q)) & 0x000F000Fu) | 0x43004300u;
+      for (int q = 0; q < 4; q++) o[q] = ((w >> (4 * q)) & mask) | exponent;
     } else {
       o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
       o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
@@ -460,18 +464,20 @@ struct Stream {
       } else {
 #pragma unroll
         for (int q = 0; q < M::groups; q++) {
-          f32x4 xs[TT];
+          // without zero points the sums start at -136 sum(x), the same for all tiles
+          f32x4 xs[TT], start[TT];
 #pragma unroll
           for (int k = 0; k < TT; k++) {
             xs[k] = none;
 #pragma unroll
             for (int j = q * per; j < (q + 1) * per; j++) xs[k] = mfma(x(k, m, j), ones, xs[k]);
+            start[k] = M::zeros ? none : xs[k] * -136.f;
           }
 #pragma unroll
           for (int i = 0; i < RT; i++) {
             f32x4 d[TT];
 #pragma unroll
-            for (int k = 0; k < TT; k++) d[k] = none;
+            for (int k = 0; k < TT; k++) d[k] = start[k];
 #pragma unroll
             for (int j = q * per; j < (q + 1) * per; j++) {
               const u32x4 o = weight(i, m, j);
@@ -483,7 +489,8 @@ struct Stream {
             for (int k = 0; k < TT; k++)
 #pragma unroll
               for (int e = 0; e < 4; e++)
-                acc[i][k][e] = fmaf(s, fmaf(-z, xs[k][e], d[k][e]), acc[i][k][e]);
+                acc[i][k][e] = fmaf(s, M::zeros ? fmaf(-z, xs[k][e], d[k][e]) : d[k][e],
+                                    acc[i][k][e]);
           }
         }
       }
