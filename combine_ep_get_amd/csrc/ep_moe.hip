@@ -55,6 +55,8 @@ constexpr int kNonTemporal = 2;            // NT in the cache-policy operand
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// Loads outside [0, bytes) return zeros.  The scalar offset counts as part of what is
+// checked, also where it is behind the end by itself (0 bytes and an offset: all zeros).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kBufferWord3);
 }
@@ -69,49 +71,6 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 }
 
 // ---------------------------------------------------------------- formats
-#ifndef EP_DQ
-#define EP_DQ 2
-#endif
-#ifndef EP_D1
-#define EP_D1 1
-#endif
-#ifndef EP_D1R
-#define EP_D1R 2
-#endif
-#ifndef EP_DMIN
-#define EP_DMIN 192
-#endif
-#ifndef EP_D2
-#define EP_D2 1
-#endif
-#ifndef EP_DB
-#define EP_DB 2
-#endif
-#ifndef EP_W0
-#define EP_W0 3
-#endif
-#ifndef EP_W1
-#define EP_W1 2
-#endif
-#define EP_UPW(F, T) (T == 0 ? EP_W0 : T == 1 ? EP_W1 : 2)
-#ifndef EP_TWO
-#define EP_TWO 64
-#endif
-#ifndef EP_UT
-#define EP_UT 2
-#endif
-#ifndef EP_URT
-#define EP_URT 4
-#endif
-#ifndef EP_DRT
-#define EP_DRT 2
-#endif
-#ifndef EP_KS
-#define EP_KS 4
-#endif
-#ifndef EP_DWAVES
-#define EP_DWAVES 8
-#endif
 // Weight format and group; Z: int4 with zero points.
 enum { kBf16, kMx, kInt128, kInt64, kInt32, kInt128Z, kInt64Z, kInt32Z };
 
@@ -158,8 +117,8 @@ struct Weight {           // kernel argument: ep_weight_t without what the kerne
 // ---------------------------------------------------------------- weight tiles
 // RT tiles of 16 rows: tile i starts at row `row` + i*16, or, where the tiles are
 // pairs of gate and up rows (`far` > 0), at row + (i/2)*16 + (i%2)*far.  `rows` is
-// how many rows there are from `row` on (for pairs: of each kind); those behind are
-// out of range.  The scales of all tiles share one buffer; what it returns for rows
+// how many rows there are from `row` on (for pairs: of each kind; none if negative);
+// those behind are out of range.  The scales of all tiles share one buffer; what it returns for rows
 // that are not there only reaches results that nobody stores.
 template <int F, int RT>
 struct Tiles {
@@ -168,6 +127,7 @@ struct Tiles {
   int bytes[RT], scale_end;
   __device__ __forceinline__ void set(const Weight& w, int64_t row, int rows, int far, int cols) {
     const int rb = row_bytes<F>(cols), rg = row_groups<F>(cols);
+    rows = max(0, rows);
 #pragma unroll
     for (int i = 0; i < RT; i++) {
       const int at = far ? (i >> 1) * 16 : i * 16;
@@ -200,10 +160,12 @@ struct Stream {
   static constexpr int rows = quad ? 1 : 4;                       // loads of x per tile and half
   static constexpr int values_per_row = RT * M::scales;           // scales of a step, all tiles
   static constexpr int scale_loads = (values_per_row + 3) / 4;    // a value per lane group
-  // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's
-  // latency, as far as the registers go.
-  static constexpr int depth = M::quant ? (quad ? EP_DQ : TT > 1 ? EP_D2 : RT == 1 ? EP_D1R : EP_D1)
-                                        : (quad ? EP_DB : 2);
+  // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's latency, as
+  // far as the registers go.  Codes with token tiles have one, where a second step's x
+  // would leave fewer wavefronts (the layer with 4-bit experts: 13 tokens, 1952 x 992:
+  // 32.1 us, with two steps 36.7; 16 tokens, 7168 x 2048: 157 and 162; 64 tokens with
+  // pairs of tiles, which spill then: 245 and 339).
+  static constexpr int depth = M::quant && !quad ? 1 : 2;
   // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros.
   // x passes through the same words, and in the end the sums.
   static constexpr int tile_words = 16 * M::chunks;
@@ -549,15 +511,21 @@ template <int F, int RT, typename S>
 struct Strided {
   Tiles<F, RT> tiles;
   int xoff[S::TT][S::rows];
-  int step, by;
+  int step, by, from, end;                           // behind the last step: from the first again
   bool live;
-  __device__ __forceinline__ void advance() { step += by; }
+  // The wavefront `part` of `of` that share the steps, beginning with its `turn`-th one
+  // (modulo their number, which is returned).
+  __device__ __forceinline__ int share(int steps, int part, int of, int turn) {
+    const int n = part < steps ? (steps - part + of - 1) / of : 0;
+    from = part, by = of, end = steps;
+    step = part + (n ? turn % n * of : 0);
+    return n;
+  }
+  __device__ __forceinline__ void advance() {
+    step += by;
+    if (step >= end) step = from;
+  }
 };
-
-// How many of `steps` a wave takes that starts at `first` and goes on by `by`.
-__device__ __forceinline__ int share_of(int steps, int first, int by) {
-  return first < steps ? (steps - first + by - 1) / by : 0;
-}
 
 // ---------------------------------------------------------------- y = x W^T
 constexpr int kLinWaves = 8;
@@ -581,11 +549,10 @@ __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
       const int t = S::token(k, q);
       at.xoff[k][q] = t < nt ? t * cols * 2 : kAbsent;
     }
-  at.step = wave;
-  at.by = kLinWaves;
+  const int count = at.share(steps_of<F>(cols), wave, kLinWaves, 0);
   S st;
   st.init(cols, 0);
-  st.run(share_of(steps_of<F>(cols), wave, kLinWaves), at, cols, x + (int64_t)t0 * cols,
+  st.run(count, at, cols, x + (int64_t)t0 * cols,
          nt * cols * 2, buf[wave], [](int) {});
   float* sums = reinterpret_cast<float*>(buf[wave]);         // [RT][tokens][16]
   S::fence();
@@ -794,11 +761,15 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
       const int t = S::token(k, q), pair = t < nt ? r.pair[pos0 + t] : -1;
       at.xoff[k][q] = pair >= 0 ? (pair >> kPairShift) * a.H * 2 : kAbsent;
     }
-  at.step = wave & (a.split - 1);
-  at.by = a.split;
+  // Wavefronts at the same columns of rows of 4 KiB or 8 KiB are all in the same few
+  // memory channels, so workgroups start at different ones (64 tokens, bf16, 4096 x 1024:
+  // 265 us, without 294).  Where the wavefronts are apart already it only costs (one
+  // token, 4-bit: 41.4 us, with 42.4).
+  const int turn = a.split < kUpWaves ? blockIdx.x : 0;
+  const int count = at.share(steps_of<F>(a.H), wave & (a.split - 1), a.split, turn);
   S st;
   st.init(a.H, a.I);
-  st.run(share_of(steps_of<F>(a.H), at.step, a.split), at, a.H, a.x, a.N * a.H * 2,
+  st.run(count, at, a.H, a.x, a.N * a.H * 2,
          buf + wave * S::buffer_words, [](int) {});
   if (pos0 == 0) gate.put(a, r);
   float* sums = reinterpret_cast<float*>(buf + wave * S::buffer_words);   // [RT][tokens][16]
@@ -829,7 +800,7 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
 // First kernel: blockIdx.x the groups of tiles, blockIdx.y the expert among the
 // active ones.  T: token tiles per pass; 0 and 1 without MANY: few tokens.
 template <int F, int RT, int T, bool MANY, bool PART>
-__global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kUpThreads, T == 0 ? 3 : 2) void moe_up_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   __shared__ Routing r;
   __shared__ u32x4 buf[kUpWaves * S::buffer_words];
@@ -875,6 +846,10 @@ __global__ __launch_bounds__(kUpThreads, EP_UPW(F, T)) void moe_up_kernel(MoeArg
 // added in the wavefronts' order: no atomics, the same sums on every run.
 
 // Few: token rows are the same for every expert, the accumulators go through.
+// 16 wavefronts where there are fewer than 256 workgroups: no faster (1952 columns,
+// 13 tokens: 35.4 us for the layer, with eight 34.8).
+constexpr int kFewWaves = 8;
+
 template <int F, int RT, typename S>
 struct FewCursor {
   const MoeArgs* a;
@@ -909,15 +884,14 @@ struct FewCursor {
 };
 
 template <int F, int RT, int T, bool PART>
-__global__ __launch_bounds__(512, 2) void moe_down_few_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves, 2) void moe_down_few_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   constexpr int wide = RT * 16;               // columns of y per workgroup
   extern __shared__ u32x4 lds4[];
   int32_t* lds = reinterpret_cast<int32_t*>(lds4);
-  const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   u32x4* buf = lds4 + wave * S::buffer_words;
-  int32_t* expert = lds + waves * S::buffer_words * 4;
+  int32_t* expert = lds + kFewWaves * S::buffer_words * 4;
   uint8_t* map = reinterpret_cast<uint8_t*>(expert + a.experts);
   const int active = a.words[1];
   for (int q = threadIdx.x; q < a.experts; q += blockDim.x) expert[q] = a.expert[q];
@@ -926,8 +900,8 @@ __global__ __launch_bounds__(512, 2) void moe_down_few_kernel(MoeArgs a) {
   __syncthreads();
   const int h0 = blockIdx.x * wide, steps = steps_of<F>(a.I);
   const int total = uniform(active) * steps;
-  const int first = (int)((int64_t)total * wave / waves);
-  const int count = (int)((int64_t)total * (wave + 1) / waves) - first;
+  const int first = (int)((int64_t)total * wave / kFewWaves);
+  const int count = (int)((int64_t)total * (wave + 1) / kFewWaves) - first;
   FewCursor<F, RT, S> at;
   at.a = &a, at.expert = expert, at.map = map, at.row0 = h0, at.rows = a.H - h0;
   at.j = first / steps, at.n = first % steps, at.steps = steps;
@@ -948,7 +922,7 @@ __global__ __launch_bounds__(512, 2) void moe_down_few_kernel(MoeArgs a) {
   for (int q = threadIdx.x; q < a.N * wide; q += blockDim.x) {
     const int t = q / wide, c = q % wide;
     float v = 0.f;
-    for (int u = 0; u < waves; u++)
+    for (int u = 0; u < kFewWaves; u++)
       v += reinterpret_cast<const float*>(lds4 + u * S::buffer_words)[t * wide + c];
     if (h0 + c < a.H) a.y[(int64_t)t * a.H + h0 + c] = bf16_bits(v);
   }
@@ -1195,20 +1169,34 @@ void launch_down(const MoeArgs& a, hipStream_t st) {
       moe_down_many_kernel<F, RT, T, part.value><<<
           grid, 64 * kManyWaves, many_lds(S::buffer_words, a.N, a.K, a.experts, RT, T), st>>>(a);
     } else {
-      constexpr int waves = EP_DWAVES;
-      const size_t lds = (size_t)waves * S::buffer_words * 16 + (size_t)a.experts * (4 + kFew);
-      moe_down_few_kernel<F, RT, T, part.value><<<grid, 64 * waves, lds, st>>>(a);
+      const size_t lds = (size_t)kFewWaves * S::buffer_words * 16 + (size_t)a.experts * (4 + kFew);
+      moe_down_few_kernel<F, RT, T, part.value><<<grid, 64 * kFewWaves, lds, st>>>(a);
     }
   });
 }
 
+// T: token tiles per item of the second product.  The first one takes pairs of tiles
+// for longer lists, its registers allow it (4-bit, 64 tokens: 245 us for the layer,
+// with single tiles 308), and single ones where no list is longer than 16.
 template <int F, int T, bool MANY>
 void launch_moe(MoeArgs a, hipStream_t st) {
-  constexpr bool coarse = F == kMx || Fmt<F>::group == 128;
-  constexpr int RT = T > 0 && Fmt<F>::quant && coarse ? EP_URT : 2, UT = MANY ? EP_UT : T;
-  a.split = EP_KS;
-  const int wide = kUpWaves / a.split * RT * 8;
-  const dim3 up((a.I + wide - 1) / wide, a.experts);
+  constexpr bool quant = Fmt<F>::quant, coarse = F == kMx || Fmt<F>::group == 128;
+  // Codes with token tiles: four row tiles per wavefront, which read x half as often
+  // as two do (64 tokens 238 us for the layer, with two 262; 16 tokens 156 and 167).
+  // Finer integer groups with their scales and zeros have no registers for that.
+  constexpr int RT = T > 0 && coarse && quant ? 4 : 2, UT = MANY ? 2 : T;
+  // A workgroup's four wavefronts share one contraction, which keeps the latency of
+  // few tokens short (one token, 4-bit: 41.4 us, two on each 42.0, one on each 48.2).
+  // For longer lists less splitting is better where that leaves a workgroup per CU:
+  // the wavefronts meet at the same columns of x in L1, and the list is made for more
+  // rows.  256 tokens, bf16, 7168 x 2048: 467 us with four on each, 455 with two, 456
+  // with one; 64 tokens, 4-bit, 4096 x 1024: 121, 114, 113; but 64 tokens, 2048 x 256,
+  // 16 experts: 25.7, 30.5, 40.4.
+  const auto groups = [&](int split) { return (a.I + kUpWaves / split * RT * 8 - 1) /
+                                              (kUpWaves / split * RT * 8); };
+  constexpr int apart = quant ? 1 : 2;
+  a.split = MANY && groups(apart) * a.experts >= 256 ? apart : kUpWaves;
+  const dim3 up(groups(a.split), a.experts);
   with_part<F>(a.H, [&](auto part) {
     moe_up_kernel<F, RT, UT, MANY, part.value>
         <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
@@ -1216,8 +1204,8 @@ void launch_moe(MoeArgs a, hipStream_t st) {
   // Codes with one token tile: two row tiles per wavefront halve what x costs, if
   // the workgroups still fill the GPU (64 tokens, 7168 columns: 115 us against 145;
   // 13 tokens, 1952 columns: 22.7 against 15.0).
-  if constexpr (T == 1 && Fmt<F>::quant && coarse)
-    if (a.H >= 32 * EP_DMIN) return launch_down<F, 2, T, MANY>(a, st);
+  if constexpr (T == 1 && quant && coarse)
+    if (a.H >= 32 * 192) return launch_down<F, 2, T, MANY>(a, st);
   launch_down<F, 1, T, MANY>(a, st);
 }
 
@@ -1227,7 +1215,11 @@ int launch_moe(const MoeArgs& a, hipStream_t st) {
   EP_LOG("moe: N=%d H=%d I=%d E=%d K=%d", a.N, a.H, a.I, a.E, a.K);
   if (a.N <= 4) launch_moe<F, 0, false>(a, st);
   else if (a.N <= kFew) launch_moe<F, 1, false>(a, st);
-  else if (pairs <= EP_TWO * a.E) launch_moe<F, 1, true>(a, st);
+  // Up to 64 tokens per expert if they were spread evenly: items of 16 for the second
+  // product, which most lists fit (256 tokens, 8 of 256 experts, 32 of them here, bf16:
+  // 455 us, with items of 32 500); longer lists would read the weights too often (64
+  // tokens to each of 64 experts, 2048 x 1024, 4-bit: 281 us with items of 16, 271).
+  else if (pairs <= 64 * a.E) launch_moe<F, 1, true>(a, st);
   else launch_moe<F, 2, true>(a, st);
   return check_launch("moe_layer");
 }

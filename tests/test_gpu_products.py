@@ -128,6 +128,22 @@ def test_layer_many_tokens_of_one_expert(fmt, group, N, n):
     held(layer(x, idx, wts, w13, w2), *ref.moe(x, idx, wts, w13, w2))
 
 
+@pytest.mark.parametrize("fmt,group,zeros,H,I", [
+    ("bf16", None, False, 40, 8), ("bf16", None, False, 264, 72), ("mxfp4", 32, False, 32, 32),
+    ("mxfp4", 32, False, 288, 160), ("int4", 128, False, 384, 128), ("int4", 32, True, 96, 64)])
+@pytest.mark.parametrize("N", [17, 70])
+def test_layer_many_experts(fmt, group, zeros, H, I, N):
+    """Enough experts for a workgroup on every CU: no contraction is shared out then."""
+    gen = torch.Generator().manual_seed(N + I)
+    E = 300
+    w13 = ref.W(fmt, (E,), 2 * I, H, group, zeros, gen)
+    w2 = ref.W(fmt, (E,), H, I, group, zeros, gen)
+    x, idx, wts = inputs(N, H, E, 18, gen)
+    idx[1] = E - 1                      # the last expert, named by every choice of a token
+    idx[: N // 2, 3] = 7
+    held(layer(x, idx, wts, w13, w2), *ref.moe(x, idx, wts, w13, w2))
+
+
 def small(seed=3, N=9, H=128, I=64, E=6, K=3, fmt="bf16"):
     gen = torch.Generator().manual_seed(seed)
     group = None if fmt == "bf16" else 32
