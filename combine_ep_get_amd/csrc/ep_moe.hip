@@ -800,7 +800,7 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
 // First kernel: blockIdx.x the groups of tiles, blockIdx.y the expert among the
 // active ones.  T: token tiles per pass; 0 and 1 without MANY: few tokens.
 template <int F, int RT, int T, bool MANY, bool PART>
-__global__ __launch_bounds__(kUpThreads, T == 0 ? 3 : 2) void moe_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kUpThreads, T == 0 && F != kInt32Z ? 3 : 2) void moe_up_kernel(MoeArgs a) {
   using S = Stream<F, RT, T, PART>;
   __shared__ Routing r;
   __shared__ u32x4 buf[kUpWaves * S::buffer_words];
@@ -1220,7 +1220,9 @@ int launch_moe(const MoeArgs& a, hipStream_t st) {
   // 455 us, with items of 32 500); longer lists would read the weights too often (64
   // tokens to each of 64 experts, 2048 x 1024, 4-bit: 281 us with items of 16, 271).
   else if (pairs <= 64 * a.E) launch_moe<F, 1, true>(a, st);
-  else launch_moe<F, 2, true>(a, st);
+  // Groups of 32 with zero points would spill with two token tiles (256 tokens, 16
+  // experts: 410 us against 333).
+  else launch_moe<F, F == kInt32Z ? 1 : 2, true>(a, st);
   return check_launch("moe_layer");
 }
 
