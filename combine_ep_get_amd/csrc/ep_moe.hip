@@ -840,6 +840,9 @@ __global__ __launch_bounds__(kUpThreads, T == 0 && F != kInt32Z ? 3 : 2) void mo
   }
 }
 
+// No tokens: only what the workspace says about the routing.
+__global__ void moe_none_kernel(int32_t* words) { words[0] = words[1] = 0; }
+
 // ---- second product.  One workgroup owns RT*16 columns of y and walks the active
 // experts; its wavefronts share the steps of all of them evenly, one stream of
 // loads each that does not stop between experts.  The parts meet in LDS and are
@@ -1269,16 +1272,20 @@ int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* a, void* stream) {
                             !a->y || ((uintptr_t)a->y & 1)))
     return EP_ERR_INVALID_ARG;
   rc = check_device();
-  if (rc != EP_OK || p->num_tokens == 0) return rc;
+  if (rc != EP_OK) return rc;
   const MoePlan m = make_moe_plan(p, a->inter);
   char* ws = (char*)a->workspace;
+  hipStream_t st = (hipStream_t)stream;
+  if (p->num_tokens == 0) {
+    moe_none_kernel<<<1, 1, 0, st>>>((int32_t*)ws);
+    return check_launch("moe_layer");
+  }
   const MoeArgs k{(const uint16_t*)a->x, a->topk_idx, a->topk_weights, kernel_weight(a->w13),
                   kernel_weight(a->w2), (uint16_t*)a->y, (int32_t*)ws,
                   (int32_t*)(ws + m.o_expert), (int32_t*)(ws + m.o_count),
                   (int32_t*)(ws + m.o_start), ws + m.o_pairs, (uint16_t*)(ws + m.o_hidden),
                   p->num_tokens, p->hidden, p->num_topk, p->num_experts, a->inter,
                   p->topk_idx_bytes == 8, m.experts, 0};
-  hipStream_t st = (hipStream_t)stream;
   switch (f) {
     case kBf16: return launch_moe<kBf16>(k, st);
     case kInt128: return launch_moe<kInt128>(k, st);
@@ -1298,8 +1305,12 @@ int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void
     return EP_ERR_INVALID_ARG;
   const int f = format_of(*w, cols);
   if (f < 0 || f == kBf16) return EP_ERR_INVALID_ARG;
-  if (num_rows > 0 && (!x || ((uintptr_t)x & 15) || !y || ((uintptr_t)y & 1)))
-    return EP_ERR_INVALID_ARG;
+  if (num_rows > 0) {
+    if (!x || ((uintptr_t)x & 15) || !y || ((uintptr_t)y & 1)) return EP_ERR_INVALID_ARG;
+    const uintptr_t x0 = (uintptr_t)x, y0 = (uintptr_t)y;
+    if (x0 < y0 + (size_t)num_rows * out_rows * 2 && y0 < x0 + (size_t)num_rows * cols * 2)
+      return EP_ERR_INVALID_ARG;         // workgroups read x while others write y
+  }
   const int rc = check_device();
   if (rc != EP_OK || num_rows == 0) return rc;
   const Weight k = kernel_weight(*w);

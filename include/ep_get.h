@@ -382,14 +382,15 @@ typedef struct ep_weight {
  * and combine:
  *   y[t] = sum over k with 0 <= topk_idx[t][k] < E of topk_weights[t][k] *
  *          W2_e ( silu(Wg_e x[t]) * (Wu_e x[t]) ),  e = topk_idx[t][k]
- * Only the experts that some token names are read, each once per 64 of its
- * tokens.  Products accumulate in float32; weight * silu * up is rounded to bf16
+ * Only the experts that some token names are read, each once per 16 or 32 of
+ * its tokens.  Products accumulate in float32; weight * silu * up is rounded to bf16
  * once, as the input of the second product, and y once.  A token without
  * experts gets zeros; an expert named twice by one token counts with the sum
  * of its weights.  Ids outside [-1, E) are skipped and flagged as by
  * ep_get_layout (ep_layout_error on `workspace`).  Deterministic.
- * x, weights and topk_weights are finite, |x| and the values before the second
- * product below 2^119 with EP_WEIGHT_INT4.
+ * Weights are finite, x and topk_weights too, |x| and the values before the
+ * second product below 2^119 with EP_WEIGHT_INT4; what a token has beyond that
+ * stays in its own row of y.
  *   p          num_tokens 0..EP_MAX_FEW_TOKENS, hidden, num_topk, num_experts,
  *              topk_idx_bytes; num_ranks, expert_alignment, use_fp8 and
  *              cu_budget are only checked
@@ -398,7 +399,7 @@ typedef struct ep_weight {
  *   w2         [E][hidden][inter], in the same format and group as w13
  *   inter      % 8 == 0 (bf16) or % group == 0; hidden and inter at most
  *              EP_MAX_CONTRACTION
- *   y          [N][hidden] bf16 out
+ *   y          [N][hidden] bf16 out; may be x
  *   workspace  ep_moe_workspace_bytes, 256-byte aligned; no initialisation;
  *              calls that overlap need their own */
 typedef struct ep_moe_args {
@@ -418,8 +419,9 @@ int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* args, void* stream)
  *   x [num_rows][cols] bf16 (16-byte aligned), w [out_rows][cols],
  *   y [num_rows][out_rows] bf16; num_rows 0..EP_MAX_FEW_TOKENS, cols at most
  *   EP_MAX_CONTRACTION, out_rows 1..EP_MAX_HIDDEN.
- * float32 accumulation, one rounding.  x finite, below 2^119 with
- * EP_WEIGHT_INT4.  Deterministic. */
+ * y must not overlap x.  float32 accumulation, one rounding.  Weights are finite,
+ * x too, |x| below 2^119 with EP_WEIGHT_INT4; what a row has beyond that stays in
+ * its own row of y.  Deterministic. */
 int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void* x,
                     const ep_weight_t* w, void* y, void* stream);
 

@@ -144,6 +144,27 @@ def test_layer_many_experts(fmt, group, zeros, H, I, N):
     held(layer(x, idx, wts, w13, w2), *ref.moe(x, idx, wts, w13, w2))
 
 
+@pytest.mark.parametrize("fmt,group", [("bf16", None), ("int4", 32), ("mxfp4", 32)])
+@pytest.mark.parametrize("E", [1024, 40])
+def test_layer_most_pairs(fmt, group, E):
+    """The largest batch, 32 choices each: of the most experts, and of a few."""
+    gen = torch.Generator().manual_seed(E)
+    N, H, I, K = 256, 64, 32, 32
+    w13 = ref.W(fmt, (E,), 2 * I, H, group, False, gen)
+    w2 = ref.W(fmt, (E,), H, I, group, False, gen)
+    x, idx, wts = inputs(N, H, E, K, gen, absent=0.0)
+    held(layer(x, idx, wts, w13, w2), *ref.moe(x, idx, wts, w13, w2))
+
+
+def test_layer_in_place():
+    for N in (2, 12, 50):
+        x, idx, wts, w13, w2 = small(N=N)
+        want = layer(x, idx, wts, w13, w2)
+        y = x.cuda()
+        assert ep.moe_layer(y, idx.cuda(), wts.cuda(), w13.arg, w2.arg, out=y) is y
+        assert torch.equal(y, want)
+
+
 def small(seed=3, N=9, H=128, I=64, E=6, K=3, fmt="bf16"):
     gen = torch.Generator().manual_seed(seed)
     group = None if fmt == "bf16" else 32
@@ -157,6 +178,10 @@ def test_layer_no_tokens_no_experts():
                      torch.empty((0, 3), dtype=torch.int32, device="cuda"),
                      torch.empty((0, 3), device="cuda"), w13.arg, w2.arg)
     assert y.shape == (0, 128)
+    ws = torch.full((ep.moe_workspace_bytes(0, 3, 6, 128, 64),), 255, dtype=torch.uint8,
+                    device="cuda")
+    layer(x[:0], idx[:0], wts[:0], w13, w2, workspace=ws)
+    assert ep.moe_error(ws) == 0
     for n in (1, 9):                    # nobody names an expert: zeros, whatever was there
         y = torch.full((n, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
         layer(x[:n], torch.full_like(idx[:n], -1), torch.full_like(wts[:n], float("nan")), w13, w2,

@@ -8,6 +8,7 @@ import torch
 import combine_ep_get_amd as ep
 
 FAKE = 256          # never dereferenced: every call here is rejected
+FAR = 1 << 30
 
 
 def route_args(**kw):
@@ -98,12 +99,15 @@ def test_workspace_bytes():
 
 
 @pytest.mark.parametrize("n,cols,rows,w,x,y", [
-    (-1, 128, 16, weight(INT4, 128), FAKE, FAKE), (257, 128, 16, weight(INT4, 128), FAKE, FAKE),
-    (1, 0, 16, weight(INT4, 128), FAKE, FAKE), (1, 192, 16, weight(INT4, 128), FAKE, FAKE),
-    (1, 65664, 16, weight(INT4, 128), FAKE, FAKE), (1, 128, 0, weight(INT4, 128), FAKE, FAKE),
-    (1, 128, (1 << 24) + 1, weight(INT4, 128), FAKE, FAKE), (1, 128, 16, weight(), FAKE, FAKE),
-    (1, 128, 16, weight(INT4, 128), None, FAKE), (1, 128, 16, weight(INT4, 128), FAKE, None),
-    (1, 128, 16, weight(INT4, 128), FAKE + 2, FAKE), (1, 48, 16, weight(MX, 32), FAKE, FAKE)],
+    (-1, 128, 16, weight(INT4, 128), FAKE, FAR), (257, 128, 16, weight(INT4, 128), FAKE, FAR),
+    (1, 0, 16, weight(INT4, 128), FAKE, FAR), (1, 192, 16, weight(INT4, 128), FAKE, FAR),
+    (1, 65664, 16, weight(INT4, 128), FAKE, FAR), (1, 128, 0, weight(INT4, 128), FAKE, FAR),
+    (1, 128, (1 << 24) + 1, weight(INT4, 128), FAKE, FAR), (1, 128, 16, weight(), FAKE, FAR),
+    (1, 128, 16, weight(INT4, 128), None, FAR), (1, 128, 16, weight(INT4, 128), FAKE, None),
+    (1, 128, 16, weight(INT4, 128), FAKE + 2, FAR), (1, 48, 16, weight(MX, 32), FAKE, FAR),
+    # y over x: the same, its end over x's start, its start over x's end
+    (4, 128, 16, weight(INT4, 128), FAKE, FAKE), (4, 128, 16, weight(INT4, 128), FAR, FAR - 126),
+    (4, 128, 16, weight(INT4, 128), FAR, FAR + 1022)],
     ids=str)
 def test_linear_refuses(n, cols, rows, w, x, y):
     assert ep.lib().ep_quant_linear(n, cols, rows, x, ctypes.byref(w), y, None) == 1
