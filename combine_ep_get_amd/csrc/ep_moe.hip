@@ -96,6 +96,8 @@ struct Fmt {
   static constexpr int groups = quant ? 128 / group : 1;    // scales per half
   static constexpr int scales = quant ? step / group : 0;   // scales of a row per step
   static constexpr int scale_bytes = F == kMx ? 1 : 2;
+  // steps whose scales of a row are 16 bytes (their zeros 8)
+  static constexpr int chunk = quant ? 16 / (scales * scale_bytes) : 1;
 };
 
 // Bytes of a row of codes (or bf16 values), and its number of groups.
@@ -146,10 +148,15 @@ struct Tiles {
 
 // ---------------------------------------------------------------- the stream
 // RT weight tiles times T token tiles of 16 (T == 0: Quad, up to 4 tokens); PART: the
-// last step has fewer columns.
+// last step may have fewer columns, the last chunk fewer steps.
 //
-// Where the steps come from is the caller's cursor: `step` (which columns),
-// `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row
+// Scales come 16 bytes of a row at a time, for Fmt::chunk steps (PART: value by value
+// at every step).  A load of them touches as many lines as four of codes do: 64 tokens,
+// 4-bit, 7168 x 2048: 214 us for the layer, with one for every step 236; one row
+// by 7168 x 7168 of mxfp4, which has eight scales a step: 7.9 us, value by value 10.1.
+//
+// Where the steps come from is the caller's cursor: `step` (which columns), `serial`
+// (another one for every run of steps inside a chunk and the same tiles), `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row
 // of x of token(k, j) in bytes, kAbsent for none) and advance().
 template <int F, int RT, int T, bool PART>
 struct Stream {
@@ -169,7 +176,12 @@ struct Stream {
   // 16-byte words of LDS per wavefront: the tiles of a step, then scales and zeros.
   // x passes through the same words, and in the end the sums.
   static constexpr int tile_words = 16 * M::chunks;
-  static constexpr int scale_words = M::integer ? 16 * scale_loads : 0;
+  // Scales by chunks?  Not where it gains nothing: Quad has one load per step either way
+  // with groups of 128 (one token: 41.4 us, by chunks 44.2); nor where the registers are
+  // out: 352 bytes spilled, 256 tokens 529 us against 333.
+  static constexpr bool wide =
+      M::quant && !PART && !(quad && M::group == 128) && !(F == kInt32Z && TT > 1);
+  static constexpr int scale_words = M::integer ? 16 * scale_loads : wide ? 8 * RT : 0;
   static constexpr int results = RT * tokens * 16;                // floats of a wavefront's sums
   static constexpr int most(int a, int b) { return a > b ? a : b; }
   static constexpr int buffer_words = most(
@@ -177,7 +189,10 @@ struct Stream {
 
   struct Slot {
     u32x4 w[RT][M::loads];                           // as loaded: see load()
-    uint32_t s[M::quant ? scale_loads : 1], z[M::zeros ? scale_loads : 1];
+    uint32_t s[M::quant && !wide ? scale_loads : 1], z[M::zeros && !wide ? scale_loads : 1];
+    u32x4 sc;                                        // wide: the chunk of row lane & 15 of
+    u32x2 zc;                                        // tile lane >> 4
+    int serial, step;
     u32x4 x[TT][M::halves][quad ? 1 : 4];            // as loaded (Quad: the MFMA operand)
   };
 
@@ -186,7 +201,7 @@ struct Stream {
   // holds weight row r of tokens g*4 .. g*4+3.
   f32x4 acc[RT][quad ? 4 : TT];
   // The lane's offsets: loads of the tiles, of the scales (in values), of x.
-  int woff[M::loads], soff[M::quant ? scale_loads : 1], xcol;
+  int woff[M::loads], soff[M::quant && !wide ? scale_loads : 1], xcol;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -203,7 +218,10 @@ struct Stream {
 #pragma unroll
     for (int q = 0; q < M::loads; q++)
       woff[q] = (q * (64 / M::chunks) + lane / M::chunks) * rb + (lane & (M::chunks - 1)) * 16;
-    if constexpr (M::quant) {
+    if constexpr (wide) {
+      const int row = r + (far ? (g >> 1) * 16 + (g & 1) * far : g * 16);
+      soff[0] = g < RT ? row * rg : kOutside / 2;
+    } else if constexpr (M::quant) {
 #pragma unroll
       for (int q = 0; q < scale_loads; q++) {        // lane group g has value q*4 + g of its row
         const int v = q * 4 + g, i = v / M::scales;
@@ -228,7 +246,21 @@ struct Stream {
         b.w[i][q] = __builtin_amdgcn_raw_buffer_load_b128(rs, woff[q], step * (M::chunks * 16),
                                                           kNonTemporal);
     }
-    if constexpr (M::quant) {
+    if constexpr (wide) {
+      b.step = step;
+      // Quad: at every step, as a load that may not be there would have the other
+      // step's wait include it
+      if (quad || (at.live && b.serial != at.serial)) {
+        b.serial = at.serial;
+        const int c = (uint32_t)step / M::chunk;
+        b.sc = __builtin_amdgcn_raw_buffer_load_b128(
+            buffer(at.tiles.scale, at.live ? at.tiles.scale_end * M::scale_bytes : 0), soff[0] * M::scale_bytes,
+            c * 16, 0);
+        if constexpr (M::zeros)
+          b.zc = __builtin_amdgcn_raw_buffer_load_b64(buffer(at.tiles.zero, at.live ? at.tiles.scale_end : 0),
+                                                      soff[0], c * 8, 0);
+      }
+    } else if constexpr (M::quant) {
       const int n = at.live ? at.tiles.scale_end : 0;
       const auto ss = buffer(at.tiles.scale, n * M::scale_bytes);
 #pragma unroll
@@ -283,13 +315,40 @@ struct Stream {
       for (int q = 0; q < M::loads; q++)
         buf[i * tile_words +
             place(q * (64 / M::chunks) + lane / M::chunks, lane & (M::chunks - 1))] = b.w[i][q];
-    if constexpr (M::integer) {
-      // [load][row][lane group]
-      float* sb = reinterpret_cast<float*>(buf + RT * tile_words);
+    if constexpr (wide) {
+      // of each row: its values of all tiles
+      const int in = (uint32_t)b.step % M::chunk;    // step of the chunk
+      if (g < RT) {
+        if constexpr (!M::integer) {
+          reinterpret_cast<u32x2*>(buf + RT * tile_words)[r * RT + g] =
+              in ? u32x2{b.sc[2], b.sc[3]} : u32x2{b.sc[0], b.sc[1]};
+        } else {
+          float* sb = reinterpret_cast<float*>(buf + RT * tile_words) + r * 4 * scale_loads +
+                      g * M::scales;
+          uint32_t v[M::scales / 2];                 // pairs of bf16
+#pragma unroll
+          for (int q = 0; q < M::scales / 2; q++) {
+            v[q] = b.sc[q];
+#pragma unroll
+            for (int c = 1; c < M::chunk; c++)
+              if (in == c) v[q] = b.sc[c * (M::scales / 2) + q];
+            sb[q * 2] = __uint_as_float(v[q] << 16);
+            sb[q * 2 + 1] = __uint_as_float(v[q] & 0xFFFF0000u);
+          }
+          if constexpr (M::zeros) {
+            float* zb = sb + scale_words * 4;
+            const uint64_t z = ((uint64_t)b.zc.y << 32 | b.zc.x) >> (in * M::scales * 8);
+#pragma unroll
+            for (int q = 0; q < M::scales; q++) zb[q] = 128.f + (float)(uint8_t)(z >> (q * 8));
+          }
+        }
+      }
+    } else if constexpr (M::integer) {
+      float* sb = reinterpret_cast<float*>(buf + RT * tile_words) + r * 4 * scale_loads + g;
 #pragma unroll
       for (int q = 0; q < scale_loads; q++) {
-        sb[q * 64 + r * 4 + g] = __uint_as_float(b.s[q] << 16);
-        if constexpr (M::zeros) sb[(scale_loads + q) * 64 + r * 4 + g] = 128.f + (float)b.z[q];
+        sb[q * 4] = __uint_as_float(b.s[q] << 16);
+        if constexpr (M::zeros) sb[scale_words * 4 + q * 4] = 128.f + (float)b.z[q];
       }
     }
     fence();
@@ -299,7 +358,8 @@ struct Stream {
   static __device__ __forceinline__ void take_scales(const u32x4* at, f32x4* v) {
     const int r = threadIdx.x & 15;
 #pragma unroll
-    for (int q = 0; q < scale_loads; q++) v[q] = reinterpret_cast<const f32x4*>(at)[q * 16 + r];
+    for (int q = 0; q < scale_loads; q++)
+      v[q] = reinterpret_cast<const f32x4*>(at)[r * scale_loads + q];
   }
 
   // Half m of tile i: the four words of codes for the MFMAs.
@@ -353,6 +413,12 @@ struct Stream {
     f32x4 sv[M::integer ? scale_loads : 1], zv[M::zeros ? scale_loads : 1];
     if constexpr (M::integer) take_scales(buf + RT * tile_words, sv);
     if constexpr (M::zeros) take_scales(buf + RT * tile_words + scale_words, zv);
+    u32x2 mx[wide && !M::integer ? RT : 1];          // the row's eight scales, by tile
+    if constexpr (wide && !M::integer) {
+#pragma unroll
+      for (int i = 0; i < RT; i++)
+        mx[i] = reinterpret_cast<const u32x2*>(buf + RT * tile_words)[r * RT + i];
+    }
     u32x4 codes[RT][M::halves];
     if constexpr (M::quant) {
 #pragma unroll
@@ -362,9 +428,11 @@ struct Stream {
     }
     const auto weight = [&](int i, int m, int j) {   // operand of MFMA j
       if constexpr (!M::quant) return buf[i * tile_words + place(r, j * 4 + g)];
-      // mxfp4: the lane group that loaded a scale is the one whose codes it scales
+      // mxfp4: lane group g's codes are under the half's scale g (PART: which it loaded)
       else return operand(codes[i][m][j],
-                          M::integer ? 0.f : __uint_as_float(b.s[i * M::halves + m] << 23));
+                          M::integer ? 0.f
+                          : wide ? __uint_as_float(__builtin_amdgcn_ubfe(mx[i][m], g * 8, 8) << 23)
+                                 : __uint_as_float(b.s[i * M::halves + m] << 23));
     };
     const auto scale = [&](int i, int m, int q) {
       const int v = i * M::scales + m * M::groups + q;
@@ -466,6 +534,7 @@ struct Stream {
     Slot slot[depth];
 #pragma unroll
     for (int d = 0; d < depth; d++) {
+      slot[d].serial = -1;
       at.live = d < count;
       load(slot[d], at, cols, x, xbytes);
       at.advance();
@@ -511,7 +580,7 @@ template <int F, int RT, typename S>
 struct Strided {
   Tiles<F, RT> tiles;
   int xoff[S::TT][S::rows];
-  int step, by, from, end;                           // behind the last step: from the first again
+  int step, by, from, end, serial;                   // behind the last step: from the first again
   bool live;
   // The wavefront `part` of `of` that share the steps, beginning with its `turn`-th one
   // (modulo their number, which is returned).
@@ -519,10 +588,12 @@ struct Strided {
     const int n = part < steps ? (steps - part + of - 1) / of : 0;
     from = part, by = of, end = steps;
     step = part + (n ? turn % n * of : 0);
+    serial = 0;
     return n;
   }
   __device__ __forceinline__ void advance() {
     step += by;
+    if (by > 1 || (uint32_t)step % Fmt<F>::chunk == 0 || step >= end) serial++;
     if (step >= end) step = from;
   }
 };
@@ -859,7 +930,7 @@ struct FewCursor {
   const int32_t* expert;                  // LDS
   const uint8_t* map;                     // LDS [experts][16]
   int64_t row0;
-  int rows, j, step, steps, n, rot;
+  int rows, j, step, steps, n, rot, serial;
   Tiles<F, RT> tiles;
   int xoff[1][S::rows];
   bool live;
@@ -875,6 +946,7 @@ struct FewCursor {
   __device__ __forceinline__ void turn() {
     step = n + rot;
     if (step >= steps) step -= steps;
+    if (n == 0 || (uint32_t)step % Fmt<F>::chunk == 0) serial++;
   }
   __device__ __forceinline__ void advance() {
     if (++n == steps) {
@@ -908,6 +980,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void moe_down_few_kernel(MoeArgs
   FewCursor<F, RT, S> at;
   at.a = &a, at.expert = expert, at.map = map, at.row0 = h0, at.rows = a.H - h0;
   at.j = first / steps, at.n = first % steps, at.steps = steps;
+  at.serial = 0;
   at.rot = blockIdx.x % steps;           // the same for all that share an expert's steps
   at.turn();
   S st;
@@ -950,13 +1023,14 @@ struct ManyCursor {
   const uint16_t* pairs;                  // LDS
   int64_t row0;
   int rows, steps, item, last, tail, rot;   // tail: the last item's end
-  int begin, end, left, step;
+  int begin, end, left, step, serial;
   Tiles<F, RT> tiles;
   int xoff[T][4];
   bool live;
   __device__ __forceinline__ void enter(int from) {
     const uint32_t it = uniform(items[min(item, last)]);
     const int e = it & 1023, first = (it >> 10) & 8191, n = it >> 23;
+    serial++;
     begin = from;
     end = item >= last ? tail : steps;
     left = end - begin;
@@ -979,8 +1053,9 @@ struct ManyCursor {
     if (--left == 0) {
       item++;
       enter(0);
-    } else if (++step == end) {
-      step = begin;
+    } else {
+      if (++step == end) step = begin;
+      if (step == begin || (uint32_t)step % Fmt<F>::chunk == 0) serial++;
     }
   }
 };
@@ -1067,7 +1142,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void moe_down_many_kernel(MoeAr
     if (s1 > s0) {
       ManyCursor<F, RT, T> at;
       at.a = &a, at.items = items, at.pairs = pairs, at.row0 = h0, at.rows = a.H - h0;
-      at.steps = steps, at.rot = blockIdx.x + wave;
+      at.steps = steps, at.rot = blockIdx.x + wave, at.serial = 0;
       at.item = i0 + s0 / steps;
       at.last = i0 + (s1 - 1) / steps;
       at.tail = (s1 - 1) % steps + 1;
@@ -1156,17 +1231,20 @@ int validate_moe(const ep_problem_t* p, int inter) {
   return EP_OK;
 }
 
-// f(std::bool_constant<last step is a part>)
+// f(std::bool_constant<PART>): whole steps and, of codes, whole chunks of scales that
+// lie where they can be loaded at once?
 template <int F, typename Fn>
-void with_part(int cols, Fn&& f) {
-  if (cols % Fmt<F>::step) f(std::true_type());
-  else f(std::false_type());
+void with_part(const Weight& w, int cols, Fn&& f) {
+  const bool whole = cols % (Fmt<F>::step * Fmt<F>::chunk) == 0 && (uintptr_t)w.scale % 16 == 0 &&
+                     (uintptr_t)w.zero % 8 == 0;
+  if (whole) f(std::false_type());
+  else f(std::true_type());
 }
 
 template <int F, int RT, int T, bool MANY>
 void launch_down(const MoeArgs& a, hipStream_t st) {
   const int grid = (a.H + RT * 16 - 1) / (RT * 16);
-  with_part<F>(a.I, [&](auto part) {
+  with_part<F>(a.w2, a.I, [&](auto part) {
     using S = Stream<F, RT, T, part.value>;
     if constexpr (MANY) {
       moe_down_many_kernel<F, RT, T, part.value><<<
@@ -1200,7 +1278,7 @@ void launch_moe(MoeArgs a, hipStream_t st) {
   constexpr int apart = quant ? 1 : 2;
   a.split = MANY && groups(apart) * a.experts >= 256 ? apart : kUpWaves;
   const dim3 up(groups(a.split), a.experts);
-  with_part<F>(a.H, [&](auto part) {
+  with_part<F>(a.w13, a.H, [&](auto part) {
     moe_up_kernel<F, RT, UT, MANY, part.value>
         <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
   });
@@ -1238,10 +1316,10 @@ int launch_linear(int n, int cols, int rows, const void* x, const Weight& w, voi
   uint16_t* yp = (uint16_t*)y;
   EP_LOG("quant_linear: n=%d cols=%d rows=%d grid=%d", n, cols, rows, gx);
   constexpr int B = 64 * kLinWaves;
-  with_part<F>(cols, [&](auto part) {
+  with_part<F>(w, cols, [&](auto part) {
     constexpr bool P = part.value;
-    // groups of 32 and two token tiles: one row tile, or the registers spill
-    constexpr int R2 = Fmt<F>::integer && Fmt<F>::group == 32 ? 1 : RT;
+    // fine groups and two token tiles: one row tile, or the registers spill
+    constexpr int R2 = (Fmt<F>::integer && Fmt<F>::group == 32) || (F == kInt64Z && P) ? 1 : RT;
     const int g2 = (rows + R2 * 16 - 1) / (R2 * 16);
     if (n <= 4) linear_kernel<F, RT, 0, P><<<dim3(gx, 1), B, 0, st>>>(xp, w, yp, n, cols, rows);
     else if (n <= 16)

@@ -52,6 +52,28 @@ def test_linear_large(fmt, group, N, rows, cols):
     held(y, *ref.linear(x, w))
 
 
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS[1:])
+@pytest.mark.parametrize("N", [2, 9, 30])
+def test_scales_anywhere(fmt, group, zeros, N):
+    """Long rows, whose scales are loaded 16 bytes at a time, and the same from
+    addresses and at lengths where they cannot be."""
+    gen = torch.Generator().manual_seed(N)
+    rows = 70
+    for cols in (2048, 4096, 2048 + 256, 1024 + 128):
+        w = ref.W(fmt, (), rows, cols, group, zeros, gen)
+        x = torch.randn((N, cols), generator=gen).to(torch.bfloat16)
+        y = ep.quant_linear(x.cuda(), w.arg)
+        held(y, *ref.linear(x, w))
+        shifted = []
+        for t, off in ((w.arg.scales, 1), (w.arg.zeros, 3)):
+            if t is not None:
+                room = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:]
+                t = room.view(t.shape).copy_(t)
+            shifted.append(t)
+        v = ep.QuantWeight(w.arg.codes, shifted[0], zeros=shifted[1], group=group, fmt=fmt)
+        held(ep.quant_linear(x.cuda(), v), *ref.linear(x, w))
+
+
 def test_linear_no_rows():
     w = ref.W("int4", (), 16, 128, gen=torch.Generator().manual_seed(0))
     assert ep.quant_linear(torch.empty((0, 128), dtype=torch.bfloat16, device="cuda"),
