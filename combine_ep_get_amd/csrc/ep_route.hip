@@ -14,6 +14,11 @@
 // not clear of each other are ranked again by their 64-bit scores, one per lane;
 // a wavefront whose groups were not clear repeats the whole selection in 64 bits
 // (choose_exact).
+//
+// One wavefront's chain of num_topk maxima is latency, so is a call: 6.0 us for one
+// token of 256 experts, of which an empty launch is 3.5.  4096 tokens of 256 experts (4.5
+// MB) take 11.4 us with VALU busy 61% of the time and 16384 of 256 in bf16 (9.4 MB)
+// 14.0 us with 92%: the selection is bound by instructions, not by HBM (1.3 us).
 #include "ep_host.h"
 
 #include <type_traits>
