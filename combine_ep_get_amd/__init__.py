@@ -732,7 +732,8 @@ def moe_error(workspace):
 
 def quant_linear(x, w, out=None):
     """y [N, rows] bf16 = x [N, cols] bf16 times the transpose of the 4-bit
-    weight ``w`` (QuantWeight [rows, cols]), N <= 256 (see ep_quant_linear)."""
+    weight ``w`` (QuantWeight [rows, cols]), N <= 256; ``out`` must not overlap
+    ``x`` (see ep_quant_linear)."""
     import torch
     if not isinstance(w, QuantWeight) or len(w.shape) != 2:
         raise ValueError("w: need a QuantWeight [rows, cols]")

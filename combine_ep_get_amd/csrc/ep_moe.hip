@@ -680,8 +680,10 @@ MoePlan make_moe_plan(const ep_problem_t* p, int inter) {
   m.o_count = m.o_expert + list;
   m.o_start = m.o_count + list;
   m.o_pairs = m.o_start + list;
-  // many: uint16 [N*K]; few: bytes [experts][16]
-  m.o_hidden = m.o_pairs + align256(N > kFew ? pairs * 2 : (int64_t)m.experts * kFew);
+  // many: uint16 [N*K]; few: bytes [experts][16]; room for both, so that a workspace
+  // does for fewer tokens as well
+  const int64_t few = (int64_t)m.experts * kFew;
+  m.o_hidden = m.o_pairs + align256(pairs * 2 > few ? pairs * 2 : few);
   m.bytes = m.o_hidden + align256(pairs * inter * 2);
   return m;
 }

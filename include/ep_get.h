@@ -400,8 +400,8 @@ typedef struct ep_weight {
  *   inter      % 8 == 0 (bf16) or % group == 0; hidden and inter at most
  *              EP_MAX_CONTRACTION
  *   y          [N][hidden] bf16 out; may be x
- *   workspace  ep_moe_workspace_bytes, 256-byte aligned; no initialisation;
- *              calls that overlap need their own */
+ *   workspace  ep_moe_workspace_bytes (enough for fewer tokens, too), 256-byte
+ *              aligned; no initialisation; calls that overlap need their own */
 typedef struct ep_moe_args {
   const void* x;
   const void* topk_idx;

@@ -92,6 +92,9 @@ def test_workspace_bytes():
     assert small >= 8 * 2048 * 2 and small % 256 == 0
     assert ep.moe_workspace_bytes(256, 8, 32, 7168, 2048) >= 256 * 8 * 2048 * 2
     assert ep.moe_workspace_bytes(0, 8, 32, 7168, 2048) > 0
+    for K, E, I in ((32, 1024, 8), (1, 3, 8), (8, 32, 2048)):      # for n tokens is for fewer
+        sizes = [ep.moe_workspace_bytes(n, K, E, 64, I) for n in range(257)]
+        assert sizes == sorted(sizes)
     for bad in ((257, 8, 32, 7168, 2048), (1, 8, 32, 7170, 2048), (1, 8, 32, 7168, 2047),
                 (256, 32, 64, 4096, 65536)):
         with pytest.raises(ValueError):
