@@ -12,7 +12,7 @@
 //     to hold columns of row r; loading that directly touches 64 bytes of 16
 //     rows at a time, which reached 5.1 TB/s where whole lines reach 7.0 (493 MB,
 //     both as bare loads).  The loaded tile is turned through LDS, private to the
-//     wavefront, so there is no barrier;
+//     wavefront, so there is no barrier (but see SHARED);
 //   - loads run `depth` steps ahead in registers;
 //   - the wavefronts of a workgroup split the contraction and meet once, at the
 //     end;
@@ -36,8 +36,8 @@
 // are ignored.
 //
 // What it reaches (weights' bytes over the whole call, HBM reads at 7.0 TB/s at best):
-// bf16 6.5 TB/s at one token and 6.2 at 256; 4-bit 4.5 at one token, 4.9 at 16, 3.4
-// at 64, where the SIMDs run VALU (codes to bf16) 40% and MFMA 25% of the time and two
+// bf16 6.5 TB/s at one token and 6.1 at 256; 4-bit 4.6 at one token, 5.3 at 16, 3.7
+// at 64, where the SIMDs run VALU (codes to bf16) 40% and MFMA 20% of the time and two
 // wavefronts each, all that the registers allow, do not cover the rest.  Calls under 50
 // MB are the two launches' and three dependent loads' latency (routing, weights, sums).
 //
@@ -167,13 +167,21 @@ struct Tiles {
 // Where the steps come from is the caller's cursor: `step` (which columns), `serial`
 // (another one for every run of steps inside a chunk and the same tiles), `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row
 // of x of token(k, j) in bytes, kAbsent for none) and advance().
-template <int F, int RT, int T, bool PART>
+//
+// SHARED: the four wavefronts of a workgroup take the same steps of the same rows of x
+// and different tiles.  Each loads a quarter of a step's x into LDS for all, and as
+// registers hold neither it nor the codes during the products, the next step's loads
+// go out before them.  One barrier a step: x alternates between two places, and who is
+// past the barrier of a step has read the step before.  64 tokens, 4-bit, 7168 x 2048:
+// 196 us for the layer, with each wavefront's own x 214.
+template <int F, int RT, int T, bool PART, bool SHARED = false>
 struct Stream {
   using M = Fmt<F>;
   static constexpr bool quad = T == 0;
   static constexpr int TT = quad ? 1 : T;
   static constexpr int tokens = quad ? 4 : 16 * TT;
-  static constexpr int rows = quad ? 1 : 4;                       // loads of x per tile and half
+  static constexpr int rows = quad || SHARED ? 1 : 4;             // loads of x per tile and half
+  static constexpr int shared_words = SHARED ? TT * M::halves * 256 : 0;   // a step's x
   static constexpr int values_per_row = RT * M::scales;           // scales of a step, all tiles
   static constexpr int scale_loads = (values_per_row + 3) / 4;    // a value per lane group
   // Steps in flight: enough that the loads of a CU's wavefronts cover HBM's latency, as
@@ -202,7 +210,7 @@ struct Stream {
     u32x4 sc;                                        // wide: the chunk of row lane & 15 of
     u32x2 zc;                                        // tile lane >> 4
     int serial, step;
-    u32x4 x[TT][M::halves][quad ? 1 : 4];            // as loaded (Quad: the MFMA operand)
+    u32x4 x[TT][M::halves][rows];                    // as loaded (Quad: the MFMA operand)
   };
 
   // acc[i][j]: Quad: MFMA j's own rows (bf16, mxfp4), or [i][0] the whole sum
@@ -244,8 +252,9 @@ struct Stream {
   // A step's loads.  x comes as the weights do: 256 bytes of four rows per load (a load
   // in the MFMA's layout, 64 bytes of 16 rows, takes four times as long in L1).
   template <typename Cursor>
-  __device__ __forceinline__ void load(Slot& b, const Cursor& at, int cols, const void* x,
+  __device__ __forceinline__ void load(Slot& b, Cursor& at, bool live, int cols, const void* x,
                                        int xbytes) {
+    at.live = live;
     const int step = uniform(at.live ? at.step : 0);
 #pragma unroll
     for (int i = 0; i < RT; i++) {
@@ -262,12 +271,11 @@ struct Stream {
       if (quad || (at.live && b.serial != at.serial)) {
         b.serial = at.serial;
         const int c = (uint32_t)step / M::chunk;
-        b.sc = __builtin_amdgcn_raw_buffer_load_b128(
-            buffer(at.tiles.scale, at.live ? at.tiles.scale_end * M::scale_bytes : 0), soff[0] * M::scale_bytes,
-            c * 16, 0);
+        const int n = at.live ? at.tiles.scale_end : 0;
+        b.sc = __builtin_amdgcn_raw_buffer_load_b128(buffer(at.tiles.scale, n * M::scale_bytes),
+                                                     soff[0] * M::scale_bytes, c * 16, 0);
         if constexpr (M::zeros)
-          b.zc = __builtin_amdgcn_raw_buffer_load_b64(buffer(at.tiles.zero, at.live ? at.tiles.scale_end : 0),
-                                                      soff[0], c * 8, 0);
+          b.zc = __builtin_amdgcn_raw_buffer_load_b64(buffer(at.tiles.zero, n), soff[0], c * 8, 0);
       }
     } else if constexpr (M::quant) {
       const int n = at.live ? at.tiles.scale_end : 0;
@@ -411,14 +419,31 @@ struct Stream {
     return o;
   }
 
-  // The products of a step.
-  __device__ __forceinline__ void compute(const Slot& b, u32x4* buf) {
+  // The products of a step.  SHARED: next() once b's registers are free.
+  template <typename Next>
+  __device__ __forceinline__ void compute(const Slot& b, u32x4* buf, u32x4* xs, Next&& next) {
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     const f32x4 none{0.f, 0.f, 0.f, 0.f};
     constexpr uint32_t kOnes = 0x3F803F80u;
     const u32x4 ones{kOnes, kOnes, kOnes, kOnes};
     constexpr int per = 4 / M::groups;               // MFMAs per group
     if constexpr (M::quant) put(b, buf);
+    // mxfp4, value by value: the scales stay in registers
+    uint32_t sm[M::quant && !wide && !M::integer ? scale_loads : 1];
+    if constexpr (M::quant && !wide && !M::integer) {
+#pragma unroll
+      for (int q = 0; q < scale_loads; q++) sm[q] = b.s[q];
+    }
+    if constexpr (SHARED) {
+      const int lane = threadIdx.x & 63, row = (threadIdx.x >> 6) * 4 + (lane >> 4);
+#pragma unroll
+      for (int k = 0; k < TT; k++)
+#pragma unroll
+        for (int m = 0; m < M::halves; m++)
+          xs[(k * M::halves + m) * 256 + row * 16 + ((lane & 15) ^ row)] = b.x[k][m][0];
+      __syncthreads();
+      next();
+    }
     f32x4 sv[M::integer ? scale_loads : 1], zv[M::zeros ? scale_loads : 1];
     if constexpr (M::integer) take_scales(buf + RT * tile_words, sv);
     if constexpr (M::zeros) take_scales(buf + RT * tile_words + scale_words, zv);
@@ -441,7 +466,7 @@ struct Stream {
       else return operand(codes[i][m][j],
                           M::integer ? 0.f
                           : wide ? __uint_as_float(__builtin_amdgcn_ubfe(mx[i][m], g * 8, 8) << 23)
-                                 : __uint_as_float(b.s[i * M::halves + m] << 23));
+                                 : __uint_as_float(sm[i * M::halves + m] << 23));
     };
     const auto scale = [&](int i, int m, int q) {
       const int v = i * M::scales + m * M::groups + q;
@@ -459,6 +484,10 @@ struct Stream {
         if constexpr (quad) {
 #pragma unroll
           for (int j = 0; j < 4; j++) xo[k][j] = b.x[k][m][0];
+        } else if constexpr (SHARED) {
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            xo[k][j] = xs[(k * M::halves + m) * 256 + r * 16 + ((M::col(g, j) / 8) ^ r)];
         } else {
           const int lane = threadIdx.x & 63;
           fence();
@@ -536,27 +565,40 @@ struct Stream {
     }
   }
 
-  // Add `count` steps of the cursor to acc; after(i) follows step i's products.
+  // Add `count` steps of the cursor to acc; after(i) follows step i's products.  SHARED:
+  // the same count in all wavefronts; xs: LDS, two times shared_words.
   template <typename Cursor, typename After>
   __device__ __forceinline__ void run(int count, Cursor& at, int cols, const void* x, int xbytes,
-                                      u32x4* buf, After&& after) {
-    Slot slot[depth];
-#pragma unroll
-    for (int d = 0; d < depth; d++) {
-      slot[d].serial = -1;
-      at.live = d < count;
-      load(slot[d], at, cols, x, xbytes);
+                                      u32x4* buf, After&& after, u32x4* xs = nullptr) {
+    if constexpr (SHARED) {
+      Slot slot;
+      slot.serial = -1;
+      load(slot, at, count > 0, cols, x, xbytes);
       at.advance();
-    }
-    for (int i = 0; i < count; i += depth) {
+      for (int i = 0; i < count; i++) {
+        compute(slot, buf, xs + (i & 1) * shared_words, [&] {
+          load(slot, at, i + 1 < count, cols, x, xbytes);
+          at.advance();
+        });
+        after(i);
+      }
+    } else {
+      Slot slot[depth];
 #pragma unroll
       for (int d = 0; d < depth; d++) {
-        if (d > 0 && i + d >= count) break;
-        compute(slot[d], buf);
-        at.live = i + d + depth < count;
-        load(slot[d], at, cols, x, xbytes);
+        slot[d].serial = -1;
+        load(slot[d], at, d < count, cols, x, xbytes);
         at.advance();
-        after(i + d);
+      }
+      for (int i = 0; i < count; i += depth) {
+#pragma unroll
+        for (int d = 0; d < depth; d++) {
+          if (d > 0 && i + d >= count) break;
+          compute(slot[d], buf, nullptr, [] {});
+          load(slot[d], at, i + d + depth < count, cols, x, xbytes);
+          at.advance();
+          after(i + d);
+        }
       }
     }
   }
@@ -564,6 +606,7 @@ struct Stream {
   // The token row that the lane's load j of x is of in token tile k.
   static __device__ __forceinline__ int token(int k, int j) {
     const int lane = threadIdx.x & 63;
+    if (SHARED) j = threadIdx.x >> 6;
     return quad ? (lane & 15) >> 2 : k * 16 + j * 4 + (lane >> 4);
   }
 
@@ -830,11 +873,12 @@ __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 // A workgroup's four wavefronts share 4/split groups of tiles (RT/2 pairs of 16 gate
 // and 16 up rows), split of them the contraction of each.
 // Entries pos0 .. of the expert's list.
-template <int F, int RT, int T, bool PART>
+template <int F, int RT, int T, bool PART, bool SHARED>
 __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Gate& gate,
-                                          u32x4* buf, const Tiles<F, RT>& tiles, int i0, int pos0,
-                                          int n) {
-  using S = Stream<F, RT, T, PART>;
+                                          u32x4* buf, u32x4* xs, const Tiles<F, RT>& tiles, int i0,
+                                          int pos0, int n) {
+  using S = Stream<F, RT, T, PART, SHARED>;
+  const int split = SHARED ? 1 : a.split;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int nt = min(n - pos0, S::tokens);
   Strided<F, RT, S> at;
@@ -850,12 +894,12 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
   // memory channels, so workgroups start at different ones (64 tokens, bf16, 4096 x 1024:
   // 265 us, without 294).  Where the wavefronts are apart already it only costs (one
   // token, 4-bit: 41.4 us, with 42.4).
-  const int turn = a.split < kUpWaves ? blockIdx.x : 0;
-  const int count = at.share(steps_of<F>(a.H), wave & (a.split - 1), a.split, turn);
+  const int turn = split < kUpWaves ? blockIdx.x : 0;
+  const int count = at.share(steps_of<F>(a.H), wave & (split - 1), split, turn);
   S st;
   st.init(a.H, a.I);
   st.run(count, at, a.H, a.x, a.N * a.H * 2,
-         buf + wave * S::buffer_words, [](int) {});
+         buf + wave * S::buffer_words, [](int) {}, xs);
   if (pos0 == 0) gate.put(a, r);
   float* sums = reinterpret_cast<float*>(buf + wave * S::buffer_words);   // [RT][tokens][16]
   S::fence();
@@ -863,12 +907,12 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
   for (int i = 0; i < RT; i++)
     st.values(i, [&](int t, float v) { sums[(i * S::tokens + t) * 16 + (lane & 15)] = v; });
   __syncthreads();
-  const int wide = kUpWaves / a.split * RT * 8;      // rows of hidden per workgroup
+  const int wide = kUpWaves / split * RT * 8;      // rows of hidden per workgroup
   for (int q = threadIdx.x; q < nt * wide; q += kUpThreads) {
     const int t = q / wide, c = q - t * wide;
-    const int w0 = c / (RT * 8) * a.split, i = c % (RT * 8) / 16 * 2;
+    const int w0 = c / (RT * 8) * split, i = c % (RT * 8) / 16 * 2;
     float g = 0.f, u = 0.f;
-    for (int v = w0; v < w0 + a.split; v++) {
+    for (int v = w0; v < w0 + split; v++) {
       const float* part = reinterpret_cast<const float*>(buf + v * S::buffer_words);
       g += part[(i * S::tokens + t) * 16 + (c & 15)];
       u += part[((i + 1) * S::tokens + t) * 16 + (c & 15)];
@@ -887,15 +931,18 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
 // workgroup finds its expert and tokens itself, from the ids in L2, rather than wait for
 // a kernel that lists them.  7168 x 2048, 32 experts: one token (8 experts) 470 MB of
 // bf16 in 70 us (6.7 TB/s) or 121 MB of int4 in 25 us (4.8); 64 tokens int4 485 MB in
-// 110 us (4.4); 256 tokens bf16 1.88 GB in 290 us (6.5).
-template <int F, int RT, int T, bool MANY, bool PART>
-__global__ __launch_bounds__(kUpThreads, T == 0 && F != kInt32Z ? 3 : 2) void moe_up_kernel(MoeArgs a) {
-  using S = Stream<F, RT, T, PART>;
+// 96 us (5.1); 256 tokens bf16 1.88 GB in 290 us (6.5).
+template <int F, int RT, int T, bool MANY, bool PART, bool SHARED>
+__global__ __launch_bounds__(kUpThreads, T == 0 && F != kInt32Z ? 3 : 2) void moe_up_kernel(
+    MoeArgs a) {
+  using S = Stream<F, RT, T, PART, SHARED>;
+  const int split = SHARED ? 1 : a.split;
   __shared__ Routing r;
   __shared__ u32x4 buf[kUpWaves * S::buffer_words];
+  __shared__ u32x4 xs[SHARED ? 2 * S::shared_words : 1];
   extern __shared__ int16_t ids[];            // [N*K]
   int n = 0, before = 0, total = 0;
-  const int j = blockIdx.y, i0 = blockIdx.x * (kUpWaves / a.split * RT * 8);
+  const int j = blockIdx.y, i0 = blockIdx.x * (kUpWaves / split * RT * 8);
   Gate gate;
   const int e = find_expert<MANY>(a, r, ids, j, gate, n, before, total);
   if (blockIdx.x == 0 && j == 0 && threadIdx.x == 0) {
@@ -916,16 +963,16 @@ __global__ __launch_bounds__(kUpThreads, T == 0 && F != kInt32Z ? 3 : 2) void mo
     }
   }
   Tiles<F, RT> tiles;
-  const int own = i0 + uniform(threadIdx.x >> 6) / a.split * (RT * 8);
+  const int own = i0 + uniform(threadIdx.x >> 6) / split * (RT * 8);
   tiles.set(a.w13, (int64_t)e * 2 * a.I + min(own, a.I), a.I - own, a.I, a.H);
   if constexpr (!MANY) {
-    up_tokens<F, RT, T, PART>(a, r, gate, buf, tiles, i0, 0, n);
+    up_tokens<F, RT, T, PART, SHARED>(a, r, gate, buf, xs, tiles, i0, 0, n);
   } else {
     if (T == 1 || n > 16)
       for (int p = 0; p < n; p += 16 * T)
-        up_tokens<F, RT, T, PART>(a, r, gate, buf, tiles, i0, p, n);
+        up_tokens<F, RT, T, PART, SHARED>(a, r, gate, buf, xs, tiles, i0, p, n);
     else
-      up_tokens<F, RT, 1, PART>(a, r, gate, buf, tiles, i0, 0, n);
+      up_tokens<F, RT, 1, PART, SHARED>(a, r, gate, buf, xs, tiles, i0, 0, n);
   }
 }
 
@@ -1289,19 +1336,32 @@ void launch_moe(MoeArgs a, hipStream_t st) {
   constexpr int RT = T > 0 && coarse && quant ? 4 : 2, UT = MANY ? 2 : T;
   // A workgroup's four wavefronts share one contraction, which keeps the latency of
   // few tokens short (one token, 4-bit: 41.4 us, two on each 42.0, one on each 48.2).
-  // For longer lists less splitting is better where that leaves a workgroup per CU:
-  // the wavefronts meet at the same columns of x in L1, and the list is made for more
-  // rows.  256 tokens, bf16, 7168 x 2048: 467 us with four on each, 455 with two, 456
-  // with one; 64 tokens, 4-bit, 4096 x 1024: 121, 114, 113; but 64 tokens, 2048 x 256,
-  // 16 experts: 25.7, 30.5, 40.4.
+  // Where there are more workgroups than CUs anyway, less splitting is better: longer
+  // lists are made for more rows, and codes go through the SHARED stream with x loaded
+  // once for all four.  256 tokens, bf16, 7168 x 2048: 467 us with four on each, 455
+  // with two; 64 tokens, 4-bit: 236 with four, 196 shared; but 64 tokens, 2048 x 256, 16
+  // experts: 25.7 with four, 40.4 with one on each.
   const auto groups = [&](int split) { return (a.I + kUpWaves / split * RT * 8 - 1) /
                                               (kUpWaves / split * RT * 8); };
   constexpr int apart = quant ? 1 : 2;
-  a.split = MANY && groups(apart) * a.experts >= 256 ? apart : kUpWaves;
+  bool enough = false;
+  if constexpr (MANY) {
+    enough = groups(apart) * a.experts >= 256;
+  } else if constexpr (T == 1 && quant) {
+    // 5 to 16 tokens: if most experts are likely to be named (16 tokens, 7168 x 2048,
+    // 8 of 32 experts: 137 us, split 148; 2048 x 768 with zero points, 8 of 64: 54.2, 64.4; if
+    // most choices are -1 it costs: 74.3, 69.1; and with 10 tokens, 4 of 32: 52.7, 49.1)
+    enough = groups(apart) * a.experts >= 512 && 2 * a.N * a.K >= 3 * a.E;
+  }
+  a.split = enough ? apart : kUpWaves;
   const dim3 up(groups(a.split), a.experts);
   with_part<F>(a.w13, a.H, [&](auto part) {
-    moe_up_kernel<F, RT, UT, MANY, part.value>
-        <<<up, kUpThreads, sizeof(int16_t) * a.N * a.K, st>>>(a);
+    const size_t lds = sizeof(int16_t) * a.N * a.K;
+    if constexpr (T > 0 && quant) {
+      if (a.split == 1)
+        return moe_up_kernel<F, RT, UT, MANY, part.value, true><<<up, kUpThreads, lds, st>>>(a);
+    }
+    moe_up_kernel<F, RT, UT, MANY, part.value, false><<<up, kUpThreads, lds, st>>>(a);
   });
   // Codes with one token tile: two row tiles per wavefront halve what x costs, if
   // the workgroups still fill the GPU (64 tokens, 7168 columns: 115 us against 145;

@@ -187,6 +187,25 @@ def test_layer_in_place():
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("fmt,group,zeros,H,I", [
+    ("mxfp4", 32, False, 512, 160), ("mxfp4", 32, False, 96, 288), ("int4", 32, True, 256, 192),
+    ("int4", 128, False, 384, 256), ("int4", 64, False, 512, 192)])
+@pytest.mark.parametrize("N", [13, 16])
+def test_layer_few_tokens_of_many_experts(fmt, group, zeros, H, I, N):
+    """Up to 16 tokens that name most of the experts: the wavefronts share x."""
+    gen = torch.Generator().manual_seed(N + H)
+    E, K = 260, 30
+    w13 = ref.W(fmt, (E,), 2 * I, H, group, zeros, gen)
+    w2 = ref.W(fmt, (E,), H, I, group, zeros, gen)
+    x, idx, wts = inputs(N, H, E, K, gen)
+    idx[0, :2] = E - 1
+    held(layer(x, idx, wts, w13, w2), *ref.moe(x, idx, wts, w13, w2))
+    clean = layer(x, idx, wts, w13, w2).cpu()
+    x[3] = float("nan")                 # stays in its row
+    y = layer(x, idx, wts, w13, w2).cpu()
+    assert torch.equal(y[4:], clean[4:]) and torch.equal(y[:3], clean[:3])
+
+
 def small(seed=3, N=9, H=128, I=64, E=6, K=3, fmt="bf16"):
     gen = torch.Generator().manual_seed(seed)
     group = None if fmt == "bf16" else 32
