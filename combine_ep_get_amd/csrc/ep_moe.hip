@@ -113,7 +113,9 @@ struct Fmt {
 template <int F>
 __device__ __forceinline__ int row_bytes(int cols) { return Fmt<F>::quant ? cols / 2 : cols * 2; }
 template <int F>
-__device__ __forceinline__ int row_groups(int cols) { return Fmt<F>::quant ? cols / Fmt<F>::group : 0; }
+__device__ __forceinline__ int row_groups(int cols) {
+  return Fmt<F>::quant ? cols / Fmt<F>::group : 0;
+}
 template <int F>
 __device__ __forceinline__ int steps_of(int cols) {
   return (cols + Fmt<F>::step - 1) / Fmt<F>::step;
@@ -129,8 +131,8 @@ struct Weight {           // kernel argument: ep_weight_t without what the kerne
 // RT tiles of 16 rows: tile i starts at row `row` + i*16, or, where the tiles are
 // pairs of gate and up rows (`far` > 0), at row + (i/2)*16 + (i%2)*far.  `rows` is
 // how many rows there are from `row` on (for pairs: of each kind; none if negative);
-// those behind are out of range.  The scales of all tiles share one buffer; what it returns for rows
-// that are not there only reaches results that nobody stores.
+// those behind are out of range.  The scales of all tiles share one buffer; what it
+// returns for rows that are not there only reaches results that nobody stores.
 template <int F, int RT>
 struct Tiles {
   const uint8_t* data[RT];
@@ -165,8 +167,9 @@ struct Tiles {
 // by 7168 x 7168 of mxfp4, which has eight scales a step: 7.9 us, value by value 10.1.
 //
 // Where the steps come from is the caller's cursor: `step` (which columns), `serial`
-// (another one for every run of steps inside a chunk and the same tiles), `live` (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row
-// of x of token(k, j) in bytes, kAbsent for none) and advance().
+// (another one for every run of steps inside a chunk and the same tiles), `live`
+// (false: load nothing, which adds zeros), `tiles`, `xoff[TT][rows]` (the row of x
+// of token(k, j) in bytes, kAbsent for none) and advance().
 //
 // SHARED: the four wavefronts of a workgroup take the same steps of the same rows of x
 // and different tiles.  Each loads a quarter of a step's x into LDS for all, and as
@@ -389,7 +392,8 @@ struct Stream {
     } else if constexpr (M::words == 2) {
 #pragma unroll
       for (int q = 0; q < 2; q++) {
-        const u32x2 t = reinterpret_cast<const u32x2*>(buf + place(r, m * 4 + q * 2 + (g >> 1)))[g & 1];
+        const u32x4* at = buf + place(r, m * 4 + q * 2 + (g >> 1));
+        const u32x2 t = reinterpret_cast<const u32x2*>(at)[g & 1];
         v[q * 2] = t.x, v[q * 2 + 1] = t.y;
       }
     } else {
