@@ -12,8 +12,8 @@
 // once in 10^3 tokens: the selection is made in float32 and stands if every
 // decision was clear by more than the error bound (error_of).  Experts that were
 // not clear of each other are ranked again by their 64-bit scores, one per lane;
-// a wavefront whose groups were not clear repeats the whole selection in 64 bits
-// (choose_exact).
+// a wavefront whose groups were not clear, or that has more such experts than lanes,
+// repeats the whole selection in 64 bits (choose_exact).
 //
 // One wavefront's chain of num_topk maxima is latency, so is a call: 6.0 us for one
 // token of 256 experts, of which an empty launch is 3.5.  4096 tokens of 256 experts (4.5
@@ -160,7 +160,7 @@ __device__ __forceinline__ double sum_of_exp(const float* l, const bool* live, d
 struct Choice {
   int expert;                                  // in lane k the k-th, -1: none
   float logit;                                 // its logit
-  bool groups_clear;                           // MARGIN: the groups' decision was clear
+  bool settled;                                // MARGIN: the selection is that of 64-bit scores
 };
 
 // The V keys of a lane.  Up to 4 are sorted once, descending and stable, with
@@ -224,10 +224,10 @@ struct Keys {
 
 // The selection, with U = uint32_t keys of floats or uint64_t keys of doubles: val[]
 // scores the groups, by orders the experts, 0 is masked.  MARGIN: float32 scores
-// that may be off by error_of; groups_clear tells whether the groups' decision
-// would stand all the same, and experts that might change places are ranked by
+// that may be off by error_of.  Experts that might change places are ranked by
 // their 64-bit scores (m, z: the softmax's maximum and sum in 64 bits, z read
-// through exact_z only then).
+// through exact_z only then).  Not settled: the groups' decision might not stand, or
+// more experts than there are lanes might change places.
 template <int V, bool MARGIN, typename U, typename Z>
 __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const float* l,
                                          const RouteParams& p, U* lds, double m, Z exact_z) {
@@ -284,7 +284,7 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
       const U in = ~wave_max(stays ? ~gk : U(0)), out = wave_max(own < p.G && !stays ? gk : U(0));
       if (in && out) {
         const float a = value_of(in), b = value_of(out);
-        c.groups_clear = a - b > 2.f * (error_of(a, p.softmax) + error_of(b, p.softmax));
+        c.settled = a - b > 2.f * (error_of(a, p.softmax) + error_of(b, p.softmax));
       }
     }
 #pragma unroll
@@ -298,7 +298,7 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
   float before = 0.f;
   bool clear = true;
   int n = 0;                                   // chosen so far, in the lanes 0 .. n-1
-  for (; n < 64; n++) {
+  for (;; n++) {
     const U best = by.largest();
     const U top = wave_max(best);
     if (top == 0) break;
@@ -306,6 +306,10 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
       const float now = value_of(top);
       const bool far = before - now > error_of(before, p.softmax) + error_of(now, p.softmax);
       if (n >= p.K && far) break;              // and of all after: they are smaller still
+      if (n == 64) {                           // a lane for each, and the run goes on
+        c.settled = false;
+        break;
+      }
       clear &= n == 0 || far;
       before = now;
     } else if (n == p.K) {
@@ -323,7 +327,7 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
     if (lane == n) c.expert = w * V + at, c.logit = logit;
   }
   if constexpr (MARGIN) {
-    if (!clear && c.groups_clear) {
+    if (!clear && c.settled) {
       const double z = exact_z();
       double s = 0.0;
       if (lane < n) s = score(c.logit, p.softmax, m, z) + (double)p.bias[c.expert];
@@ -439,7 +443,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const L* __restric
   Choice c = choose<V, SCORED>(val, by, l, p, reinterpret_cast<uint32_t*>(own), m, [&] {
     return p.softmax ? sum_of_exp<V>(l, live, m) : 1.0;
   });
-  if (SCORED && !c.groups_clear) c = choose_exact<V>(row, p, m, own);
+  if (SCORED && !c.settled) c = choose_exact<V>(row, p, m, own);
 
   // The weights in float32.  Scores that are divided by their sum only need a common
   // factor, so exponentials are taken from the largest logit chosen: nothing

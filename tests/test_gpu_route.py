@@ -128,3 +128,26 @@ def test_routes_feed_the_layout():
     lay = ep.get_layout(idx, 32, 4, 8)
     assert ep.layout_error(lay) == 0
     assert (lay.slot_of[3] == -1).all() and int(lay.num_recv_per_expert.sum()) == 63 * 4
+
+
+@pytest.mark.parametrize("E,kw", [
+    (64, {}), (65, {}), (256, {}), (1024, {}),
+    (256, dict(num_groups=8, topk_groups=4, group_top=2)), (300, dict(num_groups=3, topk_groups=2))],
+    ids=str)
+def test_runs_of_unclear_experts_of_any_length(E, kw):
+    """More experts than a wavefront has lanes, none clear of the next in float32."""
+    gen = torch.Generator().manual_seed(E)
+    noise = torch.randn((6, E), generator=gen)
+    flat = lambda v: torch.full((E,), v)                            # noqa: E731
+    check(20 + noise, 8, flat(0.0), **kw)             # every float32 score is 1
+    check(-22 + noise, 8, flat(0.1), **kw)
+    check(8 + 1e-4 * noise, 8, flat(0.1), **kw)
+    check(noise, 8, flat(1e6), **kw)
+    for above, b in ((25.0, 0.1), (110.0, 0.0)):      # the rest's scores vanish in float32
+        logits = noise.clone()
+        logits[torch.arange(6), torch.randint(0, E, (6,), generator=gen)] += above
+        check(logits, 8, flat(b), scoring="softmax", **kw)
+    if not kw:                                        # clear groups of unclear experts
+        for G in (g for g in (1, 2, 3) if E % g == 0):
+            by_group = torch.arange(G).repeat_interleave(E // G).float()
+            check(20 + noise, 8, by_group, num_groups=G, topk_groups=1, group_top=2)
