@@ -237,6 +237,7 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
   if (p.G > 1) {
     const int per = p.E / p.G, lanes = per / V;
     U gk = 0;                                  // of the lane's group (inside) or group `lane`
+    Num first, second;                         // its two largest, where gk is not 0
     const bool two = p.top == 2;
     // whole lanes per group, a power of two of them: butterflies; else through LDS
     const bool inside = per % V == 0 && (lanes & (lanes - 1)) == 0;
@@ -253,6 +254,7 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
         if (two) b = fmax(fmin(a, oa), fmax(b, __shfl_xor(b, d)));
         a = fmax(a, oa);
       }
+      first = a, second = b;
       const Num s = two ? a + b : a;
       gk = lane * V < p.E && s > -INFINITY ? ordered(s) : U(0);
     } else {
@@ -268,7 +270,8 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
           b = k > a ? a : (k > b ? k : b);
           a = k > a ? k : a;
         }
-      gk = !two ? a : b ? ordered(value_of(a) + value_of(b)) : U(0);
+      first = value_of(a), second = value_of(b);
+      gk = !two ? a : b ? ordered(first + second) : U(0);
     }
     // rank of the lane's group: those with a larger score, or an equal one and before it
     const int step = inside ? lanes : 1, own = inside ? lane / lanes : lane;
@@ -280,12 +283,17 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
     const bool stays = own < p.G && rank < p.keep;
     const uint64_t kept = __ballot(stays);
     if constexpr (MARGIN) {
-      // the worst that stays (~: the minimum) against the best that goes
-      const U in = ~wave_max(stays ? ~gk : U(0)), out = wave_max(own < p.G && !stays ? gk : U(0));
-      if (in && out) {
-        const float a = value_of(in), b = value_of(out);
-        c.settled = a - b > 2.f * (error_of(a, p.softmax) + error_of(b, p.softmax));
-      }
+      // The least that a group that stays may have (~: the minimum) against the most of
+      // one that goes.  Of a sum both terms may be off, however small it is itself: the
+      // bias may be large and of either sign.  error_of(s) covers the rounding of the sum
+      // and of s -+ off.  (inf - inf: not clear.)
+      const float s = value_of(gk);
+      const float off = error_of(s, p.softmax) +
+                        (two ? error_of(first, p.softmax) + error_of(second, p.softmax) : 0.f);
+      const U least = ordered(fmaxf(s - off, -INFINITY)), most = ordered(fminf(s + off, INFINITY));
+      const U in = ~wave_max(stays && gk ? ~least : U(0));
+      const U out = wave_max(own < p.G && !stays && gk ? most : U(0));
+      if (out) c.settled = in > out;           // else all that go are masked
     }
 #pragma unroll
     for (int v = 0; v < V; v++) {

@@ -151,3 +151,18 @@ def test_runs_of_unclear_experts_of_any_length(E, kw):
         for G in (g for g in (1, 2, 3) if E % g == 0):
             by_group = torch.arange(G).repeat_interleave(E // G).float()
             check(20 + noise, 8, by_group, num_groups=G, topk_groups=1, group_top=2)
+
+
+
+@pytest.mark.parametrize("E,G", [(32, 4), (48, 4), (256, 8), (1024, 64)])
+def test_group_scores_of_large_opposite_terms(E, G):
+    """Biases that cancel inside a group: the sum is small, what its terms lost is not."""
+    gen = torch.Generator().manual_seed(E)
+    a = 0.2 + 0.5 * torch.rand((40, G), generator=gen, dtype=torch.float64)
+    b = 0.93 - a + 1e-6 * torch.randn((40, G), generator=gen, dtype=torch.float64)
+    logits = torch.zeros((40, G, E // G))
+    logits[:, :, 1], logits[:, :, 3] = torch.logit(a).float(), torch.logit(b).float()
+    for big in (100.0, 1e4):
+        bias = torch.full((G, E // G), -1e5)
+        bias[:, 1], bias[:, 3] = big, -big
+        check(logits.view(40, E), 2, bias.view(-1), num_groups=G, topk_groups=G // 2, group_top=2)
