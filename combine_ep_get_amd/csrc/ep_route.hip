@@ -255,8 +255,8 @@ __device__ __forceinline__ Choice choose(const U* val, Keys<V, U> by, const floa
         a = fmax(a, oa);
       }
       first = a, second = b;
-      const Num s = two ? a + b : a;
-      gk = lane * V < p.E && s > -INFINITY ? ordered(s) : U(0);
+      // no group without its terms (their sum may be -inf in float32)
+      if (lane * V < p.E && (two ? b : a) > -INFINITY) gk = ordered(two ? a + b : a);
     } else {
       fence();
 #pragma unroll

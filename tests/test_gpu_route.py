@@ -166,3 +166,13 @@ def test_group_scores_of_large_opposite_terms(E, G):
         bias = torch.full((G, E // G), -1e5)
         bias[:, 1], bias[:, 3] = big, -big
         check(logits.view(40, E), 2, bias.view(-1), num_groups=G, topk_groups=G // 2, group_top=2)
+
+
+
+@pytest.mark.parametrize("E,G", [(16, 2), (12, 2), (256, 2)])
+def test_group_scores_below_the_lowest_float32(E, G):
+    """A group whose two terms add up to less than the lowest float32 still comes
+    before one that has too few experts."""
+    logits = torch.randn((3, E), generator=torch.Generator().manual_seed(6))
+    logits[:, 1:E // 2] = -math.inf
+    check(logits, 2, torch.full((E,), -3e38), num_groups=G, topk_groups=1, group_top=2)
