@@ -454,13 +454,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const L* __restric
   if (SCORED && !c.settled) c = choose_exact<V>(row, p, m, own);
 
   // The weights in float32.  Scores that are divided by their sum only need a common
-  // factor, so exponentials are taken from the largest logit chosen: nothing
-  // underflows that counts.  sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).
+  // factor, so exponentials are taken from the largest logit chosen, and a softmax's sum
+  // z is left out: nothing underflows that counts.  sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).
   float s = 0.f;
   const bool any = c.expert >= 0;
   if (p.softmax) {
     const float from = p.renorm ? value_of(wave_max(any ? ordered(c.logit) : 0u)) : m;
-    s = any ? expf(c.logit - from) / z : 0.f;
+    s = any ? expf(c.logit - from) : 0.f;
+    if (any && !p.renorm) s /= z;
   } else {
     const float from = p.renorm ? fminf(value_of(wave_max(any ? ordered(c.logit) : 0u)), 0.f) : 0.f;
     s = any ? expf(fminf(c.logit, 0.f) - from) / (1.f + expf(-fabsf(c.logit))) : 0.f;

@@ -176,3 +176,12 @@ def test_group_scores_below_the_lowest_float32(E, G):
     logits = torch.randn((3, E), generator=torch.Generator().manual_seed(6))
     logits[:, 1:E // 2] = -math.inf
     check(logits, 2, torch.full((E,), -3e38), num_groups=G, topk_groups=1, group_top=2)
+
+
+
+def test_a_bias_of_zero_changes_nothing():
+    """Divided by their sum the weights do not depend on the row's other scores."""
+    logits = torch.randn((500, 200), generator=torch.Generator().manual_seed(8)).cuda()
+    a = ep.route(logits, 6, scoring="softmax")
+    b = ep.route(logits, 6, scoring="softmax", bias=torch.zeros(200, device="cuda"))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
