@@ -21,6 +21,7 @@
 // 14.0 us with 92%: the selection is bound by instructions, not by HBM (1.3 us).
 #include "ep_host.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace {
@@ -476,28 +477,37 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const L* __restric
   }
 }
 
+// A grid has less than 2^32 threads in all, 2^26 tokens: more tokens take several launches.
+constexpr int kTokensPerLaunch = 1 << 24;
+
 template <typename L, typename I, bool SCORED>
 int launch_route(const ep_route_args_t* a, hipStream_t st) {
-  RouteParams p{a->bias, a->topk_weights, a->num_tokens, a->num_experts, a->num_topk,
+  RouteParams p{a->bias, nullptr, 0, a->num_experts, a->num_topk,
                 a->num_groups, a->topk_groups, a->group_top, a->scoring == EP_SCORE_SOFTMAX,
                 a->renormalize != 0, a->scale};
-  const int grid = (p.N + kRouteWaves - 1) / kRouteWaves;
   const size_t lds = p.G > 1 ? sizeof(uint64_t) * kRouteWaves * p.E : 0;
-  const L* lg = (const L*)a->logits;
-  I* ix = (I*)a->topk_idx;
   const int v = (p.E + 63) / 64;
-  EP_LOG("route: N=%d E=%d K=%d groups=%d/%d grid=%d", p.N, p.E, p.K, p.keep, p.G, grid);
-  const auto go = [&](auto V) {
-    constexpr int n = decltype(V)::value;
-    const bool wide = p.E % n == 0 && ((uintptr_t)lg & (n * sizeof(L) - 1)) == 0;
-    route_kernel<n, L, I, SCORED><<<grid, kRouteThreads, lds, st>>>(lg, ix, p, wide);
-  };
-  if (v <= 1) go(std::integral_constant<int, 1>());
-  else if (v <= 2) go(std::integral_constant<int, 2>());
-  else if (v <= 4) go(std::integral_constant<int, 4>());
-  else if (v <= 8) go(std::integral_constant<int, 8>());
-  else go(std::integral_constant<int, 16>());
-  return check_launch("route_kernel");
+  EP_LOG("route: N=%d E=%d K=%d groups=%d/%d", a->num_tokens, p.E, p.K, p.keep, p.G);
+  for (int64_t t = 0; t < a->num_tokens; t += kTokensPerLaunch) {
+    p.N = (int)std::min<int64_t>(a->num_tokens - t, kTokensPerLaunch);
+    p.weights = a->topk_weights + t * p.K;
+    const L* lg = (const L*)a->logits + t * p.E;
+    I* ix = (I*)a->topk_idx + t * p.K;
+    const int grid = (p.N + kRouteWaves - 1) / kRouteWaves;
+    const auto go = [&](auto V) {
+      constexpr int n = decltype(V)::value;
+      const bool wide = p.E % n == 0 && ((uintptr_t)lg & (n * sizeof(L) - 1)) == 0;
+      route_kernel<n, L, I, SCORED><<<grid, kRouteThreads, lds, st>>>(lg, ix, p, wide);
+    };
+    if (v <= 1) go(std::integral_constant<int, 1>());
+    else if (v <= 2) go(std::integral_constant<int, 2>());
+    else if (v <= 4) go(std::integral_constant<int, 4>());
+    else if (v <= 8) go(std::integral_constant<int, 8>());
+    else go(std::integral_constant<int, 16>());
+    const int rc = check_launch("route_kernel");
+    if (rc != EP_OK) return rc;
+  }
+  return EP_OK;
 }
 
 template <typename L, typename I>

@@ -185,3 +185,17 @@ def test_a_bias_of_zero_changes_nothing():
     a = ep.route(logits, 6, scoring="softmax")
     b = ep.route(logits, 6, scoring="softmax", bias=torch.zeros(200, device="cuda"))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+
+@pytest.mark.parametrize("N", [2 ** 26 + 3, 2 ** 31 - 1])
+def test_most_tokens(N):
+    """More tokens than one grid has wavefronts for, up to the most that are accepted."""
+    logits = torch.empty((N, 2), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, N, 2 ** 26):
+        logits[a:a + 2 ** 26].normal_()
+    idx, w = ep.route(logits, 1, scale=1.5)
+    for a in range(0, N, 2 ** 26):
+        part = logits[a:a + 2 ** 26]
+        assert torch.equal(idx[a:a + 2 ** 26, 0], (part[:, 1] > part[:, 0]).int())
+        assert (w[a:a + 2 ** 26] == 1.5).all()
