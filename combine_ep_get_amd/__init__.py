@@ -615,7 +615,12 @@ class QuantWeight:
     [..., rows, cols/2] as pack_codes lays them out, and
     ``fmt`` "int4": ``scales`` bf16 [..., rows, cols/group], optional ``zeros``
     uint8 of that shape (8 without), group 32, 64 or 128;
-    ``fmt`` "mxfp4": ``scales`` uint8 (E8M0) [..., rows, cols/32], group 32."""
+    ``fmt`` "mxfp4": ``scales`` uint8 (E8M0) [..., rows, cols/32], group 32.
+
+    The weight shares the tensors' memory (changed values count) and is fixed
+    otherwise: its attributes are read-only, and a call on a weight whose memory
+    was resized or freed since raises.  Copies (copy.deepcopy, pickle) are weights of
+    their own."""
 
     def __init__(self, codes, scales, zeros=None, group=None, fmt="int4"):
         import torch
@@ -626,24 +631,45 @@ class QuantWeight:
             raise ValueError(f"group: {group} is not a group size of {fmt}")
         if codes.dim() < 2:
             raise ValueError("codes: need [..., rows, cols/2]")
-        self.shape = (*codes.shape[:-1], 2 * codes.shape[-1])
-        if self.shape[-1] % group != 0:
-            raise ValueError(f"cols {self.shape[-1]} is no multiple of the group {group}")
-        per = (*codes.shape[:-1], self.shape[-1] // group)
+        shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+        if shape[-1] % group != 0:
+            raise ValueError(f"cols {shape[-1]} is no multiple of the group {group}")
+        per = (*codes.shape[:-1], shape[-1] // group)
         _arg(codes, torch.uint8, codes.shape, "codes", codes)
         _arg(scales, torch.bfloat16 if fmt == "int4" else torch.uint8, per, "scales", codes)
         if zeros is not None:
             if fmt != "int4":
                 raise ValueError("zeros: only int4 has zero points")
             _arg(zeros, torch.uint8, per, "zeros", codes)
-        self.codes, self.scales, self.zeros, self.group, self.fmt = codes, scales, zeros, group, fmt
-        self.device = codes.device
-        # what the calls read; the tensors above keep the memory
-        self.desc = (codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(),
-                     EP_WEIGHT_INT4 if fmt == "int4" else EP_WEIGHT_MXFP4, group)
+        # aliases of the tensors: what is done to those afterwards (.data, set_) does not
+        # reach them; desc is what the calls read
+        codes, scales = codes.detach(), scales.detach()
+        zeros = None if zeros is None else zeros.detach()
+        self.__dict__.update(
+            codes=codes, scales=scales, zeros=zeros, group=group, fmt=fmt, shape=shape,
+            device=codes.device,
+            desc=(codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(),
+                  EP_WEIGHT_INT4 if fmt == "int4" else EP_WEIGHT_MXFP4, group))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"QuantWeight.{name} is read-only: make a new QuantWeight")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"QuantWeight.{name} is read-only")
+
+    def __reduce__(self):
+        return QuantWeight, (self.codes, self.scales, self.zeros, self.group, self.fmt)
 
     def get_device(self):
         return self.codes.get_device()
+
+    def checked_desc(self):
+        """desc, if the memory is still where it was."""
+        d, z = self.desc, self.zeros
+        if self.codes.data_ptr() != d[0] or self.scales.data_ptr() != d[1] \
+                or (z is not None and z.data_ptr() != d[2]):
+            raise ValueError("QuantWeight: the memory of its tensors was resized or freed")
+        return d
 
 
 def pack_codes(codes, fmt="int4"):
@@ -666,7 +692,7 @@ def _weight_desc(w, shape, name, ref):
             raise ValueError(f"{name}: need {shape}, got {w.shape}")
         if w.get_device() != ref.get_device():
             raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
-        return w.desc
+        return w.checked_desc()
     _arg(w, torch.bfloat16, shape, name, ref)
     return w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0
 
@@ -745,7 +771,7 @@ def quant_linear(x, w, out=None):
     else:
         _arg(out, torch.bfloat16, (N, rows), "y", w)
     _call(lib().ep_quant_linear, "ep_quant_linear", x, N, cols, rows, x.data_ptr(),
-          _WEIGHT_DESC(*w.desc), out.data_ptr())
+          _WEIGHT_DESC(*w.checked_desc()), out.data_ptr())
     return out
 
 

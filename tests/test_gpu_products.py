@@ -1,5 +1,7 @@
 """The expert layer for a few tokens and the 4-bit product on the GPU, against
 plain 64-bit implementations with bounds from the arithmetic (product_ref.py)."""
+import copy
+
 import pytest
 import torch
 
@@ -369,3 +371,23 @@ def test_layer_is_dispatch_experts_combine():
         rows_mag += wts[:, k].double().cpu()[:, None] * out.double()[slot[:, k].long()].abs()
     assert ((z - y.double().cpu()).abs()
             <= bound + ref.HALF * 1.01 * rows_mag + ref.HALF * z.abs() + 4 * ref.U * rows_mag).all()
+
+
+@pytest.mark.parametrize("fmt,zeros", [("int4", True), ("mxfp4", False)])
+def test_copied_weights_and_rebound_tensors(fmt, zeros):
+    """A copy does not read its original, nor a weight what its tensors became since;
+    values changed in place count."""
+    gen = torch.Generator().manual_seed(12)
+    w = ref.W(fmt, (), 40, 256, zeros=zeros, gen=gen)
+    x = torch.randn((3, 256), generator=gen).to(torch.bfloat16).cuda()
+    want = ep.quant_linear(x, w.arg)
+    codes, scales = w.arg.codes.clone(), w.arg.scales.clone()
+    v = ep.QuantWeight(codes, scales, zeros=w.arg.zeros, group=w.group, fmt=fmt)
+    u = copy.deepcopy(v)
+    codes.data, scales.data = torch.zeros_like(codes), torch.zeros_like(scales)
+    assert torch.equal(ep.quant_linear(x, v), want)
+    v.scales.zero_()                    # 0 of int4, 2^-127 of mxfp4
+    tiny = ep.quant_linear(x, v)
+    assert (tiny.abs() <= (0 if fmt == "int4" else 2.0 ** -127 * 6 * 256 * 8)).all()
+    del v
+    assert torch.equal(ep.quant_linear(x, u), want)

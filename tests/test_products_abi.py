@@ -1,6 +1,8 @@
 """Refusals of the router's and the products' entry points: host checks that
 run before any launch, so no GPU is needed."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -163,3 +165,36 @@ def test_packed_structs_are_the_structs():
                            (ep._MOE_ARGS(*[0] * 16), ep.MoeArgs),
                            (ep._PROBLEM(*[0] * 9), ep.Problem)):
         assert len(packed) == ctypes.sizeof(struct)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quant_weight_is_fixed(monkeypatch, zeros):
+    """Calls pass the addresses a weight was made with, so nothing may leave them behind:
+    no attribute is rebound, changed storage is noticed, copies have their own."""
+    monkeypatch.setattr(ep, "_arg", lambda *a: None)     # CPU tensors will do here
+    parts = [torch.zeros((16, 64), dtype=torch.uint8), torch.ones((16, 1), dtype=torch.bfloat16),
+             torch.full((16, 1), 8, dtype=torch.uint8) if zeros else None]
+    w = ep.QuantWeight(*parts)
+    for name in ("codes", "scales", "zeros", "group", "fmt", "shape", "device", "desc", "other"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, getattr(w, name, None))
+        with pytest.raises(AttributeError):
+            delattr(w, name)
+    desc = w.checked_desc()
+    held = [t.clone() for t in parts if t is not None]
+    for t in parts:
+        if t is not None:
+            t.data = torch.zeros(4, dtype=t.dtype)       # the caller's tensor goes elsewhere
+    assert w.checked_desc() == desc
+    assert all(torch.equal(a, b) for a, b in zip((w.codes, w.scales, w.zeros), held))
+    for copied in (copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
+        assert copied.desc[0] == copied.codes.data_ptr() != desc[0] and copied.shape == w.shape
+        assert copied.desc[3:] == desc[3:] and bool(copied.desc[2]) == zeros
+    assert copy.copy(w).checked_desc() == desc           # shares the memory, and holds it
+    for t in (w.codes, w.scales, w.zeros):
+        if t is not None:
+            v = copy.deepcopy(w)
+            at = v.codes if t is w.codes else v.scales if t is w.scales else v.zeros
+            at.untyped_storage().resize_(0)
+            with pytest.raises(ValueError):
+                ep._weight_desc(v, v.shape, "w", v)
