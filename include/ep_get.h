@@ -389,7 +389,7 @@ typedef struct ep_weight {
  * of its weights.  Ids outside [-1, E) are skipped and flagged as by
  * ep_get_layout (ep_layout_error on `workspace`).  Deterministic.
  * Weights are finite, x and topk_weights too, |x| and the values before the
- * second product below 2^119 with EP_WEIGHT_INT4; what a token has beyond that
+ * second product below 2^112 with EP_WEIGHT_INT4; what a token has beyond that
  * stays in its own row of y.
  *   p          num_tokens 0..EP_MAX_FEW_TOKENS, hidden, num_topk, num_experts,
  *              topk_idx_bytes; num_ranks, expert_alignment, use_fp8 and
@@ -420,7 +420,7 @@ int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* args, void* stream)
  *   y [num_rows][out_rows] bf16; num_rows 0..EP_MAX_FEW_TOKENS, cols at most
  *   EP_MAX_CONTRACTION, out_rows 1..EP_MAX_HIDDEN.
  * y must not overlap x.  float32 accumulation, one rounding.  Weights are finite,
- * x too, |x| below 2^119 with EP_WEIGHT_INT4; what a row has beyond that stays in
+ * x too, |x| below 2^112 with EP_WEIGHT_INT4; what a row has beyond that stays in
  * its own row of y.  Deterministic. */
 int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void* x,
                     const ep_weight_t* w, void* y, void* stream);

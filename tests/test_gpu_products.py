@@ -391,3 +391,15 @@ def test_copied_weights_and_rebound_tensors(fmt, zeros):
     assert (tiny.abs() <= (0 if fmt == "int4" else 2.0 ** -127 * 6 * 256 * 8)).all()
     del v
     assert torch.equal(ep.quant_linear(x, u), want)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS[1:7])
+@pytest.mark.parametrize("N", [1, 4, 5, 20])
+def test_int4_largest_inputs(fmt, group, zeros, N):
+    """|x| up to 2^112: a group's sum of 128 + code, and of its zero point, times x of
+    one sign is below 2^112 * 128 * (143 or 255) < 2^127."""
+    gen = torch.Generator().manual_seed(N)
+    w = ref.W(fmt, (), 40, 256, group, zeros, gen)
+    x = (2.0 ** 111 * (1 + torch.rand((N, 256), generator=gen))).to(torch.bfloat16)
+    for sign in (1, -1):
+        held(ep.quant_linear((sign * x).cuda(), w.arg), *ref.linear(sign * x, w))
