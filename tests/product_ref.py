@@ -7,6 +7,7 @@ order, with U = 2^-23 (one step per addition: the matrix instruction need not
 round to nearest).  A rounding to bf16 is off by at most 2^-8 of the value
 (half of torch.finfo(bfloat16).eps).
 """
+import copy
 import math
 
 import torch
@@ -58,6 +59,12 @@ class W:
         self.arg = ep.QuantWeight(packed.to(device), s.to(device),
                                   zeros=None if z is None else z.to(device), group=group, fmt=fmt)
 
+    def only(self, e, device):
+        """The values of one of a stack, on `device` (no `arg`)."""
+        w = copy.copy(self)
+        w.value, w.mags, w.arg = self.value[e].to(device), self.mags[e].to(device), None
+        return w
+
     def product(self, x, at=()):
         """(x W^T, bound of the kernel's float32 error) in 64 bits."""
         v, m = self.value[at], self.mags[at]
@@ -97,6 +104,32 @@ def moe(x, idx, wts, w13, w2):
             bound[t] += (ep_ + eh @ w2.value[e].abs().t())[0] * (1 + 2.0 ** -6)
         bound[t] += 64 * U * y[t].abs()              # the sum over experts and wavefronts
     return y, bound + HALF * (y.abs() + bound) + TINY
+
+
+def moe_by_expert(x, idx, wts, w13, w2, device="cpu"):
+    """moe() with an expert's tokens together, on `device`: for larger sizes."""
+    x, wts = x.double().to(device), wts.double().to(device)
+    E, H, I = w2.value.shape
+    y, bound = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(E):
+        w = (wts * (idx == e).to(device)).sum(dim=1)
+        at = (idx == e).any(dim=1).nonzero()[:, 0].to(device)
+        if not len(at):
+            continue
+        w = w[at, None]
+        a, b = w13.only(e, device), w2.only(e, device)
+        gu, err = a.product(x[at])
+        g, u, eg, eu = gu[:, :I], gu[:, I:], err[:, :I], err[:, I:]
+        sg = g * torch.sigmoid(g)
+        h = w * sg * u
+        eh = w.abs() * (1.1 * u.abs() * eg + sg.abs() * eu + 1.1 * eg * eu
+                        + 16 * U * (sg * u).abs())
+        eh = eh + HALF * (h.abs() + eh)
+        p, ep_ = b.product(h)
+        y[at] += p
+        bound[at] += (ep_ + eh @ b.value.abs().t()) * (1 + 2.0 ** -6)
+    bound += 64 * U * y.abs()
+    return y.cpu(), (bound + HALF * (y.abs() + bound) + TINY).cpu()
 
 
 def linear(x, w):
