@@ -46,7 +46,7 @@ def test_second_product(fmt, group, zeros, I, N):
     check(*weights(fmt, group, zeros, 3, 6144 + 128, I), N, 2)
 
 
-@pytest.mark.parametrize("N", [5, 16, 33])
+@pytest.mark.parametrize("N", [2, 4, 5, 16, 33])
 @pytest.mark.parametrize("fmt,group,zeros", QUANT + [("bf16", None, False)])
 def test_second_product_of_one_expert(fmt, group, zeros, N):
     """All tokens to one of two experts: few items, each of them split over wavefronts."""
