@@ -36,9 +36,10 @@
 // are ignored.
 //
 // What it reaches (weights' bytes over the whole call, HBM reads at 7.0 TB/s at best):
-// bf16 6.5 TB/s at one token and 6.1 at 256; 4-bit 4.6 at one token, 5.3 at 16, 3.7
+// bf16 6.5 TB/s at one token and 6.2 at 256; 4-bit 4.6 at one token, 5.1 at 16, 3.7
 // at 64, where the SIMDs run VALU (codes to bf16) 40% and MFMA 20% of the time and two
-// wavefronts each, all that the registers allow, do not cover the rest.  Calls under 50
+// wavefronts each do not cover the rest: the first product has no registers for more
+// (233), the second no workgroups (224 of eight wavefronts for 256 CUs).  Calls under 50
 // MB are the two launches' and three dependent loads' latency (routing, weights, sums).
 //
 // Times in the comments below compare two builds that differ in that point alone;
@@ -659,8 +660,8 @@ constexpr int kLinWaves = 8;
 
 // One workgroup: RT*16 rows of the weight, all columns split over the waves, 16 T
 // rows of x (blockIdx.y).  Eight wavefronts, so that 7168 columns are four steps each:
-// one row by 7168 x 7168 int4 takes 7.7 us (3.4 TB/s of 26.5 MB, 4 us of it latency),
-// 64 rows by 7168 x 2048 with zero points 11.0 us (each of two row groups reads all
+// one row by 7168 x 7168 int4 takes 7.3 us (3.6 TB/s of 26.5 MB, 4 us of it latency),
+// 64 rows by 7168 x 2048 with zero points 9.9 us (each of two row groups reads all
 // codes, from L2 the second time).
 template <int F, int RT, int T, bool PART>
 __global__ __launch_bounds__(64 * kLinWaves) void linear_kernel(
@@ -922,7 +923,10 @@ __device__ __forceinline__ void up_tokens(const MoeArgs& a, Routing& r, const Ga
       u += part[((i + 1) * S::tokens + t) * 16 + (c & 15)];
     }
     const int pair = r.pair[pos0 + t];
-    // the one rounding between the products: the second one's operand is bf16
+    // The one rounding between the products: the second one's MFMA takes bf16, and a
+    // second operand for what that loses would double its products and its reads of
+    // these rows.  Off by 2^-8 of a value at most, the layer by 0.0024 of y's norm
+    // (0.0017 is y's own rounding).
     if (pair >= 0 && i0 + c < a.I)
       a.hidden[(int64_t)((pair >> kPairShift) * a.K + (pair & ((1 << kPairShift) - 1))) * a.I +
                i0 + c] = bf16_bits(r.weight[pos0 + t] * (silu(g) * u));

@@ -15,10 +15,10 @@
 // a wavefront whose groups were not clear, or that has more such experts than lanes,
 // repeats the whole selection in 64 bits (choose_exact).
 //
-// One wavefront's chain of num_topk maxima is latency, so is a call: 6.0 us for one
+// One wavefront's chain of num_topk maxima is latency, so is a call: 5.8 us for one
 // token of 256 experts, of which an empty launch is 3.5.  4096 tokens of 256 experts (4.5
-// MB) take 11.4 us with VALU busy 61% of the time and 16384 of 256 in bf16 (9.4 MB)
-// 14.0 us with 92%: the selection is bound by instructions, not by HBM (1.3 us).
+// MB) take 11.2 us with VALU busy 63% of the time and 16384 of 256 in bf16 (9.4 MB)
+// 13.7 us with 97%: this selection's instructions are what counts, not HBM (1.3 us).
 #include "ep_host.h"
 
 #include <algorithm>

@@ -318,12 +318,14 @@ int ep_ll_dispatch_ex(const ep_problem_t* p, int32_t max_tokens_per_rank, const 
  *   weight_k = scale * s_k, divided by the sum of the chosen s if renormalize.
  * Equal values go to the lowest expert (and group).  The selection is the one
  * that scores in 64 bits make: neighbours at the border are ordered as the
- * formula orders them; without a bias the experts are ordered by their logits
- * themselves.  The weights are computed in float32.
+ * formula orders them; without a bias the experts (and with group_top 1 the
+ * groups) are ordered by their logits themselves.  The weights are computed in
+ * float32.
  * A logit of -inf or NaN masks its expert: it is never chosen, and a group with
  * fewer than group_top unmasked experts comes after all others.  Where fewer
  * than num_topk experts are left, the remaining entries are -1 with weight 0.
  * +inf counts as the largest finite float.
+ *   num_tokens    N * num_topk at most 2^31 - 1
  *   logits        [N][E] float32 (logits_bytes 4) or bf16 (2)
  *   bias          [E] float32, finite, or NULL
  *   num_groups    1..64, divides E; 1 <= topk_groups <= num_groups;
