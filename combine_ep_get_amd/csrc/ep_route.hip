@@ -13,7 +13,8 @@
 // decision was clear by more than the error bound (error_of).  Experts that were
 // not clear of each other are ranked again by their 64-bit scores, one per lane;
 // a wavefront whose groups were not clear, or that has more such experts than lanes,
-// repeats the whole selection in 64 bits (choose_exact).
+// repeats the whole selection in 64 bits (choose_exact).  4096 tokens of 256 experts with
+// a bias, no groups: 8 us, and 38 where no token is clear (all scores 1 in float32).
 //
 // One wavefront's chain of num_topk maxima is latency, so is a call: 5.8 us for one
 // token of 256 experts, of which an empty launch is 3.5.  4096 tokens of 256 experts (4.5
