@@ -103,22 +103,54 @@ class MoeArgs(ctypes.Structure):
                 ("inter", ctypes.c_int32)]
 
 
+class RowsDesc(ctypes.Structure):
+    _fields_ = [("offset", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("capacity", ctypes.c_int64), ("num_experts", ctypes.c_int32),
+                ("num_sources", ctypes.c_int32), ("rows_per_source", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32)]
+
+
+class FfnArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w13", WeightDesc), ("w2", WeightDesc),
+                ("y", ctypes.c_void_p), ("gate_up", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("hidden", ctypes.c_int32),
+                ("inter", ctypes.c_int32)]
+
+
+class FfnGradArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("dy", "x", "gate_up", "w13", "w2", "dx", "dw13", "dw2", "workspace")] + \
+        [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32)]
+
+
+class Int8Args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("w", WeightDesc),
+                ("y", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("cols", ctypes.c_int32), ("out_rows", ctypes.c_int32)]
+
+
 # The same structs as bytes, for calls whose time is the host's: packing them is
 # several times quicker than filling a ctypes structure.
 _PROBLEM = struct.Struct("@9i").pack
 _ROUTE_ARGS = struct.Struct("@4P10if4x").pack
 _WEIGHT_DESC = struct.Struct("@3P2i").pack
 _MOE_ARGS = struct.Struct("@3P3P2i3P2i2Pi4x").pack
+_ROWS = struct.Struct("@2Pq4i").pack
+_FFN_ARGS = struct.Struct("@P3P2i3P2i3P2i").pack
+_FFN_GRAD_ARGS = struct.Struct("@9P2i").pack
+_INT8_ARGS = struct.Struct("@2P3P2i2P2i").pack
 
 EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX = 0, 1
-EP_WEIGHT_BF16, EP_WEIGHT_INT4, EP_WEIGHT_MXFP4 = 0, 1, 2
+EP_WEIGHT_BF16, EP_WEIGHT_INT4, EP_WEIGHT_MXFP4, EP_WEIGHT_INT8 = 0, 1, 2, 3
 EP_MAX_FEW_TOKENS = 256
 EP_MAX_CONTRACTION = 65536
 
 EXPORTS = ("ep_recv_capacity", "ep_workspace_bytes", "ep_get_layout", "ep_dispatch",
            "ep_dispatch_ex", "ep_combine", "ep_layout_error", "ep_status_str", "ep_ll_capacity",
            "ep_ll_dispatch", "ep_ll_dispatch_ex", "ep_get_layout_noalloc",
-           "ep_route", "ep_moe_workspace_bytes", "ep_moe_layer", "ep_quant_linear")
+           "ep_route", "ep_moe_workspace_bytes", "ep_moe_layer", "ep_quant_linear",
+           "ep_ffn_workspace_bytes", "ep_ffn", "ep_ffn_backward", "ep_combine_backward",
+           "ep_quantize_int8", "ep_int8_workspace_bytes", "ep_int8_linear")
 EP_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 2 << 20
 EP_LAYOUT_ERR_OVERFLOW = 2
@@ -179,6 +211,20 @@ def load(path):
     L.ep_moe_layer.argtypes = [vp, vp, vp]
     L.ep_quant_linear.restype = ctypes.c_int
     L.ep_quant_linear.argtypes = [ctypes.c_int32] * 3 + [vp] * 4
+    L.ep_ffn_workspace_bytes.restype = i64
+    L.ep_ffn_workspace_bytes.argtypes = [vp] + [ctypes.c_int32] * 4
+    L.ep_ffn.restype = ctypes.c_int
+    L.ep_ffn.argtypes = [vp, vp, vp]
+    L.ep_ffn_backward.restype = ctypes.c_int
+    L.ep_ffn_backward.argtypes = [vp, vp, vp]
+    L.ep_combine_backward.restype = ctypes.c_int
+    L.ep_combine_backward.argtypes = [vp] * 7 + [i64, vp]
+    L.ep_quantize_int8.restype = ctypes.c_int
+    L.ep_quantize_int8.argtypes = [i64, ctypes.c_int32] + [vp] * 4
+    L.ep_int8_workspace_bytes.restype = i64
+    L.ep_int8_workspace_bytes.argtypes = [vp, ctypes.c_int32]
+    L.ep_int8_linear.restype = ctypes.c_int
+    L.ep_int8_linear.argtypes = [vp, vp, vp]
     return L
 
 
@@ -775,6 +821,276 @@ def quant_linear(x, w, out=None):
     return out
 
 
+# ------------------------------------------- the experts' block and its gradients
+class Int8Weight:
+    """An 8-bit integer weight [rows, cols] or, of a stack of experts, [E, rows, cols] on
+    the GPU: ``codes`` int8 and ``scales`` float32 [..., rows], one per output channel;
+    value = scale * code.  It shares the tensors' memory (changed values count) and is
+    fixed otherwise: its attributes are read-only, and a call on a weight whose memory
+    was resized or freed since raises."""
+
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dim() not in (2, 3) or codes.shape[-1] % 16 != 0:
+            raise ValueError(f"codes: need [rows, cols] or [E, rows, cols] with cols % 16 == 0, "
+                             f"got {tuple(codes.shape)}")
+        _arg(codes, torch.int8, codes.shape, "codes", codes)
+        _arg(scales, torch.float32, codes.shape[:-1], "scales", codes)
+        codes, scales = codes.detach(), scales.detach()
+        self.__dict__.update(codes=codes, scales=scales, shape=tuple(codes.shape),
+                             device=codes.device,
+                             desc=(codes.data_ptr(), scales.data_ptr(), 0, EP_WEIGHT_INT8, 0))
+
+    @classmethod
+    def from_weight(cls, w):
+        """A bf16 weight rounded to 8-bit integers, a scale per row (quantize_int8)."""
+        codes, scales = quantize_int8(w.reshape(-1, w.shape[-1]))
+        return cls(codes.view(w.shape), scales.view(w.shape[:-1]))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"Int8Weight.{name} is read-only: make a new Int8Weight")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"Int8Weight.{name} is read-only")
+
+    def __reduce__(self):
+        return Int8Weight, (self.codes, self.scales)
+
+    def get_device(self):
+        return self.codes.get_device()
+
+    def checked_desc(self):
+        """desc, if the memory is still where it was."""
+        if self.codes.data_ptr() != self.desc[0] or self.scales.data_ptr() != self.desc[1]:
+            raise ValueError("Int8Weight: the memory of its tensors was resized or freed")
+        return self.desc
+
+
+def _rows(x, layout, lead, name):
+    """ep_rows_t of x's rows as bytes: of a Layout, an LLLayout, or (None) a plain matrix.
+    ``lead`` is the weight's leading shape: (E,), or () for a plain matrix."""
+    import torch
+    cap = x.shape[0]
+    if layout is None:
+        if lead != ():
+            raise ValueError(f"{name}: without a layout it has no expert axis")
+        return _ROWS(0, 0, cap, 1, 1, 0, cap)
+    E = layout.num_experts
+    if lead != (E,):
+        raise ValueError(f"{name}: need the {E} experts of the layout, got {tuple(lead)}")
+    most = layout.num_tokens * layout.num_topk
+    if isinstance(layout, LLLayout):
+        if cap < layout.capacity:
+            raise ValueError(f"x: need the {layout.capacity} rows of the layout, got {cap}")
+        R = layout.num_ranks
+        _arg(layout.recv_count, torch.int32, (E, R), "recv_count", x)
+        return _ROWS(0, layout.recv_count.data_ptr(), cap, E, R, layout.max_tokens_per_rank, most)
+    _arg(layout.expert_slot_offset, torch.int32, (E + 1,), "expert_slot_offset", x)
+    _arg(layout.num_recv_per_expert, torch.int32, (E,), "num_recv_per_expert", x)
+    return _ROWS(layout.expert_slot_offset.data_ptr(), layout.num_recv_per_expert.data_ptr(), cap,
+                 E, 1, 0, most)
+
+
+def _workspace(workspace, need, ref):
+    import torch
+    if need < 0:
+        raise ValueError("invalid problem sizes")
+    if workspace is None:
+        return ref.new_empty((need,), dtype=torch.uint8)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace: need {need} bytes, got {workspace.numel()}")
+    _arg(workspace, torch.uint8, workspace.shape, "workspace", ref)
+    return workspace
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_bytes(rows, hidden, inter, int8, backward):
+    # its size depends on the rows of the buffers alone
+    return int(lib().ep_ffn_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), hidden, inter,
+                                            EP_WEIGHT_INT8 if int8 else EP_WEIGHT_BF16,
+                                            1 if backward else 0))
+
+
+def ffn_workspace_bytes(rows, hidden, inter, int8=False, backward=False):
+    """Bytes of workspace of expert_ffn (or expert_ffn_backward) on buffers of ``rows``."""
+    v = _ffn_bytes(int(rows), int(hidden), int(inter), bool(int8), bool(backward))
+    if v < 0:
+        raise ValueError("invalid problem sizes")
+    return v
+
+
+def alloc_ffn_workspace(rows, hidden, inter, int8=False, backward=False, device="cuda"):
+    """The workspace of expert_ffn or, ``backward``, expert_ffn_backward calls on buffers
+    of up to ``rows`` rows (one per stream; a captured graph needs its own)."""
+    import torch
+    return torch.empty((ffn_workspace_bytes(rows, hidden, inter, int8, backward),),
+                       dtype=torch.uint8, device=device)
+
+
+def _ffn_weight(w, name, shape, ref):
+    """(leading shape, descriptor) of one of the block's weights [*lead, *shape]."""
+    import torch
+    lead, got = tuple(w.shape[:-2]), tuple(w.shape[-2:])
+    if got != shape:
+        raise ValueError(f"{name}: need [..., {shape[0]}, {shape[1]}], got {tuple(w.shape)}")
+    if isinstance(w, Int8Weight):
+        if w.get_device() != ref.get_device():
+            raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
+        return lead, w.checked_desc()
+    _arg(w, torch.bfloat16, w.shape, name, ref)
+    return lead, (w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0)
+
+
+def expert_ffn(x, w13, w2, layout=None, out=None, gate_up=None, workspace=None):
+    """The gated feed-forward block of every expert on its rows of ``x`` [cap, H] bf16:
+    y = (silu(x Wg^T) * (x Wu^T)) W2^T (see ep_ffn).  ``layout`` says where the rows lie:
+    a Layout (x = recv_x of dispatch), an LLLayout (of ll_dispatch), or None for a plain
+    matrix, whose weights have no expert axis.  ``w13`` [E, 2*I, H] (gate rows first) and
+    ``w2`` [E, H, I] are bf16 tensors or both Int8Weight.  Slots without a row are
+    neither read nor written.  ``out`` [cap, H]; ``gate_up`` [cap, 2*I] bf16 receives
+    what expert_ffn_backward needs; ``workspace`` from alloc_ffn_workspace."""
+    import torch
+    cap, H = x.shape
+    I = w2.shape[-1]
+    int8 = isinstance(w13, Int8Weight)
+    if int8 != isinstance(w2, Int8Weight):
+        raise ValueError("w13 and w2: need the same kind of weight")
+    _arg(x, torch.bfloat16, (cap, H), "x", x)
+    lead, d13 = _ffn_weight(w13, "w13", (2 * I, H), x)
+    lead2, d2 = _ffn_weight(w2, "w2", (H, I), x)
+    if lead2 != lead:
+        raise ValueError(f"w2: need {lead} experts, got {lead2}")
+    rows = _rows(x, layout, lead, "w13")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _arg(out, torch.bfloat16, (cap, H), "y", x)
+    if gate_up is not None:
+        _arg(gate_up, torch.bfloat16, (cap, 2 * I), "gate_up", x)
+    workspace = _workspace(workspace, _ffn_bytes(cap, H, I, int8, False), x)
+    _call(lib().ep_ffn, "ep_ffn", x, rows,
+          _FFN_ARGS(x.data_ptr(), *d13, *d2, out.data_ptr(),
+                    0 if gate_up is None else gate_up.data_ptr(), workspace.data_ptr(), H, I))
+    return out
+
+
+def expert_ffn_backward(dy, x, gate_up, w13, w2, layout=None, out=None, workspace=None):
+    """The gradients (dx, dw13, dw2) of expert_ffn from ``dy`` [cap, H], with ``x``,
+    the ``gate_up`` that expert_ffn wrote, and bf16 weights (see ep_ffn_backward).
+    ``layout`` is a Layout or None.  ``out`` is a triple of preallocated gradients, all
+    bf16; slots without a row are neither read nor written (dx keeps what it held
+    there), experts without rows get zero gradients."""
+    import torch
+    cap, H = x.shape
+    I = w2.shape[-1]
+    if isinstance(layout, LLLayout):
+        raise ValueError("layout: need a Layout or None, the low-latency path has no backward")
+    _arg(x, torch.bfloat16, (cap, H), "x", x)
+    _arg(dy, torch.bfloat16, (cap, H), "dy", x)
+    _arg(gate_up, torch.bfloat16, (cap, 2 * I), "gate_up", x)
+    for w, name in ((w13, "w13"), (w2, "w2")):
+        if isinstance(w, Int8Weight):
+            raise ValueError(f"{name}: need a bf16 tensor")
+    lead, _ = _ffn_weight(w13, "w13", (2 * I, H), x)
+    lead2, _ = _ffn_weight(w2, "w2", (H, I), x)
+    if lead2 != lead:
+        raise ValueError(f"w2: need {lead} experts, got {lead2}")
+    rows = _rows(x, layout, lead, "w13")
+    if out is None:
+        out = torch.empty_like(x), torch.empty_like(w13), torch.empty_like(w2)
+    dx, dw13, dw2 = out
+    _arg(dx, torch.bfloat16, (cap, H), "dx", x)
+    _arg(dw13, torch.bfloat16, w13.shape, "dw13", x)
+    _arg(dw2, torch.bfloat16, w2.shape, "dw2", x)
+    workspace = _workspace(workspace, _ffn_bytes(cap, H, I, False, True), x)
+    _call(lib().ep_ffn_backward, "ep_ffn_backward", x, rows,
+          _FFN_GRAD_ARGS(dy.data_ptr(), x.data_ptr(), gate_up.data_ptr(), w13.data_ptr(),
+                         w2.data_ptr(), dx.data_ptr(), dw13.data_ptr(), dw2.data_ptr(),
+                         workspace.data_ptr(), H, I))
+    return dx, dw13, dw2
+
+
+def combine_backward(dy, expert_out, layout, topk_weights, out=None):
+    """The gradients (d_expert_out [cap, H] bf16, d_topk_weights [N, K] float32) of
+    combine from ``dy`` [N, H] bf16 (see ep_combine_backward); rows of d_expert_out that
+    no pair names keep what ``out`` held.  The gradient of dispatch's x is
+    combine(d_recv_x, layout, ones)."""
+    import torch
+    cap, H = expert_out.shape
+    N, K = layout.num_tokens, layout.num_topk
+    _arg(dy, torch.bfloat16, (N, H), "dy", dy)
+    _arg(expert_out, torch.bfloat16, (cap, H), "expert_out", dy)
+    _arg(layout.slot_of, torch.int32, (N, K), "slot_of", dy)
+    _arg(topk_weights, torch.float32, (N, K), "topk_weights", dy)
+    if out is None:
+        out = torch.empty_like(expert_out), torch.empty_like(topk_weights)
+    deo, dwts = out
+    _arg(deo, torch.bfloat16, (cap, H), "d_expert_out", dy)
+    _arg(dwts, torch.float32, (N, K), "d_topk_weights", dy)
+    _call(lib().ep_combine_backward, "ep_combine_backward", dy,
+          _PROBLEM(N, H, K, layout.num_experts, layout.num_ranks, 1, 0, 4, 0), dy.data_ptr(),
+          expert_out.data_ptr(), layout.slot_of.data_ptr(), topk_weights.data_ptr(),
+          deo.data_ptr(), dwts.data_ptr(), cap)
+    return deo, dwts
+
+
+def quantize_int8(x, out=None):
+    """Rows of ``x`` [rows, cols] bf16 as (codes int8 [rows, cols], scales float32 [rows]),
+    scale = amax / 127 (see ep_quantize_int8)."""
+    import torch
+    rows, cols = x.shape
+    _arg(x, torch.bfloat16, (rows, cols), "x", x)
+    if out is None:
+        out = x.new_empty((rows, cols), dtype=torch.int8), x.new_empty((rows,),
+                                                                       dtype=torch.float32)
+    codes, scales = out
+    _arg(codes, torch.int8, (rows, cols), "codes", x)
+    _arg(scales, torch.float32, (rows,), "scales", x)
+    _call(lib().ep_quantize_int8, "ep_quantize_int8", x, rows, cols, x.data_ptr(),
+          codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+@functools.lru_cache(maxsize=256)
+def _int8_bytes(rows, cols):
+    return int(lib().ep_int8_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), cols))
+
+
+def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
+    """y = x W^T in 8-bit integers with a scale per row and per output channel, bf16
+    [cap, out_rows] (see ep_int8_linear).  ``x`` [cap, cols] is bf16, rounded by
+    quantize_int8 on the way, or int8 codes with their ``x_scales`` [cap]; ``w`` an
+    Int8Weight [out_rows, cols], or [E, out_rows, cols] with the ``layout`` (Layout or
+    LLLayout) that says which rows are whose.  Slots without a row are neither read nor
+    written.  ``workspace``: ep_int8_workspace_bytes(cap, cols) bytes."""
+    import torch
+    if not isinstance(w, Int8Weight):
+        raise ValueError("w: need an Int8Weight")
+    cap, C = x.shape
+    O = w.shape[-2]
+    if w.shape[-1] != C:
+        raise ValueError(f"w: need [..., {C}], got {w.shape}")
+    if w.get_device() != x.get_device():
+        raise ValueError(f"w is on {w.device}, expected {x.device}")
+    rows = _rows(x, layout, w.shape[:-2], "w")
+    if x_scales is None:
+        _arg(x, torch.bfloat16, (cap, C), "x", x)
+        workspace = _workspace(workspace, _int8_bytes(cap, C), x)
+    else:
+        _arg(x, torch.int8, (cap, C), "x", x)
+        _arg(x_scales, torch.float32, (cap,), "x_scales", x)
+        workspace = None
+    if out is None:
+        out = x.new_empty((cap, O), dtype=torch.bfloat16)
+    else:
+        _arg(out, torch.bfloat16, (cap, O), "y", x)
+    _call(lib().ep_int8_linear, "ep_int8_linear", x, rows,
+          _INT8_ARGS(x.data_ptr(), 0 if x_scales is None else x_scales.data_ptr(),
+                     *w.checked_desc(), out.data_ptr(),
+                     0 if workspace is None else workspace.data_ptr(), C, O))
+    return out
+
+
 # The other C entry points under their own names, for callers who read
 # include/ep_get.h: each is the function above that marshals that entry
 # point's arguments from tensors.
@@ -791,3 +1107,17 @@ ep_route = route
 ep_moe_workspace_bytes = moe_workspace_bytes
 ep_moe_layer = moe_layer
 ep_quant_linear = quant_linear
+ep_ffn_workspace_bytes = ffn_workspace_bytes
+ep_ffn = expert_ffn
+ep_ffn_backward = expert_ffn_backward
+ep_combine_backward = combine_backward
+ep_quantize_int8 = quantize_int8
+ep_int8_linear = int8_linear
+
+
+def ep_int8_workspace_bytes(rows, cols):
+    """Bytes of workspace of int8_linear on a bf16 x of ``rows`` rows."""
+    v = _int8_bytes(int(rows), int(cols))
+    if v < 0:
+        raise ValueError("invalid problem sizes")
+    return v

@@ -12,8 +12,9 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ep_get.hip")
-# the rest of libepget: the router, and the experts' products
-MORE_SRC = [os.path.join(HERE, "csrc", n) for n in ("ep_route.hip", "ep_moe.hip")]
+# the rest of libepget: the router, the experts' products, and what works on their rows
+MORE_SRC = [os.path.join(HERE, "csrc", n)
+            for n in ("ep_route.hip", "ep_moe.hip", "ep_ffn.hip", "ep_rowops.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libepget.so")

@@ -1,0 +1,221 @@
+// ep_rowops.hip -- rows as 8-bit integers, and combine's gradient (include/ep_get.h
+// states the contracts).  Both read each row once and are bound by HBM.
+#include "ep_host.h"
+#include "ep_rows.h"
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ void unpack8(u32x4 r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[2 * i] = __builtin_bit_cast(float, r[i] << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, r[i] & 0xFFFF0000u);
+  }
+}
+
+// ---------------------------------------------------------------- 8-bit integers
+// Codes of eight values.  q = rint(x * inv) is off by one at most, next to a half: the
+// remainder x - q * s is exact there (q has 7 bits, s 24, x 8, and they cancel), so its
+// comparison with s / 2 decides as the exact quotient would, halves to even.
+__device__ __forceinline__ u32x2 codes8(u32x4 raw, float up, float inv, float s) {
+  float v[8];
+  unpack8(raw, v);
+  u32x2 out = {0, 0};
+  const float half = 0.5f * s;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float x = v[i] * up;
+    float q = rintf(x * inv);
+    const float r = fmaf(-q, s, x);
+    const bool odd = ((int)q & 1) != 0;
+    if (r > half || (r == half && odd)) q += 1.f;
+    if (-r > half || (-r == half && odd)) q -= 1.f;
+    const int c = (int)fminf(127.f, fmaxf(-127.f, q));
+    out[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+  }
+  return out;
+}
+
+constexpr int kHeld = 16;      // 16-byte chunks per lane that stay in registers: 8192 columns
+
+// A wavefront per row; blocks (segment, part): segments are the experts, or the sub-blocks
+// of ep_ll_dispatch, whose rows are shared out over the parts.
+template <int CH>
+__global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t* x, int cols,
+                                                       uint8_t* codes, float* scales) {
+  const int seg = blockIdx.x, l = threadIdx.x & 63;
+  int first, n;
+  if (rows.count && !rows.offset) {
+    first = seg * rows.M;
+    n = max(0, min(rows.count[seg], rows.M));
+  } else {
+    first = rows.first_slot(seg);
+    n = rows.rows_of(seg);
+  }
+  const int chunks = cols / 8;
+  for (int64_t j = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); j < n; j += gridDim.y * 4) {
+    const int64_t slot = first + j;
+    const u32x4* in = (const u32x4*)(x + slot * cols * 2);
+    u32x2* out = (u32x2*)(codes + slot * cols);
+    u32x4 held[CH];
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+      held[i] = i * 64 + l < chunks ? in[i * 64 + l] : u32x4{0, 0, 0, 0};
+    // magnitudes of bf16 are ordered as their bits are, infinities and NaN last
+    uint32_t top = 0;
+    auto look = [&](u32x4 r) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) top = max(top, max(r[i] & 0x7FFFu, (r[i] >> 16) & 0x7FFFu));
+    };
+#pragma unroll
+    for (int i = 0; i < CH; i++) look(held[i]);
+    for (int c = CH * 64 + l; c < chunks; c += 64) look(in[c]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    const float amax = __builtin_bit_cast(float, top << 16);
+    float s = amax / 127.f;
+    if (top == 0) s = 1.f;
+    if (l == 0) scales[slot] = top >= 0x7F80u ? __builtin_bit_cast(float, 0x7FC00000u) : s;
+    // tiny rows are taken 2^64 times as large (exact), where 1 / s would overflow
+    const float up = amax < 0x1p-100f && top != 0 ? 0x1p64f : 1.f;
+    const float su = s * up, inv = 1.f / su;
+    const bool finite = top < 0x7F80u;
+    auto put = [&](int c, u32x4 r) {
+      out[c] = finite ? codes8(r, up, inv, su) : u32x2{0, 0};
+    };
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+      if (i * 64 + l < chunks) put(i * 64 + l, held[i]);
+    for (int c = CH * 64 + l; c < chunks; c += 64) put(c, in[c]);
+  }
+}
+
+// ---------------------------------------------------------------- combine's gradient
+constexpr int kPairs = 8;      // pairs of a token handled together
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+// A workgroup per token: dy's row is read once for all pairs, 16 bytes per thread and
+// step; the K sums meet in LDS at the end, in a fixed order.
+__global__ __launch_bounds__(256) void combine_backward_kernel(
+    const u32x4* dy, const u32x4* eo, const int* slot_of, const float* wts, u32x4* deo,
+    float* dwts, int H8, int K, int cap) {
+  __shared__ float sums[4][kPairs];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  for (int k0 = 0; k0 < K; k0 += kPairs) {
+    int slot[kPairs];
+    float w[kPairs], sum[kPairs];
+#pragma unroll
+    for (int k = 0; k < kPairs; k++) {
+      const bool in = k0 + k < K;
+      slot[k] = in ? slot_of[t * K + k0 + k] : -1;
+      if (slot[k] >= cap) slot[k] = -1;
+      w[k] = in ? wts[t * K + k0 + k] : 0.f;
+      sum[k] = 0.f;
+    }
+    for (int c = tid; c < H8; c += 256) {
+      const u32x4 g = dy[t * H8 + c];
+      u32x4 o[kPairs];
+#pragma unroll
+      for (int k = 0; k < kPairs; k++)
+        if (slot[k] >= 0) o[k] = eo[(int64_t)slot[k] * H8 + c];
+      float gf[8];
+      unpack8(g, gf);
+#pragma unroll
+      for (int k = 0; k < kPairs; k++) {
+        if (slot[k] < 0) continue;
+        float of[8];
+        unpack8(o[k], of);
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; i++) r[i] = pack2(w[k] * gf[2 * i], w[k] * gf[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum[k] = fmaf(of[i], gf[i], sum[k]);
+        __builtin_nontemporal_store(r, deo + (int64_t)slot[k] * H8 + c);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPairs; k++) {
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) sum[k] += __shfl_xor(sum[k], d);
+      if ((tid & 63) == 0) sums[tid >> 6][k] = sum[k];
+    }
+    __syncthreads();
+    if (tid < kPairs && k0 + tid < K)
+      dwts[t * K + k0 + tid] = sums[0][tid] + sums[1][tid] + sums[2][tid] + sums[3][tid];
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+namespace ep {
+
+int quantize_rows(const Rows& rows, int max_rows, const void* x, int cols, void* codes,
+                  float* scales, hipStream_t st) {
+  const int segments = rows.count && !rows.offset ? rows.E * rows.R : rows.E;
+  // four rows per workgroup and pass, at most about 16 workgroups per CU; at least twice
+  // the average segment, so that an uneven one takes few passes
+  const int64_t per = ((int64_t)max_rows / segments + 1) * 2;
+  int64_t parts = (per + 3) / 4;
+  const int64_t most = segments >= 4096 ? 1 : 4096 / segments;
+  if (parts > most) parts = most;
+  const dim3 grid(segments, (int)parts);
+  const uint8_t* in = (const uint8_t*)x;
+  if (cols <= 2048)
+    quantize_kernel<4><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
+  else
+    quantize_kernel<kHeld><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
+  return check_launch("quantize_rows");
+}
+
+}  // namespace ep
+
+extern "C" {
+
+int ep_quantize_int8(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
+                     void* stream) {
+  if (num_rows < 0 || num_rows > INT32_MAX || !valid_width(cols, EP_WEIGHT_INT8))
+    return EP_ERR_INVALID_ARG;
+  if (num_rows == 0) return EP_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned(scales, 4))
+    return EP_ERR_INVALID_ARG;
+  int rc = check_device();
+  if (rc != EP_OK) return rc;
+  const Rows r{nullptr, nullptr, (int)num_rows, 1, 1, 0, (int)num_rows};
+  return quantize_rows(r, (int)num_rows, x, cols, codes, scales, (hipStream_t)stream);
+}
+
+int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* expert_out,
+                        const int32_t* slot_of, const float* topk_weights, void* d_expert_out,
+                        float* d_topk_weights, int64_t recv_capacity, void* stream) {
+  int rc = validate_layout(p);
+  if (rc != EP_OK) return rc;
+  const int H = p->hidden, N = p->num_tokens;
+  if (H <= 0 || H > EP_MAX_HIDDEN || H % 8 != 0 || (p->use_fp8 != 0 && p->use_fp8 != 1) ||
+      recv_capacity < 0 || recv_capacity > INT32_MAX)
+    return EP_ERR_INVALID_ARG;
+  if (N == 0) return EP_OK;
+  if (!dy || !slot_of || !topk_weights || !d_topk_weights ||
+      (recv_capacity > 0 && (!expert_out || !d_expert_out)) || !aligned16(dy) ||
+      !aligned16(expert_out) || !aligned16(d_expert_out))
+    return EP_ERR_INVALID_ARG;
+  rc = check_device();
+  if (rc != EP_OK) return rc;
+  EP_LOG("combine_backward N=%d H=%d K=%d cap=%lld", N, H, p->num_topk, (long long)recv_capacity);
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  combine_backward_kernel<<<dim3(N), dim3(256), 0, (hipStream_t)stream>>>(
+      (const u32x4*)dy, (const u32x4*)expert_out, slot_of, topk_weights, (u32x4*)d_expert_out,
+      d_topk_weights, H / 8, p->num_topk, (int)recv_capacity);
+  return check_launch("combine_backward");
+}
+
+}  // extern "C"

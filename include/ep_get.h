@@ -427,6 +427,152 @@ int ep_moe_layer(const ep_problem_t* p, const ep_moe_args_t* args, void* stream)
 int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void* x,
                     const ep_weight_t* w, void* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The experts' block on dispatched rows, its gradient, and 8-bit integer
+ * products.  Same conventions as above.  What stands between dispatch and
+ * combine works on the rows of each expert, wherever they lie in a buffer of
+ * `capacity` rows (recv_x and every buffer beside it):
+ *   offset and count given   ep_get_layout's expert_slot_offset [E+1] and
+ *                            num_recv_per_expert [E]: rows of expert e are
+ *                            slots offset[e] .. offset[e] + count[e] - 1
+ *   count alone              ep_ll_dispatch's recv_count [E][R], R = num_sources,
+ *                            M = rows_per_source: the first count[e][s] rows of
+ *                            sub-block (e, s) at slot (e*R + s)*M;
+ *                            E*R*M <= capacity
+ *   neither                  a plain matrix: num_experts 1, rows 0 .. max_rows - 1
+ *                            (max_rows <= capacity), a weight without the expert axis
+ * Rows of no expert (padding, the end of the buffer) are neither read nor
+ * written: outputs keep what they held there, inputs may hold anything, NaN too.
+ *   capacity         0..INT32_MAX
+ *   num_experts      1..EP_MAX_EXPERTS
+ *   num_sources      1 (with offset, or plain), 1..EP_MAX_RANKS
+ *   rows_per_source  0 (with offset, or plain), >= 1
+ *   max_rows         0..INT32_MAX: a bound of all counts together (N*K).  It picks
+ *                    launch shapes; more rows than that are computed just the same,
+ *                    except that 0 launches nothing
+ * Counts and offsets come from the device as they are: what reaches outside of
+ * [0, capacity) (or of M) is cut off there. */
+typedef struct ep_rows {
+  const int32_t* offset;
+  const int32_t* count;
+  int64_t capacity;
+  int32_t num_experts;
+  int32_t num_sources;
+  int32_t rows_per_source;
+  int32_t max_rows;
+} ep_rows_t;
+
+/* 8-bit integer weights: data [rows][cols] int8, scales [rows] float32 (one per
+ * output channel), value = scale * code; zeros and group ignored; cols % 16 == 0;
+ * data 16-byte aligned.  Taken by ep_ffn and ep_int8_linear. */
+enum { EP_WEIGHT_INT8 = 3 };
+
+/* The gated feed-forward block of each expert on its rows:
+ *   g = x Wg^T, u = x Wu^T, h = silu(g) * u, y = h W2^T
+ * bf16: products accumulate in float32; h is rounded to bf16 as the input of the
+ * second product, y once.
+ * EP_WEIGHT_INT8: rows of x, and of h after its rounding to bf16, become 8-bit
+ * integers as by ep_int8_linear; the integer sums are exact.
+ * The values of a row of x reach that row of y only.  Deterministic.
+ *   x          [capacity][hidden] bf16
+ *   w13        [E][2*inter][hidden]: rows 0..inter-1 are Wg, the rest Wu; bf16 or
+ *              EP_WEIGHT_INT8
+ *   w2         [E][hidden][inter], in the same format
+ *   y          [capacity][hidden] bf16 out; must not overlap x
+ *   gate_up    [capacity][2*inter] bf16 out, g and u (rounded) for
+ *              ep_ffn_backward, or NULL
+ *   workspace  ep_ffn_workspace_bytes (backward = 0); 256-byte aligned; no
+ *              initialisation; calls that overlap need their own
+ *   hidden, inter  % 8 == 0 (bf16) or % 16 == 0 (int8), at most EP_MAX_CONTRACTION
+ * Tensors are 16-byte aligned. */
+typedef struct ep_ffn_args {
+  const void* x;
+  ep_weight_t w13;
+  ep_weight_t w2;
+  void* y;
+  void* gate_up;
+  void* workspace;
+  int32_t hidden;
+  int32_t inter;
+} ep_ffn_args_t;
+int64_t ep_ffn_workspace_bytes(const ep_rows_t* rows, int32_t hidden, int32_t inter, int32_t format,
+                               int32_t backward);
+int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* args, void* stream);
+
+/* Its gradient (bf16 weights; ep_get_layout's rows or a plain matrix):
+ *   dh = dy W2;  s = sigmoid(g);  dg = dh * u * s * (1 + g * (1 - s));  du = dh * g * s
+ *   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dW2 = dy^T h
+ * float32 accumulation; dg, du and h are rounded to bf16 as inputs of their
+ * products, the gradients once.  An expert without rows has zero gradients
+ * (written).  Deterministic.
+ *   dy, x      [capacity][hidden] bf16;  gate_up as ep_ffn wrote it
+ *   w13, w2    the bf16 weights
+ *   dx         [capacity][hidden] bf16 out
+ *   dw13, dw2  in the shapes of the weights, bf16 out (overwritten)
+ *   workspace  ep_ffn_workspace_bytes (backward = 1); 256-byte aligned
+ * No output overlaps an input.  With max_rows 0 the weights' gradients are zeroed. */
+typedef struct ep_ffn_grad_args {
+  const void* dy;
+  const void* x;
+  const void* gate_up;
+  const void* w13;
+  const void* w2;
+  void* dx;
+  void* dw13;
+  void* dw2;
+  void* workspace;
+  int32_t hidden;
+  int32_t inter;
+} ep_ffn_grad_args_t;
+int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* args, void* stream);
+
+/* Combine's gradient.  With y as ep_combine makes it, for every pair with a slot:
+ *   d_expert_out[slot_of[t][k]] = topk_weights[t][k] * dy[t]
+ *   d_topk_weights[t][k] = sum over c of expert_out[slot_of[t][k]][c] * dy[t][c]
+ * in float32, d_expert_out rounded to bf16 once; 0 for a pair without a slot
+ * (slot_of outside [0, recv_capacity)).  Rows of d_expert_out that no pair names
+ * keep what they held.  Deterministic.  (Dispatch's own gradient is ep_combine of
+ * the rows' gradients with unit weights.)
+ *   dy            [N][H] bf16;  expert_out [recv_capacity][H] bf16
+ *   d_expert_out  [recv_capacity][H] bf16 out; may be expert_out
+ *   d_topk_weights [N][K] float32 out
+ * hidden, num_tokens, num_topk as for ep_combine; use_fp8 and cu_budget are only
+ * checked. */
+int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* expert_out,
+                        const int32_t* slot_of, const float* topk_weights, void* d_expert_out,
+                        float* d_topk_weights, int64_t recv_capacity, void* stream);
+
+/* Rows of bf16 as 8-bit integers with a scale each:
+ *   scale = amax / 127 (one float32 division; 1 where amax is 0),
+ *   code = x / scale rounded to the nearest integer, halves to even (decided on the
+ *   exact quotient), within [-127, 127].
+ * A row with an infinity or a NaN gets a NaN scale and codes 0.
+ *   x [num_rows][cols] bf16, codes [num_rows][cols] int8, scales [num_rows] float32;
+ *   cols % 16 == 0, at most EP_MAX_CONTRACTION; x and codes 16-byte aligned and apart */
+int ep_quantize_int8(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
+                     void* stream);
+
+/* y = x W^T in 8-bit integers: y[r][o] = bf16(x_scale[r] * w_scale[o] * sum over c of
+ * x_code[r][c] * w_code[o][c]), the sum exact in 32 bits, on each expert's rows.
+ *   x          [capacity][cols]: bf16, rounded as by ep_quantize_int8 in the
+ *              workspace; or, with x_scales [capacity] float32, int8 codes
+ *   w          EP_WEIGHT_INT8 [E][out_rows][cols]
+ *   y          [capacity][out_rows] bf16 out; must not overlap x
+ *   workspace  ep_int8_workspace_bytes, 256-byte aligned; not read with x_scales
+ *   cols % 16 == 0, at most EP_MAX_CONTRACTION; out_rows 1..EP_MAX_HIDDEN
+ * x, y and w.data are 16-byte aligned.  Deterministic. */
+typedef struct ep_int8_args {
+  const void* x;
+  const float* x_scales;
+  ep_weight_t w;
+  void* y;
+  void* workspace;
+  int32_t cols;
+  int32_t out_rows;
+} ep_int8_args_t;
+int64_t ep_int8_workspace_bytes(const ep_rows_t* rows, int32_t cols);
+int ep_int8_linear(const ep_rows_t* rows, const ep_int8_args_t* args, void* stream);
+
 /* SYNCHRONOUS debug query: waits for `stream`, then stores the error word of
  * the last ep_get_layout that used `workspace` into *flags (host pointer).
  * Bits: EP_LAYOUT_ERR_INDEX. */
