@@ -150,7 +150,7 @@ EXPORTS = ("ep_recv_capacity", "ep_workspace_bytes", "ep_get_layout", "ep_dispat
            "ep_ll_dispatch", "ep_ll_dispatch_ex", "ep_get_layout_noalloc",
            "ep_route", "ep_moe_workspace_bytes", "ep_moe_layer", "ep_quant_linear",
            "ep_ffn_workspace_bytes", "ep_ffn", "ep_ffn_backward", "ep_combine_backward",
-           "ep_quantize_int8", "ep_int8_workspace_bytes", "ep_int8_linear")
+           "ep_quantize_rows", "ep_integer_workspace_bytes", "ep_integer_linear")
 EP_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 2 << 20
 EP_LAYOUT_ERR_OVERFLOW = 2
@@ -219,12 +219,12 @@ def load(path):
     L.ep_ffn_backward.argtypes = [vp, vp, vp]
     L.ep_combine_backward.restype = ctypes.c_int
     L.ep_combine_backward.argtypes = [vp] * 7 + [i64, vp]
-    L.ep_quantize_int8.restype = ctypes.c_int
-    L.ep_quantize_int8.argtypes = [i64, ctypes.c_int32] + [vp] * 4
-    L.ep_int8_workspace_bytes.restype = i64
-    L.ep_int8_workspace_bytes.argtypes = [vp, ctypes.c_int32]
-    L.ep_int8_linear.restype = ctypes.c_int
-    L.ep_int8_linear.argtypes = [vp, vp, vp]
+    L.ep_quantize_rows.restype = ctypes.c_int
+    L.ep_quantize_rows.argtypes = [i64, ctypes.c_int32] + [vp] * 4
+    L.ep_integer_workspace_bytes.restype = i64
+    L.ep_integer_workspace_bytes.argtypes = [vp, ctypes.c_int32]
+    L.ep_integer_linear.restype = ctypes.c_int
+    L.ep_integer_linear.argtypes = [vp, vp, vp]
     return L
 
 
@@ -1036,7 +1036,7 @@ def combine_backward(dy, expert_out, layout, topk_weights, out=None):
 
 def quantize_int8(x, out=None):
     """Rows of ``x`` [rows, cols] bf16 as (codes int8 [rows, cols], scales float32 [rows]),
-    scale = amax / 127 (see ep_quantize_int8)."""
+    scale = amax / 127 (see ep_quantize_rows)."""
     import torch
     rows, cols = x.shape
     _arg(x, torch.bfloat16, (rows, cols), "x", x)
@@ -1046,23 +1046,23 @@ def quantize_int8(x, out=None):
     codes, scales = out
     _arg(codes, torch.int8, (rows, cols), "codes", x)
     _arg(scales, torch.float32, (rows,), "scales", x)
-    _call(lib().ep_quantize_int8, "ep_quantize_int8", x, rows, cols, x.data_ptr(),
+    _call(lib().ep_quantize_rows, "ep_quantize_rows", x, rows, cols, x.data_ptr(),
           codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 @functools.lru_cache(maxsize=256)
 def _int8_bytes(rows, cols):
-    return int(lib().ep_int8_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), cols))
+    return int(lib().ep_integer_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), cols))
 
 
 def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
     """y = x W^T in 8-bit integers with a scale per row and per output channel, bf16
-    [cap, out_rows] (see ep_int8_linear).  ``x`` [cap, cols] is bf16, rounded by
+    [cap, out_rows] (see ep_integer_linear).  ``x`` [cap, cols] is bf16, rounded by
     quantize_int8 on the way, or int8 codes with their ``x_scales`` [cap]; ``w`` an
     Int8Weight [out_rows, cols], or [E, out_rows, cols] with the ``layout`` (Layout or
     LLLayout) that says which rows are whose.  Slots without a row are neither read nor
-    written.  ``workspace``: ep_int8_workspace_bytes(cap, cols) bytes."""
+    written.  ``workspace``: ep_integer_workspace_bytes(cap, cols) bytes."""
     import torch
     if not isinstance(w, Int8Weight):
         raise ValueError("w: need an Int8Weight")
@@ -1084,7 +1084,7 @@ def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
         out = x.new_empty((cap, O), dtype=torch.bfloat16)
     else:
         _arg(out, torch.bfloat16, (cap, O), "y", x)
-    _call(lib().ep_int8_linear, "ep_int8_linear", x, rows,
+    _call(lib().ep_integer_linear, "ep_integer_linear", x, rows,
           _INT8_ARGS(x.data_ptr(), 0 if x_scales is None else x_scales.data_ptr(),
                      *w.checked_desc(), out.data_ptr(),
                      0 if workspace is None else workspace.data_ptr(), C, O))
@@ -1111,11 +1111,11 @@ ep_ffn_workspace_bytes = ffn_workspace_bytes
 ep_ffn = expert_ffn
 ep_ffn_backward = expert_ffn_backward
 ep_combine_backward = combine_backward
-ep_quantize_int8 = quantize_int8
-ep_int8_linear = int8_linear
+ep_quantize_rows = quantize_int8
+ep_integer_linear = int8_linear
 
 
-def ep_int8_workspace_bytes(rows, cols):
+def ep_integer_workspace_bytes(rows, cols):
     """Bytes of workspace of int8_linear on a bf16 x of ``rows`` rows."""
     v = _int8_bytes(int(rows), int(cols))
     if v < 0:

@@ -669,12 +669,12 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   return check_launch("ep_ffn_backward dw2");
 }
 
-int64_t ep_int8_workspace_bytes(const ep_rows_t* rows, int32_t cols) {
+int64_t ep_integer_workspace_bytes(const ep_rows_t* rows, int32_t cols) {
   if (validate_rows(rows) != EP_OK || !valid_width(cols, EP_WEIGHT_INT8)) return -1;
   return up(rows->capacity * cols) + up(rows->capacity * 4);
 }
 
-int ep_int8_linear(const ep_rows_t* rows, const ep_int8_args_t* a, void* stream) {
+int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* a, void* stream) {
   int rc = validate_rows(rows);
   if (rc != EP_OK) return rc;
   if (!a || !valid_width(a->cols, EP_WEIGHT_INT8) || a->out_rows < 1 ||

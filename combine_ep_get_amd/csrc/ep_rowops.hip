@@ -181,7 +181,7 @@ int quantize_rows(const Rows& rows, int max_rows, const void* x, int cols, void*
 
 extern "C" {
 
-int ep_quantize_int8(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
+int ep_quantize_rows(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
                      void* stream) {
   if (num_rows < 0 || num_rows > INT32_MAX || !valid_width(cols, EP_WEIGHT_INT8))
     return EP_ERR_INVALID_ARG;

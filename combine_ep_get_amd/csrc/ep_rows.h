@@ -42,7 +42,7 @@ struct Rows {            // kernel argument
   }
 };
 
-// A row quantiser for other sources (ep_quantize_int8 on the rows of Rows).
+// A row quantiser for other sources (ep_quantize_rows on the rows of Rows).
 __attribute__((visibility("hidden"))) int quantize_rows(const Rows& rows, int max_rows,
                                                         const void* x, int cols, void* codes,
                                                         float* scales, hipStream_t st);

@@ -464,7 +464,7 @@ typedef struct ep_rows {
 
 /* 8-bit integer weights: data [rows][cols] int8, scales [rows] float32 (one per
  * output channel), value = scale * code; zeros and group ignored; cols % 16 == 0;
- * data 16-byte aligned.  Taken by ep_ffn and ep_int8_linear. */
+ * data 16-byte aligned.  Taken by ep_ffn and ep_integer_linear. */
 enum { EP_WEIGHT_INT8 = 3 };
 
 /* The gated feed-forward block of each expert on its rows:
@@ -472,7 +472,7 @@ enum { EP_WEIGHT_INT8 = 3 };
  * bf16: products accumulate in float32; h is rounded to bf16 as the input of the
  * second product, y once.
  * EP_WEIGHT_INT8: rows of x, and of h after its rounding to bf16, become 8-bit
- * integers as by ep_int8_linear; the integer sums are exact.
+ * integers as by ep_integer_linear; the integer sums are exact.
  * The values of a row of x reach that row of y only.  Deterministic.
  *   x          [capacity][hidden] bf16
  *   w13        [E][2*inter][hidden]: rows 0..inter-1 are Wg, the rest Wu; bf16 or
@@ -549,19 +549,19 @@ int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* exper
  * A row with an infinity or a NaN gets a NaN scale and codes 0.
  *   x [num_rows][cols] bf16, codes [num_rows][cols] int8, scales [num_rows] float32;
  *   cols % 16 == 0, at most EP_MAX_CONTRACTION; x and codes 16-byte aligned and apart */
-int ep_quantize_int8(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
+int ep_quantize_rows(int64_t num_rows, int32_t cols, const void* x, int8_t* codes, float* scales,
                      void* stream);
 
 /* y = x W^T in 8-bit integers: y[r][o] = bf16(x_scale[r] * w_scale[o] * sum over c of
  * x_code[r][c] * w_code[o][c]), the sum exact in 32 bits, on each expert's rows.
- *   x          [capacity][cols]: bf16, rounded as by ep_quantize_int8 in the
+ *   x          [capacity][cols]: bf16, rounded as by ep_quantize_rows in the
  *              workspace; or, with x_scales [capacity] float32, int8 codes
  *   w          EP_WEIGHT_INT8 [E][out_rows][cols]
  *   y          [capacity][out_rows] bf16 out; must not overlap x
- *   workspace  ep_int8_workspace_bytes, 256-byte aligned; not read with x_scales
+ *   workspace  ep_integer_workspace_bytes, 256-byte aligned; not read with x_scales
  *   cols % 16 == 0, at most EP_MAX_CONTRACTION; out_rows 1..EP_MAX_HIDDEN
  * x, y and w.data are 16-byte aligned.  Deterministic. */
-typedef struct ep_int8_args {
+typedef struct ep_integer_args {
   const void* x;
   const float* x_scales;
   ep_weight_t w;
@@ -569,9 +569,9 @@ typedef struct ep_int8_args {
   void* workspace;
   int32_t cols;
   int32_t out_rows;
-} ep_int8_args_t;
-int64_t ep_int8_workspace_bytes(const ep_rows_t* rows, int32_t cols);
-int ep_int8_linear(const ep_rows_t* rows, const ep_int8_args_t* args, void* stream);
+} ep_integer_args_t;
+int64_t ep_integer_workspace_bytes(const ep_rows_t* rows, int32_t cols);
+int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* args, void* stream);
 
 /* SYNCHRONOUS debug query: waits for `stream`, then stores the error word of
  * the last ep_get_layout that used `workspace` into *flags (host pointer).
