@@ -7,8 +7,6 @@
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -20,7 +18,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRange = 0x60000000;     // bytes that a buffer descriptor spans
 constexpr int kAbsent = 0x7F000000;    // an offset outside of it: the load returns zeros
-constexpr int kBN = 256;               // columns of a tile
+constexpr int kBM = 256, kBN = 256;    // rows and columns of a tile
+constexpr int kHalf = 16384;           // bytes of half of either operand's tile (128 by 128 bytes)
+constexpr int kStage = 4 * kHalf;      // a's two halves, b's two halves
+constexpr int kSteps = 2;              // stages in LDS
 constexpr int kGroupM = 8;             // row tiles that are neighbours in the order of tiles
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -47,11 +48,18 @@ struct Product {            // kernel argument
 // waits are written out at the loop.  The s_nop covers a descriptor word or base that a
 // VALU instruction has just written (five wait states), which the compiler cannot see
 // here, and m0.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds(uint32_t lds, int offset, i32x4 desc) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(lds), "v"(offset), "s"(desc)
-               : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(uniform((int)lds)), "v"(offset), "s"(desc)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(uniform((int)lds)), "v"(offset), "s"(desc)
+                 : "memory");
 }
 
 template <int N>
@@ -85,14 +93,6 @@ __device__ __forceinline__ u32x4 pack8(const float* v) {
     r[i] = __builtin_bit_cast(uint32_t, p);
   }
   return r;
-}
-
-__device__ __forceinline__ void unpack8(u32x4 r, float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    v[2 * i] = __builtin_bit_cast(float, r[i] << 16);
-    v[2 * i + 1] = __builtin_bit_cast(float, r[i] & 0xFFFF0000u);
-  }
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
@@ -224,9 +224,11 @@ __device__ __forceinline__ typename Acc<I8>::type mfma(u32x4 a, u32x4 b,
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// One operand's half tile in LDS: R rows by 128 bytes of k (16-byte chunk c of row r at
-// c ^ (r & 7)), or, where k is the slow axis, 64 k by 128 columns (256 bytes; chunk c of
-// row k at c ^ 4 (k & 3)): no two lanes of a read share a bank.
+// One operand's half tile in LDS: rows by 128 bytes of k (16-byte chunk c of row r at
+// c ^ (r / 2 & 7)), or, where k is the slow axis, 64 k by 128 columns (256 bytes; chunk c of
+// row k at c ^ 4 (k & 3)): no two lanes that LDS serves together share a bank.  (It
+// serves lanes 0-3, 12-15 and 20-27 of a 16-byte read together: with c ^ (r & 7) half of
+// the time went into conflicts.)
 template <bool SLOW_K>
 __device__ __forceinline__ u32x4 fragment(const uint8_t* half, int lane_off, int ks) {
   if constexpr (SLOW_K) {
@@ -241,85 +243,114 @@ __device__ __forceinline__ u32x4 fragment(const uint8_t* half, int lane_off, int
   }
 }
 
-template <int KIND, class Epi, bool I8, int BM>
+template <int KIND, class Epi, bool I8>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void product_kernel(Product p, Epi epi) {
-  constexpr int kHalfA = BM / 2 * 128, kHalfB = 16384;     // bytes
-  constexpr int kStage = 2 * kHalfA + 2 * kHalfB;
-  constexpr int NA = BM / 128, NB = 2;                     // loads per wavefront and half
-  constexpr int WM = BM / 4, MB = WM / 32;                 // a wavefront's rows of a half
   constexpr bool kSlowA = KIND == kOuter, kSlowB = KIND != kRowsT;
-  static_assert(KIND != kOuter || BM == 256, "k-major tiles of 128 rows only");
   using acc_t = typename Acc<I8>::type;
   using val_t = typename Acc<I8>::scalar;
 
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
-  __shared__ int first_tile[EP_MAX_EXPERTS + 1];
-  __shared__ int slot_of_row[BM];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps * kStage];
+  __shared__ int first_tile[EP_MAX_EXPERTS + 1], first_short[EP_MAX_EXPERTS + 1];
+  __shared__ int slot_of_row[2][kBM];    // the epilogue's tile, and the one being loaded
 
   const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
-  const int wm = w >> 2, wn = w & 3;
+  const int wm = w >> 2, wn = w & 3;     // rows wm*64.., columns wn*32.. of each half
   const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
   const int NT = KIND == kRowsT && p.far ? (p.n + 127) / 128 : (p.n + kBN - 1) / kBN;
-  const int MT = (p.m + BM - 1) / BM;                      // kOuter
-  int total;
+  const int MT = (p.m + kBM - 1) / kBM;                    // kOuter
+  int total, tall = 0;                                     // tiles, those of over 128 rows
   if constexpr (KIND == kOuter) {
     total = p.rows.E * MT * NT;
   } else {
-    scan_tiles(p.rows, BM, first_tile);
-    total = uniform(first_tile[p.rows.E]) * NT;
+    scan_tiles(p.rows, kBM, first_tile, first_short);
+    tall = uniform(first_tile[p.rows.E]) * NT;
+    total = tall + uniform(first_short[p.rows.E]) * NT;
   }
 
-  // where this lane's bytes of a load go, and where it reads
-  const int chunk_k = (l & 7) ^ (l >> 3);                  // of 128 bytes of a row
+  // where this lane's bytes of a load go (a wavefront sends two loads per half: rows
+  // w*16 + 8 j + l/8, or k w*8 + 4 j + l/16), and where it reads
   const int chunk_n = (l & 15) ^ ((l >> 4) << 2);          // of 128 columns of a k
-  const int read_k = (l & 31) * 128 + ((((l >> 5) ^ (l & 7))) << 4);
+  auto chunk_k = [&](int j) { return (l & 7) ^ ((j << 2) + (l >> 4)); };   // of a row
+  const int read_k = (l & 31) * 128 + (((l >> 5) ^ ((l >> 1) & 7)) << 4);
   const int i16 = l & 15;
   auto read_n = [&](int chunk) {
     return ((l >> 5) * 8 + (i16 >> 2)) * 256 +
            (((chunk + ((l >> 4) & 1) * 2 + ((i16 & 3) >> 1)) ^ ((i16 >> 2) << 2)) << 4) +
            (i16 & 1) * 8;
   };
-  int read_a[MB];
+  int read_a[2];
 #pragma unroll
-  for (int mb = 0; mb < MB; mb++)
-    read_a[mb] = kSlowA ? read_n(wm * 8 + mb * 4) : (wm * WM + mb * 32) * 128 + read_k;
+  for (int mb = 0; mb < 2; mb++)
+    read_a[mb] = kSlowA ? read_n(wm * 8 + mb * 4) : (wm * 64 + mb * 32) * 128 + read_k;
   const int read_b = kSlowB ? read_n(wn * 4) : wn * 32 * 128 + read_k;
 
-  // workgroup ids go round robin over the 8 XCDs: give each XCD neighbouring tiles
-  const int G = gridDim.x;
-  const int me = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
-  for (int tile = me; tile < total; tile += G) {
-    // ---- which tile
-    int e = 0, mt, nt, nrows, KT;
-    int row0, slot0 = 0;
-    const uint8_t *a0, *b0;
+  // ---- the tile whose loads are under way
+  int e = 0, nt = 0, nrows = 0, row0 = 0, KT = 0;
+  int k_a = 0, k_b = 0;        // contraction of a and b in what their tail counts
+  const uint8_t *a0 = nullptr, *b0 = nullptr;
+  int off_a[2][2], off_b[2][2];
+  const int64_t far = (int64_t)p.far * p.b_row;
+  const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
+
+  auto load_a = [&](int t, int h) {
+    const i32x4 d = descriptor(a0 + t * step_a);
+    const uint32_t to = lds0 + (t & 1) * kStage + h * kHalf + w * 2048;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const bool in = kSlowA ? w * 8 + j * 4 + (l >> 4) < k_a - t * 64
+                             : chunk_k(j) * 16 < k_a - t * 128;
+      load_lds<false>(to + j * 1024, in ? off_a[h][j] : kAbsent, d);
+    }
+  };
+  auto load_b = [&](int t, int h) {
+    const i32x4 d = descriptor(b0 + t * step_b + h * far);
+    const uint32_t to = lds0 + (t & 1) * kStage + (2 + h) * kHalf + w * 2048;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const bool in = kSlowB ? w * 8 + j * 4 + (l >> 4) < k_b - t * 64
+                             : chunk_k(j) * 16 < k_b - t * 128;
+      load_lds<KIND == kRowsT>(to + j * 1024, in ? off_b[h][j] : kAbsent, d);
+    }
+  };
+  auto load_first = [&](int t) {         // what the first phase of step t reads
+    load_b(t, 0);
+    load_a(t, 0);
+    load_b(t, 1);
+  };
+
+  // Finds tile `tile` and sends the loads of its first step.
+  auto begin = [&](int tile, int* slots) {
+    int slot0;
     if constexpr (KIND == kOuter) {
       e = tile / (MT * NT);
       const int r = tile - e * MT * NT;
       const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, MT - f);
       const int q = r - g * kGroupM * NT;
-      mt = f + q % gs;
+      row0 = (f + q % gs) * kBM;
       nt = q / gs;
-      row0 = mt * BM;
-      nrows = min(BM, p.m - row0);
-      const int cnt = uniform(p.rows.rows_of(e));
-      KT = (cnt + 63) / 64;
+      nrows = min(kBM, p.m - row0);
+      k_a = k_b = uniform(p.rows.rows_of(e));
+      KT = (k_a + 63) / 64;
       slot0 = uniform(p.rows.first_slot(e));
       a0 = p.a + (int64_t)slot0 * p.a_row + (int64_t)row0 * 2;
       b0 = p.b + (int64_t)slot0 * p.b_row + (int64_t)nt * kBN * 2;
-      p.k = cnt;
     } else {
-      e = find_expert(first_tile, p.rows.E, tile / NT);
-      const int f0 = uniform(first_tile[e]), mts = uniform(first_tile[e + 1]) - f0;
-      const int r = tile - f0 * NT;
+      // the short ones last: they take half the time, and a workgroup whose share was all
+      // tall ones would keep the others waiting
+      const bool is_short = tile >= tall;
+      const int at = is_short ? tile - tall : tile;
+      const int* first = is_short ? first_short : first_tile;
+      e = find_expert(first, p.rows.E, at / NT);
+      const int f0 = uniform(first[e]), mts = uniform(first[e + 1]) - f0;
+      const int r = at - f0 * NT;
       const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, mts - f);
       const int q = r - g * kGroupM * NT;
-      mt = f + q % gs;
+      row0 = (f + q % gs) * kBM;
+      if (is_short) row0 = (uniform(first_tile[e + 1]) - uniform(first_tile[e])) * kBM;
       nt = q / gs;
-      row0 = mt * BM;
-      nrows = min(BM, uniform(p.rows.rows_of(e)) - row0);
-      if (tid < BM) slot_of_row[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
+      nrows = min(kBM, uniform(p.rows.rows_of(e)) - row0);
+      if (tid < kBM) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
       slot0 = uniform(p.rows.base_slot(e, row0));
       a0 = p.a + (int64_t)slot0 * p.a_row;
       b0 = p.b + (int64_t)e * p.b_expert;
@@ -327,196 +358,596 @@ void product_kernel(Product p, Epi epi) {
         b0 += (int64_t)nt * (p.far ? 128 : kBN) * p.b_row;
       else
         b0 += (int64_t)nt * kBN * 2;
+      k_a = p.k;
+      k_b = KIND == kRows ? p.k / 2 : p.k;    // rows of b, or bytes of its rows
       KT = (p.k + 127) / 128;
       __syncthreads();
     }
-
-    // ---- offsets of this lane's loads from a0 and b0
-    int off_a[2][NA], off_b[2][NB];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < 2; h++)
 #pragma unroll
-      for (int j = 0; j < NA; j++) {
+      for (int j = 0; j < 2; j++) {
+        const int r = w * 16 + j * 8 + (l >> 3), k = w * 8 + j * 4 + (l >> 4);
+        const int c = h * 128 + chunk_n * 8;
         if constexpr (kSlowA) {
-          const int c = h * 128 + chunk_n * 8;
-          off_a[h][j] = c < nrows ? ((w * NA + j) * 4 + (l >> 4)) * (int)p.a_row + c * 2 : kAbsent;
+          off_a[h][j] = c < nrows ? k * (int)p.a_row + c * 2 : kAbsent;
         } else {
-          const int s = slot_of_row[h * (BM / 2) + (w * NA + j) * 8 + (l >> 3)];
-          off_a[h][j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k * 16 : kAbsent;
+          const int s = slots[h * 128 + r];
+          off_a[h][j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
         }
+        if constexpr (kSlowB)
+          off_b[h][j] = nt * kBN + c < p.n ? k * (int)p.b_row + c * 2 : kAbsent;
+        else if (p.far)
+          off_b[h][j] = nt * 128 + r < p.n ? (int)(r * p.b_row) + chunk_k(j) * 16 : kAbsent;
+        else
+          off_b[h][j] = nt * kBN + h * 128 + r < p.n
+                            ? (int)((r + h * 128) * p.b_row) + chunk_k(j) * 16 : kAbsent;
       }
-#pragma unroll
-      for (int j = 0; j < NB; j++) {
-        if constexpr (kSlowB) {
-          const int c = h * 128 + chunk_n * 8;
-          off_b[h][j] = nt * kBN + c < p.n
-                            ? ((w * NB + j) * 4 + (l >> 4)) * (int)p.b_row + c * 2 : kAbsent;
-        } else {
-          const int c = (w * NB + j) * 8 + (l >> 3);
-          if (p.far)
-            off_b[h][j] = nt * 128 + c < p.n ? (int)(c * p.b_row) + chunk_k * 16 : kAbsent;
-          else
-            off_b[h][j] = nt * kBN + h * 128 + c < p.n
-                              ? (int)((c + h * 128) * p.b_row) + chunk_k * 16 : kAbsent;
-        }
-      }
-    }
+    if (KT == 0) return;
+    load_first(0);
+    load_a(0, 1);
+  };
 
-    const int64_t far = (int64_t)p.far * p.b_row;
-    const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
-    auto load_a = [&](int t, int h) {
-      const i32x4 d = descriptor(a0 + t * step_a);
-      const uint32_t to = lds0 + (t & 1) * kStage + h * kHalfA + w * NA * 1024;
+  // workgroup ids go round robin over the 8 XCDs: give each XCD neighbouring tiles
+  const int G = gridDim.x;
+  int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  if (tile >= total) return;
+  int* slots = slot_of_row[0];
+  begin(tile, slots);
+  for (;;) {
+    acc_t acc[2][2][2];
 #pragma unroll
-      for (int j = 0; j < NA; j++) {
-        const bool in = kSlowA ? (w * NA + j) * 4 + (l >> 4) < p.k - t * 64
-                               : chunk_k * 16 < p.k - t * 128;
-        load_lds(to + j * 1024, in ? off_a[h][j] : kAbsent, d);
-      }
-    };
-    // k of b's rows: p.k counts bytes of a's rows where those hold k
-    const int k_b = KIND == kRows ? p.k / 2 : p.k;
-    auto load_b = [&](int t, int h) {
-      const i32x4 d = descriptor(b0 + t * step_b + h * far);
-      const uint32_t to = lds0 + (t & 1) * kStage + 2 * kHalfA + h * kHalfB + w * NB * 1024;
-#pragma unroll
-      for (int j = 0; j < NB; j++) {
-        const bool in = kSlowB ? (w * NB + j) * 4 + (l >> 4) < k_b - t * 64
-                               : chunk_k * 16 < k_b - t * 128;
-        load_lds(to + j * 1024, in ? off_b[h][j] : kAbsent, d);
-      }
-    };
+    for (int i = 0; i < 8; i++) acc[i >> 2][(i >> 1) & 1][i & 1] = acc_t{};
 
     // ---- the loop.  Two groups of four wavefronts, one of each group on every SIMD,
-    // half a phase apart: while one group's MFMAs run, the other reads its next
-    // fragments and sends loads.  A half tile is loaded again as soon as both groups
-    // have read it: its reads have returned (wait_lds) before the barrier behind which
-    // the load is sent.
-    acc_t acc[2][2][MB];
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-      for (int j = 0; j < 2; j++)
-#pragma unroll
-        for (int k = 0; k < MB; k++) acc[i][j][k] = acc_t{};
-
+    // one phase's half apart: while one group's MFMAs run, the other reads its next
+    // fragments and sends loads.  Phases per step: b and a's first half, a's second half.
+    // Loads run one step and a phase ahead; a half tile is loaded again as soon as both
+    // groups have read it: reads have returned (wait_lds) before the barrier behind which
+    // the load is sent, and a load has arrived (wait_loads) one barrier before it is read.
     if (KT > 0) {
-      load_b(0, 0);
-      load_a(0, 0);
-      load_b(0, 1);
-      load_a(0, 1);
-      load_b(1, 0);
-      load_a(1, 0);
-      load_b(1, 1);
-      wait_loads<2 * NB + NA>();
+      load_first(1);
+      wait_loads<8>();
       barrier();
       if (wm == 1) barrier();
+      const bool any0 = wm * 64 < nrows, any1 = 128 + wm * 64 < nrows;
       for (int t = 0; t < KT; t++) {
         const uint8_t* st = lds + (t & 1) * kStage;
-        u32x4 fa[MB][4], fb[2][4];
+        u32x4 fa[2][4], fb[2][4];
         auto read_as = [&](int h) {
 #pragma unroll
-          for (int mb = 0; mb < MB; mb++)
+          for (int mb = 0; mb < 2; mb++)
 #pragma unroll
             for (int ks = 0; ks < 4; ks++)
-              fa[mb][ks] = fragment<kSlowA>(st + h * kHalfA, read_a[mb], ks);
+              fa[mb][ks] = fragment<kSlowA>(st + h * kHalf, read_a[mb], ks);
         };
-        auto read_bs = [&](int h) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ks++)
-            fb[h][ks] = fragment<kSlowB>(st + 2 * kHalfA + h * kHalfB, read_b, ks);
-        };
-        auto multiply = [&](int qm, int qn) {
-          wait_lds();
-          barrier();
+        auto multiply = [&](int h) {
           __builtin_amdgcn_s_setprio(1);
 #pragma unroll
           for (int ks = 0; ks < 4; ks++)
 #pragma unroll
-            for (int mb = 0; mb < MB; mb++)
-              acc[qm][qn][mb] = mfma<I8>(fb[qn][ks], fa[mb][ks], acc[qm][qn][mb]);
+            for (int i = 0; i < 4; i++)
+              acc[h][i >> 1][i & 1] =
+                  mfma<I8>(fb[i >> 1][ks], fa[i & 1][ks], acc[h][i >> 1][i & 1]);
           __builtin_amdgcn_s_setprio(0);
-          barrier();
         };
-        read_bs(0);
-        read_as(0);
+        if (any0) {
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int ks = 0; ks < 4; ks++)
+              fb[h][ks] = fragment<kSlowB>(st + (2 + h) * kHalf, read_b, ks);
+          read_as(0);
+        }
         load_a(t + 1, 1);
-        multiply(0, 0);
-        read_bs(1);
-        load_b(t + 2, 0);
-        multiply(0, 1);
-        read_as(1);
-        load_a(t + 2, 0);
-        multiply(1, 1);
-        load_b(t + 2, 1);
-        wait_loads<2 * NB + NA>();
-        multiply(1, 0);
+        wait_loads<8>();
+        wait_lds();
+        barrier();
+        if (any0) multiply(0);
+        barrier();
+        if (any1) read_as(1);
+        load_first(t + 2);
+        wait_loads<8>();
+        wait_lds();
+        barrier();
+        if (any1) multiply(1);
+        barrier();
       }
+      wait_loads<0>();               // those behind the last step: zeros
       if (wm == 0) barrier();
-      wait_loads<0>();
     }
 
-    // ---- epilogue: through LDS, so that a lane has eight neighbouring columns
+    // ---- this tile's results are in registers: the next tile's first step loads meanwhile
+    const int e_ = e, nt_ = nt, nrows_ = nrows, row0_ = row0;
+    const int* slots_ = slots;
+    tile += G;
+    const bool more = tile < total;
+    if (more) {
+      slots = slots == slot_of_row[0] ? slot_of_row[1] : slot_of_row[0];
+      begin(tile, slots);
+    }
+
+    // Blocks of 32 by 32 through LDS, where a lane's four columns of a row become eight
+    // of another: stores of 64 bytes of a row.  It is the part of the second stage that
+    // this wavefront's own next loads fill, so that no other one is waited for.
+    uint8_t* mine = lds + kStage + w * 2048;
+    auto turn = [&](const acc_t& v, int at) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      __syncthreads();
+      for (int i = 0; i < 4; i++) {
+        u32x4 q;
 #pragma unroll
-      for (int mb = 0; mb < MB; mb++) {
-        const int row = wm * WM + mb * 32 + (l & 31);
-#pragma unroll
-        for (int qn = 0; qn < 2; qn++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int c = qn * 32 + wn * 8 + 2 * i + (l >> 5);
-            u32x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-              v[j] = __builtin_bit_cast(uint32_t, (val_t)acc[h][qn][mb][i * 4 + j]);
-            *(u32x4*)(lds + row * 1024 + ((c ^ (l & 31)) << 4)) = v;
-          }
+        for (int j = 0; j < 4; j++)
+          q[j] = __builtin_bit_cast(uint32_t, (val_t)v[i * 4 + j]);
+        const int r = l & 31;
+        *(u32x4*)(mine + (at + (r >> 4)) * kHalf + (r & 15) * 128 +
+                  (((2 * i + (l >> 5)) ^ ((r >> 1) & 7)) << 4)) = q;
       }
-      __syncthreads();
-      constexpr int kChunks = Epi::gate ? 16 : 32;
-#pragma unroll 2
-      for (int i = tid; i < BM / 2 * kChunks; i += 512) {
-        const int r = i / kChunks, c = i % kChunks, x = r & 31;
-        if (h * (BM / 2) + r >= nrows) break;
-        val_t v[8], u[8];
-        auto take = [&](int chunk, val_t* to) {
+    };
+    auto take = [&](int it, int at, val_t* to) {
+      const int r = l >> 2;              // of 16; `it` which 16
 #pragma unroll
-          for (int q = 0; q < 2; q++) {
-            const u32x4 t = *(const u32x4*)(lds + r * 1024 + (((chunk + q) ^ x) << 4));
+      for (int q = 0; q < 2; q++) {
+        const u32x4 x = *(const u32x4*)(mine + (at + it) * kHalf + r * 128 +
+                                        (((2 * (l & 3) + q) ^ ((r >> 1) & 7)) << 4));
 #pragma unroll
-            for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)t[j]);
-          }
-        };
-        take(2 * c, v);
-        if constexpr (Epi::gate) take(32 + 2 * c, u);
-        const int row = KIND == kOuter ? row0 + h * (BM / 2) + r : slot_of_row[h * (BM / 2) + r];
-        epi(e, row, nt * (Epi::gate ? 128 : kBN) + c * 8, v, u);
+        for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)x[j]);
       }
+    };
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int mb = 0; mb < 2; mb++) {
+        const int r0 = h * 128 + wm * 64 + mb * 32;
+        if (r0 >= nrows_) continue;
+#pragma unroll
+        for (int qn = 0; qn < (Epi::gate ? 1 : 2); qn++) {
+          turn(acc[h][qn][mb], 0);
+          if constexpr (Epi::gate) turn(acc[h][1][mb], 2);
+#pragma unroll
+          for (int it = 0; it < 2; it++) {
+            val_t v[8], u[8];
+            take(it, 0, v);
+            if constexpr (Epi::gate) take(it, 2, u);
+            const int r = r0 + it * 16 + (l >> 2);
+            if (r >= nrows_) continue;
+            const int row = KIND == kOuter ? row0_ + r : slots_[r];
+            epi(e_, row, nt_ * (Epi::gate ? 128 : kBN) + qn * 128 + wn * 32 + (l & 3) * 8, v, u);
+          }
+        }
+      }
+    if (!more) break;
+    wait_lds();
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Rows that are too few to fill 256-row tiles: a workgroup takes 32 rows of the weight (16
+// of gate and 16 of up) and 16 TT rows of x, its four wavefronts take every fourth 128
+// bytes of the contraction, each with loads of its own running ahead in LDS of its own, so
+// that there is no barrier before the sums meet at the end.
+// FUSE: at most 16 rows of x in bf16, which every workgroup rounds to 8-bit integers
+// itself while its first weights are on their way.
+template <bool I8>
+struct Acc4 {
+  using type = std::conditional_t<I8, i32x4, f32x4>;
+};
+
+template <bool I8>
+__device__ __forceinline__ typename Acc4<I8>::type mfma16(u32x4 a, u32x4 b,
+                                                          typename Acc4<I8>::type c) {
+  if constexpr (I8)
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+constexpr int kFuseBytes = 32768;      // codes of x in LDS
+
+template <class Epi, bool I8, int TT, bool FUSE>
+__global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
+  constexpr int kRowsX = 16 * TT, kCols = Epi::gate ? 16 : 32;
+  constexpr int kW = 4096, kX = FUSE ? 0 : kRowsX * 128;     // bytes of a stage
+  constexpr int kDepth = FUSE ? 7 : TT == 1 ? 3 : 2;
+  constexpr int kLoads = 4 + (FUSE ? 0 : 2 * TT);
+  constexpr int kMine = kDepth * (kW + kX);
+  using acc_t = typename Acc4<I8>::type;
+  using val_t = typename Acc<I8>::scalar;
+  static_assert(kMine >= kRowsX * 32 * 4, "a wavefront's sums fit where its stages were");
+
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kMine + (FUSE ? kFuseBytes : 0)];
+  __shared__ int first_tile[EP_MAX_EXPERTS + 1];
+  __shared__ int slots[kRowsX];
+  __shared__ float scale[16];
+  __shared__ uint32_t tops[4];
+
+  const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
+  const uint32_t mine = lds0 + w * kMine;
+  const uint8_t* my = lds + w * kMine;
+  const int NT = (p.n + kCols - 1) / kCols, KT = (p.k + 127) / 128, NI = (KT + 3) / 4;
+  int total = NT;
+  if constexpr (!FUSE) {
+    scan_tiles(p.rows, kRowsX, first_tile);
+    total = uniform(first_tile[p.rows.E]) * NT;
+  }
+  const int64_t far = (int64_t)p.far * p.b_row;
+  auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
+  const int read = (l & 15) * 128 + (((l >> 4) ^ ((l >> 1) & 7)) << 4);
+  const int G = gridDim.x;
+  int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  for (; tile < total; tile += G) {
+    int e = 0, nt = tile, nrows = p.rows.plain, slot0 = 0;
+    if constexpr (!FUSE) {
+      e = find_expert(first_tile, p.rows.E, tile / NT);
+      const int f0 = uniform(first_tile[e]), mts = uniform(first_tile[e + 1]) - f0;
+      const int r = tile - f0 * NT;
+      const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, mts - f);
+      const int q = r - g * kGroupM * NT;
+      const int row0 = (f + q % gs) * kRowsX;
+      nt = q / gs;
+      nrows = min(kRowsX, uniform(p.rows.rows_of(e)) - row0);
+      if (tid < kRowsX) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
+      slot0 = uniform(p.rows.base_slot(e, row0));
+      __syncthreads();
+    } else if (tid < kRowsX) {
+      slots[tid] = tid < nrows ? tid : -1;
+    }
+    const uint8_t* a0 = p.a + (int64_t)slot0 * p.a_row;
+    const uint8_t* b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kCols * p.b_row;
+    int off_w[4], off_x[FUSE ? 1 : 2 * TT];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int r = (Epi::gate ? j & 1 : j) * 8 + (l >> 3);
+      off_w[j] = nt * kCols + r < p.n ? (int)(r * p.b_row) + chunk_k(j) * 16 : kAbsent;
+    }
+    if constexpr (!FUSE) {
+#pragma unroll
+      for (int j = 0; j < 2 * TT; j++) {
+        const int s = slots[j * 8 + (l >> 3)];
+        off_x[j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
+      }
+    }
+    // step i of this wavefront: bytes 128 (4 i + w) .. of the contraction
+    auto load = [&](int i, int stage) {
+      const int at = (i * 4 + w) * 128;
+      const uint32_t to = mine + stage * (kW + kX);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const i32x4 d = descriptor(b0 + at + (Epi::gate && j >= 2 ? far : 0));
+        load_lds<true>(to + j * 1024, chunk_k(j) * 16 < p.k - at ? off_w[j] : kAbsent, d);
+      }
+      if constexpr (!FUSE) {
+        const i32x4 d = descriptor(a0 + at);
+#pragma unroll
+        for (int j = 0; j < 2 * TT; j++)
+          load_lds<false>(to + kW + j * 1024, chunk_k(j) * 16 < p.k - at ? off_x[j] : kAbsent, d);
+      }
+    };
+    // x is still bf16 (FUSE): p.a_row counts its bytes, and rows of codes have p.k.  Its
+    // first row is asked for before the weights, since loads arrive in order.
+    u32x4 held[4];
+    const int chunks = p.k / 8;
+    auto take = [&](const u32x4* in) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        held[i] = i * 256 + tid < chunks ? in[i * 256 + tid] : u32x4{0, 0, 0, 0};
+    };
+    if constexpr (FUSE) take((const u32x4*)p.a);
+#pragma unroll
+    for (int i = 0; i < kDepth; i++) load(i, i);
+
+    if constexpr (FUSE) {
+      for (int r = 0; r < nrows; r++) {
+        const u32x4* in = (const u32x4*)(p.a + r * p.a_row);
+        if (r > 0) take(in);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) top = max(top, largest8(held[i]));
+        for (int c = 1024 + tid; c < chunks; c += 256) top = max(top, largest8(in[c]));
+        top = wave_max(top);
+        if (l == 0) tops[w] = top;
+        __syncthreads();
+        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+        const RowScale s(top);
+        if (tid == 0) scale[r] = s.scale;
+        u32x2* out = (u32x2*)(lds + 4 * kMine + r * p.k);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (i * 256 + tid < chunks) out[i * 256 + tid] = s.codes8(held[i]);
+        for (int c = 1024 + tid; c < chunks; c += 256) out[c] = s.codes8(in[c]);
+        __syncthreads();
+      }
+      epi.sx = scale;
+    }
+
+    acc_t acc[2][TT];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int j = 0; j < TT; j++) acc[i][j] = acc_t{};
+    int stage = 0;
+    for (int i = 0; i < NI; i++) {
+      wait_loads<(kDepth - 1) * kLoads>();
+      const uint8_t* st = my + stage * (kW + kX);
+      u32x4 fw[2][2], fx[TT][2];
+#pragma unroll
+      for (int m = 0; m < 2; m++) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) fw[r][m] = *(const u32x4*)(st + r * 2048 + (read ^ (m * 64)));
+        if constexpr (FUSE) {
+          const int at = (i * 4 + w) * 128 + m * 64 + (l >> 4) * 16;
+          fx[0][m] = (l & 15) < nrows && at < p.k
+                         ? *(const u32x4*)(lds + 4 * kMine + (l & 15) * p.k + at)
+                         : u32x4{0, 0, 0, 0};
+        } else {
+#pragma unroll
+          for (int j = 0; j < TT; j++)
+            fx[j][m] = *(const u32x4*)(st + kW + j * 2048 + (read ^ (m * 64)));
+        }
+      }
+      wait_lds();                       // read before the stage is loaded again
+      load(i + kDepth, stage);
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+          for (int j = 0; j < TT; j++) acc[r][j] = mfma16<I8>(fw[r][m], fx[j][m], acc[r][j]);
+    }
+    wait_loads<0>();                    // those behind the last step: zeros
+
+    // ---- lane l has weight rows 16 r + 4 (l / 16) + 0..3 of x's row 16 j + l % 16
+#pragma unroll
+    for (int r = 0; r < 2; r++)
+#pragma unroll
+      for (int j = 0; j < TT; j++)
+        *(u32x4*)(lds + w * kMine + (j * 16 + (l & 15)) * 128 +
+                  (((r * 4 + (l >> 4)) ^ ((l >> 1) & 7)) << 4)) =
+            __builtin_bit_cast(u32x4, acc[r][j]);
+    __syncthreads();
+    constexpr int kChunks = kCols / 8;
+    const int row = tid / kChunks, c = tid % kChunks;
+    if (row < nrows && row < kRowsX) {
+      val_t v[8], u[8];
+      auto sum = [&](int chunk, val_t* to) {
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          acc_t t = {};
+#pragma unroll
+          for (int o = 0; o < 4; o++)
+            t += *(const acc_t*)(lds + o * kMine + row * 128 +
+                                 (((chunk + q) ^ ((row >> 1) & 7)) << 4));
+#pragma unroll
+          for (int j = 0; j < 4; j++) to[q * 4 + j] = t[j];
+        }
+      };
+      sum(2 * c, v);
+      if constexpr (Epi::gate) sum(4 + 2 * c, u);
+      epi(e, slots[row], nt * kCols + c * 8, v, u);
     }
     __syncthreads();
   }
 }
 
-template <int KIND, class Epi, bool I8, int BM>
-void launch(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
-  // one workgroup per CU at most: each takes more than half of a CU's LDS
-  const int grid = (int)(tiles < 256 ? tiles : 256);
-  product_kernel<KIND, Epi, I8, BM><<<dim3(grid), dim3(512), 0, st>>>(p, epi);
+// ---------------------------------------------------------------- small products
+// Gradients whose 256 by 256 tiles would leave most CUs idle: 64 by 64 tiles, each
+// wavefront all of a tile over every fourth step of the contraction, with loads of its own
+// in LDS of its own, as above.
+constexpr int kST = 64;                // rows and columns of a tile
+
+template <int KIND, class Epi>
+__global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
+  constexpr bool kSlowA = KIND == kOuter;
+  static_assert(KIND != kRowsT && !Epi::gate);
+  constexpr int kOp = 8192, kSmallStage = 2 * kOp, kMine = 2 * kSmallStage, kLoads = 16;
+
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kMine];
+  __shared__ int first_tile[EP_MAX_EXPERTS + 1];
+  __shared__ int slots[kST];
+
+  const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
+  const uint32_t mine = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds + w * kMine;
+  const uint8_t* my = lds + w * kMine;
+  const int NT = (p.n + kST - 1) / kST, MT = (p.m + kST - 1) / kST;
+  int total;
+  if constexpr (KIND == kOuter) {
+    total = p.rows.E * MT * NT;
+  } else {
+    scan_tiles(p.rows, kST, first_tile);
+    total = uniform(first_tile[p.rows.E]) * NT;
+  }
+  // chunk c of row r at c ^ (r / 2 & 7); where k is slow, of 128 bytes of a k at c ^ 4 (k / 2 & 1)
+  auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
+  const int chunk_n = (l & 7) ^ (((l >> 4) & 1) << 2);
+  const int read_k = (l & 31) * 128 + (((l >> 5) ^ ((l >> 1) & 7)) << 4);
+  const int i16 = l & 15;
+  const int read_n = ((l >> 5) * 8 + (i16 >> 2)) * 128 +
+                     (((((l >> 4) & 1) * 2 + ((i16 & 3) >> 1)) ^ ((i16 >> 3) << 2)) << 4) +
+                     (i16 & 1) * 8;
+  auto slow = [&](const uint8_t* op, int b, int ks) {      // columns 32 b .., k 16 ks ..
+    const int at = (read_n ^ (b << 6)) + ks * 2048;
+    const u32x2 lo = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((EP_LDS bf16x4*)(op + at)));
+    const u32x2 hi = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((EP_LDS bf16x4*)(op + at + 512)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3);
+  };
+  auto fast = [&](const uint8_t* op, int b, int ks) {
+    return *(const u32x4*)(op + b * 4096 + (read_k ^ (ks * 32)));
+  };
+
+  const int G = gridDim.x;
+  int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  for (; tile < total; tile += G) {
+    int e, nt, nrows, row0, slot0, k_a, k_b, KT;
+    const uint8_t *a0, *b0;
+    if constexpr (KIND == kOuter) {
+      e = tile / (MT * NT);
+      const int r = tile - e * MT * NT;
+      row0 = r / NT * kST;
+      nt = r % NT;
+      nrows = min(kST, p.m - row0);
+      k_a = k_b = uniform(p.rows.rows_of(e));
+      KT = (k_a + 63) / 64;
+      slot0 = uniform(p.rows.first_slot(e));
+      a0 = p.a + (int64_t)slot0 * p.a_row + (int64_t)row0 * 2;
+      b0 = p.b + (int64_t)slot0 * p.b_row + (int64_t)nt * kST * 2;
+    } else {
+      e = find_expert(first_tile, p.rows.E, tile / NT);
+      const int f0 = uniform(first_tile[e]);
+      const int r = tile - f0 * NT;
+      row0 = r / NT * kST;
+      nt = r % NT;
+      nrows = min(kST, uniform(p.rows.rows_of(e)) - row0);
+      if (tid < kST) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
+      slot0 = uniform(p.rows.base_slot(e, row0));
+      a0 = p.a + (int64_t)slot0 * p.a_row;
+      b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kST * 2;
+      k_a = p.k;
+      k_b = p.k / 2;
+      KT = (p.k + 127) / 128;
+      __syncthreads();
+    }
+    const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = 64 * p.b_row;
+    int off_a[8];
+    const bool in_a = chunk_n * 8 < nrows, in_b = nt * kST + chunk_n * 8 < p.n;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      if constexpr (kSlowA) {
+        off_a[j] = in_a ? (j * 8 + (l >> 3)) * (int)p.a_row + chunk_n * 16 : kAbsent;
+      } else {
+        const int s = slots[j * 8 + (l >> 3)];
+        off_a[j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
+      }
+    }
+    auto load = [&](int i, int stage) {
+      const int64_t t = i * 4 + w;
+      const uint32_t to = mine + stage * kSmallStage;
+      const i32x4 da = descriptor(a0 + t * step_a), db = descriptor(b0 + t * step_b);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int k = j * 8 + (l >> 3);
+        const bool ok = kSlowA ? k < k_a - t * 64 : chunk_k(j) * 16 < k_a - t * 128;
+        load_lds<false>(to + j * 1024, ok ? off_a[j] : kAbsent, da);
+        load_lds<false>(to + kOp + j * 1024,
+                        in_b && k < k_b - t * 64 ? k * (int)p.b_row + chunk_n * 16 : kAbsent, db);
+      }
+    };
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[i >> 1][i & 1] = f32x16{};
+    load(0, 0);
+    load(1, 1);
+    for (int i = 0; i * 4 < KT; i++) {
+      wait_loads<kLoads>();
+      const uint8_t* st = my + (i & 1) * kSmallStage;
+      u32x4 fa[2][4], fb[2][4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          if constexpr (kSlowA) fa[b][ks] = slow(st, b, ks);
+          else fa[b][ks] = fast(st, b, ks);
+          fb[b][ks] = slow(st + kOp, b, ks);
+        }
+      wait_lds();
+      load(i + 2, i & 1);
+#pragma unroll
+      for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+          acc[b >> 1][b & 1] = mfma<false>(fb[b >> 1][ks], fa[b & 1][ks], acc[b >> 1][b & 1]);
+    }
+    wait_loads<0>();
+
+    // sums: row r's 16 chunks of four columns, chunk c at c ^ (r & 15)
+#pragma unroll
+    for (int b = 0; b < 4; b++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int r = (b & 1) * 32 + (l & 31), c = (b >> 1) * 8 + 2 * i + (l >> 5);
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = acc[b >> 1][b & 1][i * 4 + j];
+        *(f32x4*)(lds + w * kMine + r * 256 + ((c ^ (r & 15)) << 4)) = v;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int r = h * 32 + (tid >> 3), c = tid & 7;
+      if (r >= nrows) continue;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        f32x4 t = {};
+#pragma unroll
+        for (int o = 0; o < 4; o++)
+          t += *(const f32x4*)(lds + o * kMine + r * 256 + (((2 * c + q) ^ (r & 15)) << 4));
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[q * 4 + j] = t[j];
+      }
+      epi(e, KIND == kOuter ? row0 + r : slots[r], nt * kST + c * 8, v, v);
+    }
+    __syncthreads();
+  }
 }
 
-// Rows of D: row tiles are counted on the device; here only their upper bound.
 template <int KIND, class Epi, bool I8>
-int run_rows(const Product& p, const Epi& epi, int max_rows, int64_t tiles_n, hipStream_t st) {
-  const int E = p.rows.E;
-  const bool small = max_rows / E <= 160;
-  const int bm = small ? 128 : 256;
-  const int64_t tiles = ((int64_t)max_rows / bm + E) * tiles_n;
-  if (small) launch<KIND, Epi, I8, 128>(p, epi, tiles, st);
-  else launch<KIND, Epi, I8, 256>(p, epi, tiles, st);
+int launch(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
+  // one workgroup per CU at most: each takes more than half of a CU's LDS
+  const int grid = (int)(tiles < 256 ? tiles : 256);
+  product_kernel<KIND, Epi, I8><<<dim3(grid), dim3(512), 0, st>>>(p, epi);
   return check_launch("ep_ffn product");
+}
+
+template <class Epi, bool I8, int TT, bool FUSE>
+int launch_few(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
+  const int grid = (int)(tiles < 512 ? tiles : 512);       // two workgroups per CU
+  few_kernel<Epi, I8, TT, FUSE><<<dim3(grid), dim3(256), 0, st>>>(p, epi);
+  return check_launch("ep_ffn few rows");
+}
+
+// Row tiles are counted on the device; here only their upper bound.
+int64_t row_tiles(const Rows& r, int max_rows) { return (int64_t)max_rows / kBM + r.E; }
+
+// A gradient, by the kernel for small or for large ones.
+template <int KIND, class Epi>
+int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
+  const int mode = getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : 0;
+  auto tiles = [&](int t) {
+    const int64_t m = KIND == kOuter ? (int64_t)p.rows.E * ((p.m + t - 1) / t)
+                                     : (int64_t)max_rows / t + p.rows.E;
+    return m * ((p.n + t - 1) / t);
+  };
+  if (mode) {
+    const int64_t n = tiles(kST);
+    small_kernel<KIND, Epi><<<dim3((int)(n < 256 ? n : 256)), dim3(256), 0, st>>>(p, epi);
+    return check_launch("ep_ffn small product");
+  }
+  return launch<KIND, Epi, false>(p, epi, tiles(kBM), st);
+}
+
+// Activations by a weight's rows, by the kernel for few or for many of them.
+template <class Epi, bool I8>
+int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
+  const int mode = getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : 0;
+  const int few = Epi::gate ? 16 : 32;
+  const int64_t nt = (p.n + few - 1) / few;
+  if (mode == 1)
+    return launch_few<Epi, I8, 1, false>(p, epi, (max_rows / 16 + p.rows.E) * nt, st);
+  if (mode == 2)
+    return launch_few<Epi, I8, 2, false>(p, epi, (max_rows / 32 + p.rows.E) * nt, st);
+  const int wide = Epi::gate ? 128 : kBN;
+  return launch<kRowsT, Epi, I8>(p, epi, row_tiles(p.rows, max_rows) * ((p.n + wide - 1) / wide),
+                                 st);
+}
+
+// Whether every workgroup rounds x to integers by itself.
+bool fuses(const Rows& r, int max_rows, int cols) {
+  return !r.count && max_rows <= 16 && (int64_t)max_rows * cols <= kFuseBytes;
 }
 
 // Offsets inside an expert's sub-blocks have 32 bits (see descriptor()).
@@ -582,8 +1013,8 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
   p.n = I;
   p.far = I;
   const StoreGate gate{(uint16_t*)h, (uint16_t*)a->gate_up, I, sx, (const float*)a->w13.scales};
-  rc = i8 ? run_rows<kRowsT, StoreGate, true>(p, gate, rows->max_rows, (I + 127) / 128, st)
-          : run_rows<kRowsT, StoreGate, false>(p, gate, rows->max_rows, (I + 127) / 128, st);
+  rc = i8 ? run_rows<StoreGate, true>(p, gate, rows->max_rows, st)
+          : run_rows<StoreGate, false>(p, gate, rows->max_rows, st);
   if (rc != EP_OK) return rc;
   if (i8) {
     rc = quantize_rows(r, rows->max_rows, h, I, hq, sh, st);
@@ -597,8 +1028,8 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
   p.n = H;
   p.far = 0;
   const StoreRows out{(uint16_t*)a->y, H, sh, (const float*)a->w2.scales};
-  return i8 ? run_rows<kRowsT, StoreRows, true>(p, out, rows->max_rows, (H + kBN - 1) / kBN, st)
-            : run_rows<kRowsT, StoreRows, false>(p, out, rows->max_rows, (H + kBN - 1) / kBN, st);
+  return i8 ? run_rows<StoreRows, true>(p, out, rows->max_rows, st)
+            : run_rows<StoreRows, false>(p, out, rows->max_rows, st);
 }
 
 int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* stream) {
@@ -632,7 +1063,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
     p.b_expert = (int64_t)2 * H * I;
     p.n = I;
     const StoreGateGrad gg{(const uint16_t*)a->gate_up, (uint16_t*)dgu, (uint16_t*)h, I};
-    rc = run_rows<kRows, StoreGateGrad, false>(p, gg, rows->max_rows, (I + kBN - 1) / kBN, st);
+    rc = run_grad<kRows>(p, gg, rows->max_rows, st);
     if (rc != EP_OK) return rc;
     p.a = dgu;
     p.b = (const uint8_t*)a->w13;
@@ -642,7 +1073,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
     p.b_expert = (int64_t)4 * H * I;
     p.n = H;
     const StoreRows dx{(uint16_t*)a->dx, H, nullptr, nullptr};
-    rc = run_rows<kRows, StoreRows, false>(p, dx, rows->max_rows, (H + kBN - 1) / kBN, st);
+    rc = run_grad<kRows>(p, dx, rows->max_rows, st);
     if (rc != EP_OK) return rc;
   }
   if (!any) p.rows = Rows{nullptr, nullptr, 0, r.E, 1, 0, 0};   // no rows: zeros
@@ -653,9 +1084,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   p.m = 2 * I;
   p.n = H;
   const StoreMatrix w13{(uint16_t*)a->dw13, 2 * I, H};
-  launch<kOuter, StoreMatrix, false, 256>(
-      p, w13, (int64_t)r.E * ((2 * I + 255) / 256) * ((H + 255) / 256), st);
-  rc = check_launch("ep_ffn_backward dw13");
+  rc = run_grad<kOuter>(p, w13, rows->max_rows, st);
   if (rc != EP_OK) return rc;
   p.a = (const uint8_t*)a->dy;
   p.b = h;
@@ -664,9 +1093,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   p.m = H;
   p.n = I;
   const StoreMatrix w2{(uint16_t*)a->dw2, H, I};
-  launch<kOuter, StoreMatrix, false, 256>(
-      p, w2, (int64_t)r.E * ((H + 255) / 256) * ((I + 255) / 256), st);
-  return check_launch("ep_ffn_backward dw2");
+  return run_grad<kOuter>(p, w2, rows->max_rows, st);
 }
 
 int64_t ep_integer_workspace_bytes(const ep_rows_t* rows, int32_t cols) {
@@ -688,12 +1115,23 @@ int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* a, void* s
   const Rows r = device_rows(rows);
   if (!fits_region(r, C)) return EP_ERR_INVALID_ARG;
   const int64_t tiles_n = (O + kBN - 1) / kBN;
-  if (((int64_t)rows->max_rows / 128 + r.E) * tiles_n > INT32_MAX) return EP_ERR_INVALID_ARG;
+  if (row_tiles(r, rows->max_rows) * tiles_n > INT32_MAX) return EP_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != EP_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
   const uint8_t* xq = (const uint8_t*)a->x;
   const float* sx = a->x_scales;
+  if (!sx && fuses(r, rows->max_rows, C)) {
+    Product p{};
+    p.rows = r;
+    p.a = xq;
+    p.b = (const uint8_t*)a->w.data;
+    p.k = p.b_row = C;
+    p.a_row = 2 * C;
+    p.n = O;
+    const StoreRows out{(uint16_t*)a->y, O, nullptr, (const float*)a->w.scales};
+    return launch_few<StoreRows, true, 1, true>(p, out, (O + 31) / 32, st);
+  }
   if (!sx) {
     uint8_t* q = (uint8_t*)a->workspace;
     float* s = (float*)(q + up(rows->capacity * C));
@@ -712,7 +1150,7 @@ int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* a, void* s
   p.b_expert = (int64_t)O * C;
   p.n = O;
   const StoreRows out{(uint16_t*)a->y, O, sx, (const float*)a->w.scales};
-  return run_rows<kRowsT, StoreRows, true>(p, out, rows->max_rows, tiles_n, st);
+  return run_rows<StoreRows, true>(p, out, rows->max_rows, st);
 }
 
 }  // extern "C"

@@ -5,40 +5,7 @@
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ void unpack8(u32x4 r, float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    v[2 * i] = __builtin_bit_cast(float, r[i] << 16);
-    v[2 * i + 1] = __builtin_bit_cast(float, r[i] & 0xFFFF0000u);
-  }
-}
-
 // ---------------------------------------------------------------- 8-bit integers
-// Codes of eight values.  q = rint(x * inv) is off by one at most, next to a half: the
-// remainder x - q * s is exact there (q has 7 bits, s 24, x 8, and they cancel), so its
-// comparison with s / 2 decides as the exact quotient would, halves to even.
-__device__ __forceinline__ u32x2 codes8(u32x4 raw, float up, float inv, float s) {
-  float v[8];
-  unpack8(raw, v);
-  u32x2 out = {0, 0};
-  const float half = 0.5f * s;
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float x = v[i] * up;
-    float q = rintf(x * inv);
-    const float r = fmaf(-q, s, x);
-    const bool odd = ((int)q & 1) != 0;
-    if (r > half || (r == half && odd)) q += 1.f;
-    if (-r > half || (-r == half && odd)) q -= 1.f;
-    const int c = (int)fminf(127.f, fmaxf(-127.f, q));
-    out[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
-  }
-  return out;
-}
-
 constexpr int kHeld = 16;      // 16-byte chunks per lane that stay in registers: 8192 columns
 
 // A wavefront per row; blocks (segment, part): segments are the experts, or the sub-blocks
@@ -64,37 +31,22 @@ __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t*
 #pragma unroll
     for (int i = 0; i < CH; i++)
       held[i] = i * 64 + l < chunks ? in[i * 64 + l] : u32x4{0, 0, 0, 0};
-    // magnitudes of bf16 are ordered as their bits are, infinities and NaN last
     uint32_t top = 0;
-    auto look = [&](u32x4 r) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) top = max(top, max(r[i] & 0x7FFFu, (r[i] >> 16) & 0x7FFFu));
-    };
-#pragma unroll
-    for (int i = 0; i < CH; i++) look(held[i]);
-    for (int c = CH * 64 + l; c < chunks; c += 64) look(in[c]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    const float amax = __builtin_bit_cast(float, top << 16);
-    float s = amax / 127.f;
-    if (top == 0) s = 1.f;
-    if (l == 0) scales[slot] = top >= 0x7F80u ? __builtin_bit_cast(float, 0x7FC00000u) : s;
-    // tiny rows are taken 2^64 times as large (exact), where 1 / s would overflow
-    const float up = amax < 0x1p-100f && top != 0 ? 0x1p64f : 1.f;
-    const float su = s * up, inv = 1.f / su;
-    const bool finite = top < 0x7F80u;
-    auto put = [&](int c, u32x4 r) {
-      out[c] = finite ? codes8(r, up, inv, su) : u32x2{0, 0};
-    };
+    for (int i = 0; i < CH; i++) top = max(top, largest8(held[i]));
+    for (int c = CH * 64 + l; c < chunks; c += 64) top = max(top, largest8(in[c]));
+    const RowScale s(wave_max(top));
+    if (l == 0) scales[slot] = s.scale;
 #pragma unroll
     for (int i = 0; i < CH; i++)
-      if (i * 64 + l < chunks) put(i * 64 + l, held[i]);
-    for (int c = CH * 64 + l; c < chunks; c += 64) put(c, in[c]);
+      if (i * 64 + l < chunks) out[i * 64 + l] = s.codes8(held[i]);
+    for (int c = CH * 64 + l; c < chunks; c += 64) out[c] = s.codes8(in[c]);
   }
 }
 
 // ---------------------------------------------------------------- combine's gradient
 constexpr int kPairs = 8;      // pairs of a token handled together
+constexpr int kMostWaves = 16;
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -102,14 +54,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-// A workgroup per token: dy's row is read once for all pairs, 16 bytes per thread and
-// step; the K sums meet in LDS at the end, in a fixed order.
-__global__ __launch_bounds__(256) void combine_backward_kernel(
+// A workgroup per token, with as many threads as the row has 16-byte chunks (up to 1024):
+// all loads of a token are in flight at once, and dy's row is read once for all
+// pairs.  The sums meet in LDS at the end, in a fixed order.
+__global__ __launch_bounds__(1024) void combine_backward_kernel(
     const u32x4* dy, const u32x4* eo, const int* slot_of, const float* wts, u32x4* deo,
     float* dwts, int H8, int K, int cap) {
-  __shared__ float sums[4][kPairs];
+  __shared__ float sums[kMostWaves][kPairs];
   const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, waves = blockDim.x >> 6;
   for (int k0 = 0; k0 < K; k0 += kPairs) {
     int slot[kPairs];
     float w[kPairs], sum[kPairs];
@@ -121,12 +74,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
       w[k] = in ? wts[t * K + k0 + k] : 0.f;
       sum[k] = 0.f;
     }
-    for (int c = tid; c < H8; c += 256) {
+    for (int c = tid; c < H8; c += blockDim.x) {
       const u32x4 g = dy[t * H8 + c];
       u32x4 o[kPairs];
 #pragma unroll
       for (int k = 0; k < kPairs; k++)
-        if (slot[k] >= 0) o[k] = eo[(int64_t)slot[k] * H8 + c];
+        if (slot[k] >= 0) o[k] = __builtin_nontemporal_load(eo + (int64_t)slot[k] * H8 + c);
       float gf[8];
       unpack8(g, gf);
 #pragma unroll
@@ -149,8 +102,11 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
       if ((tid & 63) == 0) sums[tid >> 6][k] = sum[k];
     }
     __syncthreads();
-    if (tid < kPairs && k0 + tid < K)
-      dwts[t * K + k0 + tid] = sums[0][tid] + sums[1][tid] + sums[2][tid] + sums[3][tid];
+    if (tid < kPairs && k0 + tid < K) {
+      float total = 0.f;
+      for (int v = 0; v < waves; v++) total += sums[v][tid];
+      dwts[t * K + k0 + tid] = total;
+    }
     __syncthreads();
   }
 }
@@ -212,7 +168,9 @@ int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* exper
   if (rc != EP_OK) return rc;
   EP_LOG("combine_backward N=%d H=%d K=%d cap=%lld", N, H, p->num_topk, (long long)recv_capacity);
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  combine_backward_kernel<<<dim3(N), dim3(256), 0, (hipStream_t)stream>>>(
+  const int q = (H / 8 + 63) / 64, passes = (q + kMostWaves - 1) / kMostWaves;
+  const int waves = (q + passes - 1) / passes;
+  combine_backward_kernel<<<dim3(N), dim3(64 * waves), 0, (hipStream_t)stream>>>(
       (const u32x4*)dy, (const u32x4*)expert_out, slot_of, topk_weights, (u32x4*)d_expert_out,
       d_topk_weights, H / 8, p->num_topk, (int)recv_capacity);
   return check_launch("combine_backward");

@@ -55,26 +55,36 @@ using ep::Rows;
 using ep::quantize_rows;
 
 // first[e] = row tiles of the experts before e, first[E] of all; by the whole workgroup.
-[[maybe_unused]] __device__ __forceinline__ void scan_tiles(const Rows& rows, int tile,
-                                                            int* first) {
-  for (int e = threadIdx.x; e < rows.E; e += blockDim.x)
-    first[e + 1] = (rows.rows_of(e) + tile - 1) / tile;
-  if (threadIdx.x == 0) first[0] = 0;
+// With `shorter`, a last tile of at most half the rows counts there instead.
+[[maybe_unused]] __device__ __forceinline__ void scan_tiles(const Rows& rows, int tile, int* first,
+                                                            int* shorter = nullptr) {
+  for (int e = threadIdx.x; e < rows.E; e += blockDim.x) {
+    const int n = rows.rows_of(e), last = n % tile;
+    const bool half = shorter && last > 0 && 2 * last <= tile;
+    first[e + 1] = n / tile + (last > 0 && !half);
+    if (shorter) shorter[e + 1] = half;
+  }
+  if (threadIdx.x == 0) {
+    first[0] = 0;
+    if (shorter) shorter[0] = 0;
+  }
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int per = (rows.E + 63) / 64, from = threadIdx.x * per,
-              to = min(rows.E, from + per);
+  // a wavefront for each of the two sums
+  if (threadIdx.x < 64 || (shorter && threadIdx.x < 128)) {
+    const int l = threadIdx.x & 63;
+    int* v = threadIdx.x < 64 ? first : shorter;
+    const int per = (rows.E + 63) / 64, from = l * per, to = min(rows.E, from + per);
     int sum = 0;
-    for (int e = from; e < to; e++) sum += first[e + 1];
+    for (int e = from; e < to; e++) sum += v[e + 1];
     int before = sum;
     for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(before, d);
-      if ((int)threadIdx.x >= d) before += v;
+      const int o = __shfl_up(before, d);
+      if (l >= d) before += o;
     }
     before -= sum;
     for (int e = from; e < to; e++) {
-      before += first[e + 1];
-      first[e + 1] = before;
+      before += v[e + 1];
+      v[e + 1] = before;
     }
   }
   __syncthreads();
@@ -90,6 +100,90 @@ using ep::quantize_rows;
   }
   return lo;
 }
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+[[maybe_unused]] __device__ __forceinline__ void unpack8(u32x4 r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[2 * i] = __builtin_bit_cast(float, r[i] << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, r[i] & 0xFFFF0000u);
+  }
+}
+
+// ---------------------------------------------------------------- rows as 8-bit integers
+// The largest magnitude of eight bf16 values as bits: they are ordered as the values are,
+// infinities and NaN last.
+[[maybe_unused]] __device__ __forceinline__ uint32_t largest8(u32x4 r) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) top = max(top, max(r[i] & 0x7FFFu, (r[i] >> 16) & 0x7FFFu));
+  return top;
+}
+[[maybe_unused]] __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  return v;
+}
+
+// A row's scale, from its largest magnitude, and its codes.  fma(x, 1 / s, 1.5 2^23) leaves
+// the nearest integer q of x * (1 / s) in its lowest bits.  That is off from x / s by less
+// than 2^-16, so only where it is this near to a half may the exact quotient round
+// otherwise: there the remainder x - q s decides, which is exact (q has 7 bits, s 24, x
+// 8, and they cancel), halves to even.  Rows below 2^-100 are taken 2^64 times as large
+// (exact), since 1 / s would overflow.
+struct RowScale {
+  float scale, s, inv, up;
+  bool finite, tiny;
+  __device__ __forceinline__ explicit RowScale(uint32_t top) {
+    const float amax = __builtin_bit_cast(float, top << 16);
+    finite = top < 0x7F80u;
+    tiny = amax < 0x1p-100f && top != 0;
+    up = tiny ? 0x1p64f : 1.f;
+    scale = top == 0 ? 1.f : amax / 127.f;
+    s = scale * up;
+    inv = 1.f / s;
+    if (!finite) scale = __builtin_bit_cast(float, 0x7FC00000u);
+  }
+  __device__ __forceinline__ u32x2 codes8(u32x4 raw) const {
+    constexpr float kMagic = 12582912.f;
+    float v[8], t[8], near = 0.f;
+    unpack8(raw, v);
+    if (tiny) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] *= up;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      t[i] = fmaf(v[i], inv, kMagic);
+      near = fmaxf(near, fabsf(fmaf(v[i], inv, kMagic - t[i])));
+    }
+    if (near > 0.5f - 0x1p-14f) {
+      const float half = 0.5f * s;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float q = t[i] - kMagic;
+        const float r = fmaf(-q, s, v[i]);
+        const bool odd = ((int)q & 1) != 0;
+        if (r > half || (r == half && odd)) q += 1.f;
+        if (-r > half || (-r == half && odd)) q -= 1.f;
+        t[i] = q + kMagic;
+      }
+    }
+    if (!finite) return u32x2{0, 0};
+    u32x2 out;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t b0 = __builtin_bit_cast(uint32_t, t[4 * h]),
+                     b1 = __builtin_bit_cast(uint32_t, t[4 * h + 1]),
+                     b2 = __builtin_bit_cast(uint32_t, t[4 * h + 2]),
+                     b3 = __builtin_bit_cast(uint32_t, t[4 * h + 3]);
+      out[h] = (b0 & 0xFFu) | (b1 & 0xFFu) << 8 | (b2 & 0xFFu) << 16 | b3 << 24;
+    }
+    return out;
+  }
+};
 
 [[maybe_unused]] bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 [[maybe_unused]] bool aligned16(const void* p) { return aligned(p, 16); }
