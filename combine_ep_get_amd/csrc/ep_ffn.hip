@@ -45,9 +45,9 @@ struct Product {            // kernel argument
 
 // 16 bytes per lane from global memory straight to LDS, lane l's at base + 16 l.  In asm,
 // because the compiler would wait for all such loads before the next read of LDS; the
-// waits are written out at the loop.  The s_nop covers a descriptor word or base that a
+// waits are written out at the loops.  The s_nop covers a descriptor word or base that a
 // VALU instruction has just written (five wait states), which the compiler cannot see
-// here, and m0.
+// here, and m0.  ONCE: the bytes are not kept in the caches for another workgroup.
 template <bool ONCE>
 __device__ __forceinline__ void load_lds(uint32_t lds, int offset, i32x4 desc) {
   if constexpr (ONCE)
@@ -59,6 +59,24 @@ __device__ __forceinline__ void load_lds(uint32_t lds, int offset, i32x4 desc) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(uniform((int)lds)), "v"(offset), "s"(desc)
+                 : "memory");
+}
+// Two of them, 1 KiB apart in LDS.
+template <bool ONCE>
+__device__ __forceinline__ void load_lds2(uint32_t lds, int offset0, int offset1, i32x4 desc) {
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %4, 0 offen nt lds\n\t"
+                 "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, 0 offen nt lds"
+                 :
+                 : "s"(uniform((int)lds)), "s"(uniform((int)lds + 1024)), "v"(offset0),
+                   "v"(offset1), "s"(desc)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds\n\t"
+                 "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds"
+                 :
+                 : "s"(uniform((int)lds)), "s"(uniform((int)lds + 1024)), "v"(offset0),
+                   "v"(offset1), "s"(desc)
                  : "memory");
 }
 
@@ -100,8 +118,12 @@ __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-
 // ---------------------------------------------------------------- epilogues
 // What becomes of eight neighbouring columns of a row of D.  `slot` is the row's slot
 // (kOuter: its row of the expert's matrix), `e` the expert, `c` the first column.
+// `stores` is how many of them a wavefront sends at least for a whole tile (16 calls, 8 of
+// a gate).
 struct StoreRows {
   static constexpr bool gate = false;
+  static constexpr int stores = 16;
+  __device__ __forceinline__ int columns() const { return n; }
   uint16_t* y;
   int n;
   const float *sx, *sw;    // 8-bit products: scales per slot and per expert and column
@@ -133,6 +155,8 @@ struct StoreRows {
 
 struct StoreMatrix {       // kOuter: [e][m][n]
   static constexpr bool gate = false;
+  static constexpr int stores = 16;
+  __device__ __forceinline__ int columns() const { return n; }
   uint16_t* y;
   int m, n;
   __device__ __forceinline__ void operator()(int e, int row, int c, const float* v,
@@ -145,6 +169,8 @@ struct StoreMatrix {       // kOuter: [e][m][n]
 // silu(gate) * up; the tile's columns are `c` of gate and of up.
 struct StoreGate {
   static constexpr bool gate = true;
+  static constexpr int stores = 8;
+  __device__ __forceinline__ int columns() const { return inter; }
   uint16_t* h;             // [slot][inter]
   uint16_t* gu;            // [slot][2 inter] or NULL
   int inter;
@@ -182,6 +208,8 @@ struct StoreGate {
 // v is the gradient of h: those of gate and up, and h itself again.
 struct StoreGateGrad {
   static constexpr bool gate = false;
+  static constexpr int stores = 48;
+  __device__ __forceinline__ int columns() const { return inter; }
   const uint16_t* gu;      // [slot][2 inter]
   uint16_t* dgu;           // [slot][2 inter]
   uint16_t* h;             // [slot][inter]
@@ -250,23 +278,20 @@ void product_kernel(Product p, Epi epi) {
   using acc_t = typename Acc<I8>::type;
   using val_t = typename Acc<I8>::scalar;
 
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps * kStage];
-  __shared__ int first_tile[EP_MAX_EXPERTS + 1], first_short[EP_MAX_EXPERTS + 1];
-  __shared__ int slot_of_row[2][kBM];    // the epilogue's tile, and the one being loaded
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSteps * kStage + 8 * 2048];
+  __shared__ Experts experts;
 
   const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
   const int wm = w >> 2, wn = w & 3;     // rows wm*64.., columns wn*32.. of each half
   const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
   const int NT = KIND == kRowsT && p.far ? (p.n + 127) / 128 : (p.n + kBN - 1) / kBN;
   const int MT = (p.m + kBM - 1) / kBM;                    // kOuter
-  int total, tall = 0;                                     // tiles, those of over 128 rows
-  if constexpr (KIND == kOuter) {
-    total = p.rows.E * MT * NT;
-  } else {
-    scan_tiles(p.rows, kBM, first_tile, first_short);
-    tall = uniform(first_tile[p.rows.E]) * NT;
-    total = tall + uniform(first_short[p.rows.E]) * NT;
-  }
+  const bool blocks = p.rows.count && !p.rows.offset;      // rows of several sub-blocks
+  experts.fill(p.rows, kBM);
+  // tiles, and those of over 128 rows
+  const int tall = KIND == kOuter ? 0 : uniform(experts.first[p.rows.E]) * NT;
+  const int total = KIND == kOuter ? p.rows.E * MT * NT
+                                   : tall + uniform(experts.first_short[p.rows.E]) * NT;
 
   // where this lane's bytes of a load go (a wavefront sends two loads per half: rows
   // w*16 + 8 j + l/8, or k w*8 + 4 j + l/16), and where it reads
@@ -285,83 +310,96 @@ void product_kernel(Product p, Epi epi) {
     read_a[mb] = kSlowA ? read_n(wm * 8 + mb * 4) : (wm * 64 + mb * 32) * 128 + read_k;
   const int read_b = kSlowB ? read_n(wn * 4) : wn * 32 * 128 + read_k;
 
-  // ---- the tile whose loads are under way
-  int e = 0, nt = 0, nrows = 0, row0 = 0, KT = 0;
-  int k_a = 0, k_b = 0;        // contraction of a and b in what their tail counts
+  struct Tile {
+    int e, nt, nrows, row0, slot0, KT;
+  };
+  // ---- what the loads run over: the current tile, and from its last steps on the next
   const uint8_t *a0 = nullptr, *b0 = nullptr;
+  int k_a = 0, k_b = 0;        // contraction of a and b in what their tail counts
   int off_a[2][2], off_b[2][2];
   const int64_t far = (int64_t)p.far * p.b_row;
   const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
 
-  auto load_a = [&](int t, int h) {
-    const i32x4 d = descriptor(a0 + t * step_a);
-    const uint32_t to = lds0 + (t & 1) * kStage + h * kHalf + w * 2048;
+  // step t of the operand at `at`; TAIL: its last bytes may be behind the contraction's end
+  auto load_a = [&](auto tail, const uint8_t* at, int t, int stage, int h) {
+    int o[2];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      const bool in = kSlowA ? w * 8 + j * 4 + (l >> 4) < k_a - t * 64
-                             : chunk_k(j) * 16 < k_a - t * 128;
-      load_lds<false>(to + j * 1024, in ? off_a[h][j] : kAbsent, d);
+      const bool in = !decltype(tail)::value ||
+                      (kSlowA ? w * 8 + j * 4 + (l >> 4) < k_a - t * 64
+                              : chunk_k(j) * 16 < k_a - t * 128);
+      o[j] = in ? off_a[h][j] : kAbsent;
     }
+    load_lds2<false>(lds0 + stage * kStage + h * kHalf + w * 2048, o[0], o[1], descriptor(at));
   };
-  auto load_b = [&](int t, int h) {
-    const i32x4 d = descriptor(b0 + t * step_b + h * far);
-    const uint32_t to = lds0 + (t & 1) * kStage + (2 + h) * kHalf + w * 2048;
+  auto load_b = [&](auto tail, const uint8_t* at, int t, int stage, int h) {
+    int o[2];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      const bool in = kSlowB ? w * 8 + j * 4 + (l >> 4) < k_b - t * 64
-                             : chunk_k(j) * 16 < k_b - t * 128;
-      load_lds<KIND == kRowsT>(to + j * 1024, in ? off_b[h][j] : kAbsent, d);
+      const bool in = !decltype(tail)::value ||
+                      (kSlowB ? w * 8 + j * 4 + (l >> 4) < k_b - t * 64
+                              : chunk_k(j) * 16 < k_b - t * 128);
+      o[j] = in ? off_b[h][j] : kAbsent;
     }
+    load_lds2<KIND == kRowsT>(lds0 + stage * kStage + (2 + h) * kHalf + w * 2048, o[0], o[1],
+                              descriptor(at + h * far));
   };
-  auto load_first = [&](int t) {         // what the first phase of step t reads
-    load_b(t, 0);
-    load_a(t, 0);
-    load_b(t, 1);
+  // what the first phase of step t reads
+  auto load_first = [&](auto tail, const uint8_t* at_a, const uint8_t* at_b, int t, int stage) {
+    load_b(tail, at_b, t, stage, 0);
+    load_a(tail, at_a, t, stage, 0);
+    load_b(tail, at_b, t, stage, 1);
   };
+  constexpr std::true_type kTail{};
+  constexpr std::false_type kWhole{};
 
-  // Finds tile `tile` and sends the loads of its first step.
-  auto begin = [&](int tile, int* slots) {
-    int slot0;
+  // Finds tile `tile` and turns the loads to it; behind the last one they load zeros.
+  auto locate = [&](int tile, Tile& x) {
+    x.KT = 2;
+    k_a = k_b = 0;
+    if (tile >= total) return;
     if constexpr (KIND == kOuter) {
-      e = tile / (MT * NT);
-      const int r = tile - e * MT * NT;
+      x.e = tile / (MT * NT);
+      const int r = tile - x.e * MT * NT;
       const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, MT - f);
       const int q = r - g * kGroupM * NT;
-      row0 = (f + q % gs) * kBM;
-      nt = q / gs;
-      nrows = min(kBM, p.m - row0);
-      k_a = k_b = uniform(p.rows.rows_of(e));
-      KT = (k_a + 63) / 64;
-      slot0 = uniform(p.rows.first_slot(e));
-      a0 = p.a + (int64_t)slot0 * p.a_row + (int64_t)row0 * 2;
-      b0 = p.b + (int64_t)slot0 * p.b_row + (int64_t)nt * kBN * 2;
+      x.row0 = (f + q % gs) * kBM;
+      x.nt = q / gs;
+      x.nrows = min(kBM, p.m - x.row0);
+      k_a = k_b = uniform(experts.count[x.e]);
+      x.slot0 = uniform(experts.slot[x.e]);
+      a0 = p.a + (int64_t)x.slot0 * p.a_row + (int64_t)x.row0 * 2;
+      b0 = p.b + (int64_t)x.slot0 * p.b_row + (int64_t)x.nt * kBN * 2;
+      x.KT = max(2, (k_a + 63) / 64);
     } else {
       // the short ones last: they take half the time, and a workgroup whose share was all
       // tall ones would keep the others waiting
       const bool is_short = tile >= tall;
       const int at = is_short ? tile - tall : tile;
-      const int* first = is_short ? first_short : first_tile;
-      e = find_expert(first, p.rows.E, at / NT);
-      const int f0 = uniform(first[e]), mts = uniform(first[e + 1]) - f0;
-      const int r = at - f0 * NT;
-      const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, mts - f);
-      const int q = r - g * kGroupM * NT;
-      row0 = (f + q % gs) * kBM;
-      if (is_short) row0 = (uniform(first_tile[e + 1]) - uniform(first_tile[e])) * kBM;
-      nt = q / gs;
-      nrows = min(kBM, uniform(p.rows.rows_of(e)) - row0);
-      if (tid < kBM) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
-      slot0 = uniform(p.rows.base_slot(e, row0));
-      a0 = p.a + (int64_t)slot0 * p.a_row;
-      b0 = p.b + (int64_t)e * p.b_expert;
+      x.e = is_short ? find_expert(experts.first_short, p.rows.E, at / NT)
+                     : find_expert(experts.first, p.rows.E, at / NT);
+      const int f0 = uniform(experts.first[x.e]), mts = uniform(experts.first[x.e + 1]) - f0;
+      if (is_short) {
+        x.row0 = mts * kBM;
+        x.nt = at % NT;
+      } else {
+        const int r = at - f0 * NT;
+        const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, mts - f);
+        const int q = r - g * kGroupM * NT;
+        x.row0 = (f + q % gs) * kBM;
+        x.nt = q / gs;
+      }
+      x.nrows = min(kBM, uniform(experts.count[x.e]) - x.row0);
+      x.slot0 = uniform(experts.slot[x.e]) + (blocks ? 0 : x.row0);
+      a0 = p.a + (int64_t)x.slot0 * p.a_row;
+      b0 = p.b + (int64_t)x.e * p.b_expert;
       if constexpr (KIND == kRowsT)
-        b0 += (int64_t)nt * (p.far ? 128 : kBN) * p.b_row;
+        b0 += (int64_t)x.nt * (p.far ? 128 : kBN) * p.b_row;
       else
-        b0 += (int64_t)nt * kBN * 2;
+        b0 += (int64_t)x.nt * kBN * 2;
       k_a = p.k;
       k_b = KIND == kRows ? p.k / 2 : p.k;    // rows of b, or bytes of its rows
-      KT = (p.k + 127) / 128;
-      __syncthreads();
+      x.KT = max(2, (p.k + 127) / 128);
     }
 #pragma unroll
     for (int h = 0; h < 2; h++)
@@ -370,125 +408,155 @@ void product_kernel(Product p, Epi epi) {
         const int r = w * 16 + j * 8 + (l >> 3), k = w * 8 + j * 4 + (l >> 4);
         const int c = h * 128 + chunk_n * 8;
         if constexpr (kSlowA) {
-          off_a[h][j] = c < nrows ? k * (int)p.a_row + c * 2 : kAbsent;
+          off_a[h][j] = c < x.nrows ? k * (int)p.a_row + c * 2 : kAbsent;
         } else {
-          const int s = slots[h * 128 + r];
-          off_a[h][j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
+          int s = h * 128 + r;               // slots behind slot0
+          const bool in = s < x.nrows;
+          if (blocks && in) s = p.rows.slot(x.e, x.row0 + s) - x.slot0;
+          off_a[h][j] = in ? s * (int)p.a_row + chunk_k(j) * 16 : kAbsent;
         }
         if constexpr (kSlowB)
-          off_b[h][j] = nt * kBN + c < p.n ? k * (int)p.b_row + c * 2 : kAbsent;
+          off_b[h][j] = x.nt * kBN + c < p.n ? k * (int)p.b_row + c * 2 : kAbsent;
         else if (p.far)
-          off_b[h][j] = nt * 128 + r < p.n ? (int)(r * p.b_row) + chunk_k(j) * 16 : kAbsent;
+          off_b[h][j] = x.nt * 128 + r < p.n ? r * (int)p.b_row + chunk_k(j) * 16 : kAbsent;
         else
-          off_b[h][j] = nt * kBN + h * 128 + r < p.n
-                            ? (int)((r + h * 128) * p.b_row) + chunk_k(j) * 16 : kAbsent;
+          off_b[h][j] = x.nt * kBN + h * 128 + r < p.n
+                            ? (r + h * 128) * (int)p.b_row + chunk_k(j) * 16 : kAbsent;
       }
-    if (KT == 0) return;
-    load_first(0);
-    load_a(0, 1);
   };
 
   // workgroup ids go round robin over the 8 XCDs: give each XCD neighbouring tiles
   const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
   if (tile >= total) return;
-  int* slots = slot_of_row[0];
-  begin(tile, slots);
+  Tile cur, next;
+  locate(tile, cur);
+  next = cur;
+  load_first(kTail, a0, b0, 0, 0);
+  load_a(kTail, a0, 0, 0, 1);
+  load_first(kTail, a0 + step_a, b0 + step_b, 1, 1);
+  wait_loads<8>();
+  barrier();
+  if (wm == 1) barrier();
+  int stage = 0;
+  bool stores = false;         // the last epilogue surely sent kStores of them
+  constexpr int kStores = Epi::stores;
   for (;;) {
     acc_t acc[2][2][2];
 #pragma unroll
     for (int i = 0; i < 8; i++) acc[i >> 2][(i >> 1) & 1][i & 1] = acc_t{};
 
-    // ---- the loop.  Two groups of four wavefronts, one of each group on every SIMD,
-    // one phase's half apart: while one group's MFMAs run, the other reads its next
-    // fragments and sends loads.  Phases per step: b and a's first half, a's second half.
-    // Loads run one step and a phase ahead; a half tile is loaded again as soon as both
-    // groups have read it: reads have returned (wait_lds) before the barrier behind which
-    // the load is sent, and a load has arrived (wait_loads) one barrier before it is read.
-    if (KT > 0) {
-      load_first(1);
-      wait_loads<8>();
-      barrier();
-      if (wm == 1) barrier();
-      const bool any0 = wm * 64 < nrows, any1 = 128 + wm * 64 < nrows;
-      for (int t = 0; t < KT; t++) {
-        const uint8_t* st = lds + (t & 1) * kStage;
-        u32x4 fa[2][4], fb[2][4];
-        auto read_as = [&](int h) {
+    // ---- the loop.  Two groups of four wavefronts, one of each group on every SIMD, half
+    // a phase apart: while one group's MFMAs run, the other reads its next fragments and
+    // sends loads.  Phases per step: b and a's first half, a's second half.  Loads run one
+    // step and a phase ahead, across the tiles; a half tile is loaded again as soon as
+    // both groups have read it: reads have returned (wait_lds) before the barrier behind
+    // which the load is sent, and a load has arrived (wait_loads) one barrier before it is
+    // read.  vmcnt counts the epilogue's stores as well, which a tile's first step leaves
+    // under way.
+    const bool any0 = wm * 64 < cur.nrows, any1 = 128 + wm * 64 < cur.nrows;
+    const int KT = cur.KT;
+    // One step; `load1` and `load2` send the loads of its two phases.
+    auto step = [&](auto&& load1, auto&& load2, auto&& wait) {
+      const uint8_t* st = lds + stage * kStage;
+      u32x4 fa[2][4], fb[2][4];
+      auto read_as = [&](int h) {
 #pragma unroll
-          for (int mb = 0; mb < 2; mb++)
-#pragma unroll
-            for (int ks = 0; ks < 4; ks++)
-              fa[mb][ks] = fragment<kSlowA>(st + h * kHalf, read_a[mb], ks);
-        };
-        auto multiply = [&](int h) {
-          __builtin_amdgcn_s_setprio(1);
+        for (int mb = 0; mb < 2; mb++)
 #pragma unroll
           for (int ks = 0; ks < 4; ks++)
+            fa[mb][ks] = fragment<kSlowA>(st + h * kHalf, read_a[mb], ks);
+      };
+      auto multiply = [&](int h) {
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-              acc[h][i >> 1][i & 1] =
-                  mfma<I8>(fb[i >> 1][ks], fa[i & 1][ks], acc[h][i >> 1][i & 1]);
-          __builtin_amdgcn_s_setprio(0);
-        };
-        if (any0) {
+        for (int ks = 0; ks < 4; ks++)
 #pragma unroll
-          for (int h = 0; h < 2; h++)
+          for (int i = 0; i < 4; i++)
+            acc[h][i >> 1][i & 1] =
+                mfma<I8>(fb[i >> 1][ks], fa[i & 1][ks], acc[h][i >> 1][i & 1]);
+        __builtin_amdgcn_s_setprio(0);
+      };
+      if (any0) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ks++)
-              fb[h][ks] = fragment<kSlowB>(st + (2 + h) * kHalf, read_b, ks);
-          read_as(0);
-        }
-        load_a(t + 1, 1);
-        wait_loads<8>();
-        wait_lds();
-        barrier();
-        if (any0) multiply(0);
-        barrier();
-        if (any1) read_as(1);
-        load_first(t + 2);
-        wait_loads<8>();
-        wait_lds();
-        barrier();
-        if (any1) multiply(1);
-        barrier();
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int ks = 0; ks < 4; ks++)
+            fb[h][ks] = fragment<kSlowB>(st + (2 + h) * kHalf, read_b, ks);
+        read_as(0);
       }
-      wait_loads<0>();               // those behind the last step: zeros
-      if (wm == 0) barrier();
+      load1();
+      wait();
+      wait_lds();
+      barrier();
+      if (any0) multiply(0);
+      barrier();
+      if (any1) read_as(1);
+      load2();
+      wait();
+      wait_lds();
+      barrier();
+      if (any1) multiply(1);
+      barrier();
+      stage ^= 1;
+    };
+    for (int t = 0; t < KT;) {
+      // the first step, and the last three, whose loads reach the end or the next tile
+      step([&] {
+             const int s = t + 1 < KT ? t + 1 : 0;
+             load_a(kTail, a0 + s * step_a, s, stage ^ 1, 1);
+           },
+           [&] {
+             if (t == KT - 2) locate(tile + G, next);
+             const int s = t + 2 < KT ? t + 2 : t + 2 - KT;
+             load_first(kTail, a0 + s * step_a, b0 + s * step_b, s, stage);
+           },
+           [&] {
+             if (t == 0 && stores) wait_loads<8 + kStores>();
+             else wait_loads<8>();
+           });
+      t++;
+      // those between, without branches or bounds
+      const uint8_t *a1 = a0 + (t + 1) * step_a, *b2 = b0 + (t + 2) * step_b;
+      for (; t < KT - 3; t++) {
+        step([&] { load_a(kWhole, a1, 0, stage ^ 1, 1); },
+             [&] {
+               a1 += step_a;
+               load_first(kWhole, a1, b2, 0, stage);
+               b2 += step_b;
+             },
+             [] { wait_loads<8>(); });
+      }
     }
 
-    // ---- this tile's results are in registers: the next tile's first step loads meanwhile
-    const int e_ = e, nt_ = nt, nrows_ = nrows, row0_ = row0;
-    const int* slots_ = slots;
-    tile += G;
-    const bool more = tile < total;
-    if (more) {
-      slots = slots == slot_of_row[0] ? slot_of_row[1] : slot_of_row[0];
-      begin(tile, slots);
-    }
-
+    // ---- this tile's results are in registers, the next one's first loads under way.
     // Blocks of 32 by 32 through LDS, where a lane's four columns of a row become eight
-    // of another: stores of 64 bytes of a row.  It is the part of the second stage that
-    // this wavefront's own next loads fill, so that no other one is waited for.
-    uint8_t* mine = lds + kStage + w * 2048;
-    auto turn = [&](const acc_t& v, int at) {
+    // of another: stores of 64 bytes of a row.  The first 16 rows lie where this
+    // wavefront's own next load goes, so that no other one is waited for.
+    uint8_t* const mine0 = lds + (stage ^ 1) * kStage + kHalf + w * 2048;
+    uint8_t* const mine1 = lds + kSteps * kStage + w * 2048;
+    // this lane as a value of its own: what follows from it is computed here, not before
+    // the loop, whose registers are all in use
+    int v = l;
+    asm volatile("" : "+v"(v));
+    const int swizzle = (v >> 1) & 7;        // of row v % 32, that is v % 16
+    uint8_t* const to_row = (v & 16 ? mine1 : mine0) + (v & 15) * 128;
+    const int take_at = (v >> 2) * 128, take_swizzle = (v >> 3) & 7;
+    auto turn = [&](const acc_t& x) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         u32x4 q;
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          q[j] = __builtin_bit_cast(uint32_t, (val_t)v[i * 4 + j]);
-        const int r = l & 31;
-        *(u32x4*)(mine + (at + (r >> 4)) * kHalf + (r & 15) * 128 +
-                  (((2 * i + (l >> 5)) ^ ((r >> 1) & 7)) << 4)) = q;
+          q[j] = __builtin_bit_cast(uint32_t, (val_t)x[i * 4 + j]);
+        *(u32x4*)(to_row + (((2 * i + (v >> 5)) ^ swizzle) << 4)) = q;
       }
     };
-    auto take = [&](int it, int at, val_t* to) {
-      const int r = l >> 2;              // of 16; `it` which 16
+    auto take = [&](int it, val_t* to) {     // 16 rows `it`, row v / 4, columns 8 (v % 4) ..
 #pragma unroll
       for (int q = 0; q < 2; q++) {
-        const u32x4 x = *(const u32x4*)(mine + (at + it) * kHalf + r * 128 +
-                                        (((2 * (l & 3) + q) ^ ((r >> 1) & 7)) << 4));
+        const u32x4 x = *(const u32x4*)((it ? mine1 : mine0) + take_at +
+                                        (((2 * (v & 3) + q) ^ take_swizzle) << 4));
 #pragma unroll
         for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)x[j]);
       }
@@ -498,26 +566,39 @@ void product_kernel(Product p, Epi epi) {
 #pragma unroll
       for (int mb = 0; mb < 2; mb++) {
         const int r0 = h * 128 + wm * 64 + mb * 32;
-        if (r0 >= nrows_) continue;
+        if (r0 >= cur.nrows) continue;
 #pragma unroll
         for (int qn = 0; qn < (Epi::gate ? 1 : 2); qn++) {
-          turn(acc[h][qn][mb], 0);
-          if constexpr (Epi::gate) turn(acc[h][1][mb], 2);
+          val_t x[2][8], u[2][8];
+          turn(acc[h][qn][mb]);
+          take(0, x[0]);
+          take(1, x[1]);
+          if constexpr (Epi::gate) {
+            turn(acc[h][1][mb]);
+            take(0, u[0]);
+            take(1, u[1]);
+          }
 #pragma unroll
           for (int it = 0; it < 2; it++) {
-            val_t v[8], u[8];
-            take(it, 0, v);
-            if constexpr (Epi::gate) take(it, 2, u);
-            const int r = r0 + it * 16 + (l >> 2);
-            if (r >= nrows_) continue;
-            const int row = KIND == kOuter ? row0_ + r : slots_[r];
-            epi(e_, row, nt_ * (Epi::gate ? 128 : kBN) + qn * 128 + wn * 32 + (l & 3) * 8, v, u);
+            const int r = r0 + it * 16 + (v >> 2);
+            if (r >= cur.nrows) continue;
+            const int row = KIND == kOuter ? cur.row0 + r
+                            : blocks       ? p.rows.slot(cur.e, cur.row0 + r)
+                                           : cur.slot0 + r;
+            epi(cur.e, row, cur.nt * (Epi::gate ? 128 : kBN) + qn * 128 + wn * 32 + (v & 3) * 8,
+                x[it], u[it]);
           }
         }
       }
-    if (!more) break;
+    tile += G;
+    if (tile >= total) break;
+    // whole tiles store the same number of times, and so do the ones behind this here
+    stores = cur.nrows == kBM && (cur.nt + 1) * (Epi::gate ? 128 : kBN) <= epi.columns();
     wait_lds();
+    cur = next;
   }
+  wait_loads<0>();             // zeros behind the last tile
+  if (wm == 0) barrier();
 }
 
 // ---------------------------------------------------------------- few rows

@@ -54,48 +54,65 @@ namespace {
 using ep::Rows;
 using ep::quantize_rows;
 
+// v[e + 1] for e < n: the sum of v[1] .. v[e + 1], by one wavefront.
+template <class T>
+__device__ __forceinline__ void scan(T* v, int n) {
+  const int l = threadIdx.x & 63, per = (n + 63) / 64, from = l * per, to = min(n, from + per);
+  int sum = 0;
+  for (int e = from; e < to; e++) sum += v[e + 1];
+  int before = sum;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(before, d);
+    if (l >= d) before += o;
+  }
+  before -= sum;
+  for (int e = from; e < to; e++) {
+    before += v[e + 1];
+    v[e + 1] = (T)before;
+  }
+}
+
 // first[e] = row tiles of the experts before e, first[E] of all; by the whole workgroup.
-// With `shorter`, a last tile of at most half the rows counts there instead.
-[[maybe_unused]] __device__ __forceinline__ void scan_tiles(const Rows& rows, int tile, int* first,
-                                                            int* shorter = nullptr) {
-  for (int e = threadIdx.x; e < rows.E; e += blockDim.x) {
-    const int n = rows.rows_of(e), last = n % tile;
-    const bool half = shorter && last > 0 && 2 * last <= tile;
-    first[e + 1] = n / tile + (last > 0 && !half);
-    if (shorter) shorter[e + 1] = half;
-  }
-  if (threadIdx.x == 0) {
-    first[0] = 0;
-    if (shorter) shorter[0] = 0;
-  }
+[[maybe_unused]] __device__ __forceinline__ void scan_tiles(const Rows& rows, int tile,
+                                                            int* first) {
+  for (int e = threadIdx.x; e < rows.E; e += blockDim.x)
+    first[e + 1] = (rows.rows_of(e) + tile - 1) / tile;
+  if (threadIdx.x == 0) first[0] = 0;
   __syncthreads();
-  // a wavefront for each of the two sums
-  if (threadIdx.x < 64 || (shorter && threadIdx.x < 128)) {
-    const int l = threadIdx.x & 63;
-    int* v = threadIdx.x < 64 ? first : shorter;
-    const int per = (rows.E + 63) / 64, from = l * per, to = min(rows.E, from + per);
-    int sum = 0;
-    for (int e = from; e < to; e++) sum += v[e + 1];
-    int before = sum;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(before, d);
-      if (l >= d) before += o;
-    }
-    before -= sum;
-    for (int e = from; e < to; e++) {
-      before += v[e + 1];
-      v[e + 1] = before;
-    }
-  }
+  if (threadIdx.x < 64) scan(first, rows.E);
   __syncthreads();
 }
 
+// What a workgroup that walks over many tiles keeps of the experts: their rows and first
+// slots, and the row tiles before each, where a last tile of at most half the rows is
+// counted apart.
+struct Experts {
+  int count[EP_MAX_EXPERTS], slot[EP_MAX_EXPERTS], first[EP_MAX_EXPERTS + 1];
+  uint16_t first_short[EP_MAX_EXPERTS + 2];
+  __device__ __forceinline__ void fill(const Rows& rows, int tile) {
+    for (int e = threadIdx.x; e < rows.E; e += blockDim.x) {
+      const int n = rows.rows_of(e), last = n % tile;
+      const bool half = last > 0 && 2 * last <= tile;
+      count[e] = n;
+      slot[e] = rows.base_slot(e, 0);
+      first[e + 1] = n / tile + (last > 0 && !half);
+      first_short[e + 1] = half;
+    }
+    if (threadIdx.x == 0) first[0] = first_short[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 64) scan(first, rows.E);
+    else if (threadIdx.x < 128) scan(first_short, rows.E);
+    __syncthreads();
+  }
+};
+
 // The expert whose tiles hold tile i: first[e] <= i < first[e + 1].
-[[maybe_unused]] __device__ __forceinline__ int find_expert(const int* first, int E, int i) {
+template <class T>
+__device__ __forceinline__ int find_expert(const T* first, int E, int i) {
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__builtin_amdgcn_readfirstlane(first[mid]) <= i) lo = mid;
+    if (__builtin_amdgcn_readfirstlane((int)first[mid]) <= i) lo = mid;
     else hi = mid;
   }
   return lo;
