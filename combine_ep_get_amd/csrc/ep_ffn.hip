@@ -3,6 +3,7 @@
 #include "ep_host.h"
 #include "ep_rows.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace {
@@ -102,21 +103,11 @@ __device__ __forceinline__ i32x4 descriptor(const uint8_t* p) {
   return d;
 }
 
-__device__ __forceinline__ u32x4 pack8(const float* v) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    bf16x2 p = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
-    r[i] = __builtin_bit_cast(uint32_t, p);
-  }
-  return r;
-}
-
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
 
 // ---------------------------------------------------------------- epilogues
-// What becomes of eight neighbouring columns of a row of D.  `slot` is the row's slot
+// What becomes of eight neighbouring columns of a row of D; put: of eight that are rounded
+// to bf16 already (bf16 products, where that comes first, with n % 8 == 0).  `slot` is the row's slot
 // (kOuter: its row of the expert's matrix), `e` the expert, `c` the first column.
 // `stores` is how many of them a wavefront sends at least for a whole tile (16 calls, 8 of
 // a gate).
@@ -127,6 +118,11 @@ struct StoreRows {
   uint16_t* y;
   int n;
   const float *sx, *sw;    // 8-bit products: scales per slot and per expert and column
+  static constexpr bool rounds = true;
+  __device__ __forceinline__ void put(int, int slot, int c, u32x4 r, int more) const {
+    c += more;
+    if (c < n) *(u32x4*)(y + (int64_t)slot * n + c) = r;
+  }
   template <class T>
   __device__ __forceinline__ void operator()(int e, int slot, int c, const T* v, const T*) const {
     if (c >= n) return;
@@ -159,6 +155,11 @@ struct StoreMatrix {       // kOuter: [e][m][n]
   __device__ __forceinline__ int columns() const { return n; }
   uint16_t* y;
   int m, n;
+  static constexpr bool rounds = true;
+  __device__ __forceinline__ void put(int e, int row, int c, u32x4 r, int more) const {
+    c += more;
+    if (c < n) *(u32x4*)(y + ((int64_t)e * m + row) * n + c) = r;
+  }
   __device__ __forceinline__ void operator()(int e, int row, int c, const float* v,
                                              const float*) const {
     if (c >= n) return;
@@ -175,6 +176,12 @@ struct StoreGate {
   uint16_t* gu;            // [slot][2 inter] or NULL
   int inter;
   const float *sx, *sw;
+  static constexpr bool rounds = true;
+  __device__ __forceinline__ void put(int, int slot, int c, u32x4 r, int what) const {
+    if (c >= inter) return;
+    if (what == 0) *(u32x4*)(h + (int64_t)slot * inter + c) = r;
+    else *(u32x4*)(gu + (int64_t)slot * 2 * inter + (what - 1) * inter + c) = r;
+  }
   template <class T>
   __device__ __forceinline__ void operator()(int e, int slot, int c, const T* g, const T* u) const {
     if (c >= inter) return;
@@ -209,6 +216,7 @@ struct StoreGate {
 struct StoreGateGrad {
   static constexpr bool gate = false;
   static constexpr int stores = 48;
+  static constexpr bool rounds = false;
   __device__ __forceinline__ int columns() const { return inter; }
   const uint16_t* gu;      // [slot][2 inter]
   uint16_t* dgu;           // [slot][2 inter]
@@ -288,10 +296,19 @@ void product_kernel(Product p, Epi epi) {
   const int MT = (p.m + kBM - 1) / kBM;                    // kOuter
   const bool blocks = p.rows.count && !p.rows.offset;      // rows of several sub-blocks
   experts.fill(p.rows, kBM);
-  // tiles, and those of over 128 rows
-  const int tall = KIND == kOuter ? 0 : uniform(experts.first[p.rows.E]) * NT;
-  const int total = KIND == kOuter ? p.rows.E * MT * NT
-                                   : tall + uniform(experts.first_short[p.rows.E]) * NT;
+  // tiles, those of over 128 rows, and those that are taken as two halves of 128 rows
+  // because a round of the grid's workgroups with these halves is all that is left
+  const int G = gridDim.x;
+  int total = p.rows.E * MT * NT, tall = 0, halved = 0;
+  if constexpr (KIND != kOuter) {
+    tall = uniform(experts.first[p.rows.E]) * NT;
+    total = tall + uniform(experts.first_short[p.rows.E]) * NT;
+    const int rest = tall % G;
+    if (rest > 0 && total - tall + 2 * rest <= G) {
+      halved = rest;
+      total += rest;
+    }
+  }
 
   // where this lane's bytes of a load go (a wavefront sends two loads per half: rows
   // w*16 + 8 j + l/8, or k w*8 + 4 j + l/16), and where it reads
@@ -374,8 +391,9 @@ void product_kernel(Product p, Epi epi) {
     } else {
       // the short ones last: they take half the time, and a workgroup whose share was all
       // tall ones would keep the others waiting
-      const bool is_short = tile >= tall;
-      const int at = is_short ? tile - tall : tile;
+      const bool is_short = tile >= tall + halved;
+      const int half = tile - (tall - halved);               // of a halved one
+      const int at = is_short ? tile - (tall + halved) : half >= 0 ? tall - halved + half / 2 : tile;
       x.e = is_short ? find_expert(experts.first_short, p.rows.E, at / NT)
                      : find_expert(experts.first, p.rows.E, at / NT);
       const int f0 = uniform(experts.first[x.e]), mts = uniform(experts.first[x.e + 1]) - f0;
@@ -389,7 +407,12 @@ void product_kernel(Product p, Epi epi) {
         x.row0 = (f + q % gs) * kBM;
         x.nt = q / gs;
       }
-      x.nrows = min(kBM, uniform(experts.count[x.e]) - x.row0);
+      int most = kBM;
+      if (!is_short && half >= 0) {
+        most = kBM / 2;
+        x.row0 += half % 2 * most;
+      }
+      x.nrows = min(most, uniform(experts.count[x.e]) - x.row0);
       x.slot0 = uniform(experts.slot[x.e]) + (blocks ? 0 : x.row0);
       a0 = p.a + (int64_t)x.slot0 * p.a_row;
       b0 = p.b + (int64_t)x.e * p.b_expert;
@@ -426,7 +449,6 @@ void product_kernel(Product p, Epi epi) {
   };
 
   // workgroup ids go round robin over the 8 XCDs: give each XCD neighbouring tiles
-  const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
   if (tile >= total) return;
   Tile cur, next;
@@ -561,32 +583,73 @@ void product_kernel(Product p, Epi epi) {
         for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)x[j]);
       }
     };
+    // the same for values that are rounded to bf16 already: half the bytes
+    auto turn16 = [&](const f32x16& x) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *(u32x2*)(mine0 + (v & 31) * 64 + ((i ^ ((v >> 2) & 3)) << 4) + (v >> 5) * 8) =
+            u32x2{pack2(x[i * 4], x[i * 4 + 1]), pack2(x[i * 4 + 2], x[i * 4 + 3])};
+    };
+    auto take16 = [&](int it) {
+      return *(const u32x4*)(mine0 + it * 1024 + (v >> 2) * 64 +
+                             (((v & 3) ^ ((v >> 4) & 3)) << 4));
+    };
+    auto row_at = [&](int r) {
+      return KIND == kOuter ? cur.row0 + r
+             : blocks       ? p.rows.slot(cur.e, cur.row0 + r)
+                            : cur.slot0 + r;
+    };
+    const int c0 = cur.nt * (Epi::gate ? 128 : kBN) + wn * 32 + (v & 3) * 8;
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
       for (int mb = 0; mb < 2; mb++) {
         const int r0 = h * 128 + wm * 64 + mb * 32;
         if (r0 >= cur.nrows) continue;
+        if constexpr (Epi::rounds && !I8) {
+          // `what` is turned and stored by epi.put (a gate: h, and g and u where asked for)
+          auto put = [&](const f32x16& x, int what) {
+            turn16(x);
+            const u32x4 q[2] = {take16(0), take16(1)};
 #pragma unroll
-        for (int qn = 0; qn < (Epi::gate ? 1 : 2); qn++) {
-          val_t x[2][8], u[2][8];
-          turn(acc[h][qn][mb]);
-          take(0, x[0]);
-          take(1, x[1]);
+            for (int it = 0; it < 2; it++) {
+              const int r = r0 + it * 16 + (v >> 2);
+              if (r < cur.nrows) epi.put(cur.e, row_at(r), c0, q[it], what);
+            }
+          };
           if constexpr (Epi::gate) {
-            turn(acc[h][1][mb]);
-            take(0, u[0]);
-            take(1, u[1]);
-          }
+            f32x16 x;
 #pragma unroll
-          for (int it = 0; it < 2; it++) {
-            const int r = r0 + it * 16 + (v >> 2);
-            if (r >= cur.nrows) continue;
-            const int row = KIND == kOuter ? cur.row0 + r
-                            : blocks       ? p.rows.slot(cur.e, cur.row0 + r)
-                                           : cur.slot0 + r;
-            epi(cur.e, row, cur.nt * (Epi::gate ? 128 : kBN) + qn * 128 + wn * 32 + (v & 3) * 8,
-                x[it], u[it]);
+            for (int j = 0; j < 16; j++) {
+              const float g = acc[h][0][mb][j];
+              x[j] = g * sigmoid(g) * acc[h][1][mb][j];
+            }
+            put(x, 0);
+            if (epi.gu) {
+              put(acc[h][0][mb], 1);
+              put(acc[h][1][mb], 2);
+            }
+          } else {
+            put(acc[h][0][mb], 0);
+            put(acc[h][1][mb], 128);
+          }
+        } else {
+#pragma unroll
+          for (int qn = 0; qn < (Epi::gate ? 1 : 2); qn++) {
+            val_t x[2][8], u[2][8];
+            turn(acc[h][qn][mb]);
+            take(0, x[0]);
+            take(1, x[1]);
+            if constexpr (Epi::gate) {
+              turn(acc[h][1][mb]);
+              take(0, u[0]);
+              take(1, u[1]);
+            }
+#pragma unroll
+            for (int it = 0; it < 2; it++) {
+              const int r = r0 + it * 16 + (v >> 2);
+              if (r < cur.nrows) epi(cur.e, row_at(r), c0 + qn * 128, x[it], u[it]);
+            }
           }
         }
       }
@@ -979,56 +1042,115 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
 template <int KIND, class Epi, bool I8>
 int launch(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
   // one workgroup per CU at most: each takes more than half of a CU's LDS
-  const int grid = (int)(tiles < 256 ? tiles : 256);
+  // (twice the tiles: they may be taken by halves)
+  const int grid = (int)(tiles < 128 ? 2 * tiles : 256);
   product_kernel<KIND, Epi, I8><<<dim3(grid), dim3(512), 0, st>>>(p, epi);
   return check_launch("ep_ffn product");
 }
 
+// ---------------------------------------------------------------- which kernel
+// Times in us that the choice between the kernels goes by, fitted to measurements of both
+// sides (MI355X, graph replays); only their order matters.  Row tiles are counted on the
+// device, so they go by the bound of all rows, taken as spread evenly.
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Most row tiles that max_rows rows of E experts can make.
+int64_t row_tiles(const Rows& r, int max_rows, int tile) { return (int64_t)max_rows / tile + r.E; }
+
+// 256 by 256 tiles, `tiles` of them, `steps` of 128 bytes of the contraction: a step takes
+// 0.86 us on half a tile's rows, 1.3 on a whole tile's, 1.25 where all CUs stream weights.
+double wide_us(int64_t tiles, int64_t steps, double rows) {
+  if (tiles >= 200) return 4 + (double)ceil_div(tiles, 256) * ((double)steps * 1.25 + 6);
+  return 10 + (double)steps * (rows > 128 ? 1.3 : 0.86);
+}
+
 template <class Epi, bool I8, int TT, bool FUSE>
-int launch_few(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
+int launch_few(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t st) {
+  const int64_t tiles = row_tiles * ceil_div(p.n, Epi::gate ? 16 : 32);
   const int grid = (int)(tiles < 512 ? tiles : 512);       // two workgroups per CU
   few_kernel<Epi, I8, TT, FUSE><<<dim3(grid), dim3(256), 0, st>>>(p, epi);
   return check_launch("ep_ffn few rows");
 }
 
-// Row tiles are counted on the device; here only their upper bound.
-int64_t row_tiles(const Rows& r, int max_rows) { return (int64_t)max_rows / kBM + r.E; }
+// Activations by a weight's rows.  Measured, few rows against wide tiles (us): one row by
+// 7168 x 7168 int8 11 : 53, 64 rows 20 : 64, 256 rows 63 : 80, 512 rows 118 : 82; 512 rows by
+// 512 x 7168 19 : 73; 32 experts of 4 rows each, bf16, both products of the block 414 : 472,
+// of 32 rows 526 : 477.
+template <class Epi, bool I8>
+int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
+  const int E = p.rows.E, wide = Epi::gate ? 128 : kBN;
+  const double rows = (double)max_rows / E, cols = Epi::gate ? 2.0 * p.n : p.n;
+  const int64_t steps = ceil_div(p.k, 128);
+  const int few = rows <= 8 ? 16 : 32;
+  const double few_tiles = E * std::max(1.0, rows <= few ? rows / few + 0.5 : rows / few + 0.25);
+  const double bytes = few_tiles * cols * p.k;             // of weights, for each row tile again
+  const double rounds = std::max(1.0, few_tiles * (cols / 32) / 512);
+  const double few_us = 4 + std::max(bytes / (few == 16 ? 7.0e6 : 6.5e6),
+                                     rounds * ((double)ceil_div(steps, 4) * 0.35 + 1));
+  const int64_t wide_tiles = E * std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5)) *
+                             ceil_div(p.n, wide);
+  if (few_us < wide_us(wide_tiles, steps, rows)) {
+    if (few == 16) return launch_few<Epi, I8, 1, false>(p, epi, row_tiles(p.rows, max_rows, 16), st);
+    return launch_few<Epi, I8, 2, false>(p, epi, row_tiles(p.rows, max_rows, 32), st);
+  }
+  return launch<kRowsT, Epi, I8>(p, epi, row_tiles(p.rows, max_rows, kBM) * ceil_div(p.n, wide),
+                                 st);
+}
 
-// A gradient, by the kernel for small or for large ones.
+// A gradient.  Measured, small tiles against wide ones: 12 experts of 88 rows, 1000 x 344: dh
+// 14 : 39, dx 16 : 20, dw13 33 : 15; one matrix of 1024 rows, 2048 x 1024, all four 88 : 149; 8
+// experts of 512 rows, 1024 x 1024, all four 187 : 126.
 template <int KIND, class Epi>
 int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
-  const int mode = getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : 0;
+  const int E = p.rows.E;
+  const double rows = (double)max_rows / E;
   auto tiles = [&](int t) {
-    const int64_t m = KIND == kOuter ? (int64_t)p.rows.E * ((p.m + t - 1) / t)
-                                     : (int64_t)max_rows / t + p.rows.E;
-    return m * ((p.n + t - 1) / t);
+    const int64_t m = KIND == kOuter ? ceil_div(p.m, t) : std::max<int64_t>(1, (int64_t)(rows / t + 0.5));
+    return E * m * ceil_div(p.n, t);
   };
-  if (mode) {
-    const int64_t n = tiles(kST);
+  const int64_t steps = KIND == kOuter ? (int64_t)(rows / 64) + 1 : ceil_div(p.k, 128);
+  const double small_us =
+      5 + (double)ceil_div(tiles(kST), 256) * ((double)ceil_div(steps, 4) * 1.8 + 1.5);
+  if (small_us < wide_us(tiles(kBM), steps, KIND == kOuter ? kBM : rows)) {
+    const int64_t n = KIND == kOuter ? tiles(kST)
+                                     : row_tiles(p.rows, max_rows, kST) * ceil_div(p.n, kST);
     small_kernel<KIND, Epi><<<dim3((int)(n < 256 ? n : 256)), dim3(256), 0, st>>>(p, epi);
     return check_launch("ep_ffn small product");
   }
-  return launch<KIND, Epi, false>(p, epi, tiles(kBM), st);
-}
-
-// Activations by a weight's rows, by the kernel for few or for many of them.
-template <class Epi, bool I8>
-int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
-  const int mode = getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : 0;
-  const int few = Epi::gate ? 16 : 32;
-  const int64_t nt = (p.n + few - 1) / few;
-  if (mode == 1)
-    return launch_few<Epi, I8, 1, false>(p, epi, (max_rows / 16 + p.rows.E) * nt, st);
-  if (mode == 2)
-    return launch_few<Epi, I8, 2, false>(p, epi, (max_rows / 32 + p.rows.E) * nt, st);
-  const int wide = Epi::gate ? 128 : kBN;
-  return launch<kRowsT, Epi, I8>(p, epi, row_tiles(p.rows, max_rows) * ((p.n + wide - 1) / wide),
-                                 st);
+  const int64_t n = KIND == kOuter ? tiles(kBM)
+                                   : row_tiles(p.rows, max_rows, kBM) * ceil_div(p.n, kBN);
+  return launch<KIND, Epi, false>(p, epi, n, st);
 }
 
 // Whether every workgroup rounds x to integers by itself.
 bool fuses(const Rows& r, int max_rows, int cols) {
   return !r.count && max_rows <= 16 && (int64_t)max_rows * cols <= kFuseBytes;
+}
+
+// Rows of bf16 by an 8-bit weight: rounded by the product itself, or before it into
+// `codes` and `scales`, which `epi` reads.
+template <class Epi>
+int run_int8(Product p, const Epi& epi, int max_rows, const void* x, uint8_t* codes, float* scales,
+             hipStream_t st) {
+  p.a = (const uint8_t*)x;
+  p.a_row = 2 * p.k;
+  if (fuses(p.rows, max_rows, p.k)) return launch_few<Epi, true, 1, true>(p, epi, 1, st);
+  const int rc = quantize_rows(p.rows, max_rows, x, p.k, codes, scales, st);
+  if (rc != EP_OK) return rc;
+  p.a = codes;
+  p.a_row = p.k;
+  return run_rows<Epi, true>(p, epi, max_rows, st);
+}
+
+template <class Epi>
+int run_bf16(Product p, const Epi& epi, int max_rows, const void* x, hipStream_t st) {
+  p.a = (const uint8_t*)x;
+  p.a_row = p.k;
+  return run_rows<Epi, false>(p, epi, max_rows, st);
+}
+
+// Tiles are counted in 32 bits, the smallest of them of 16 rows by 16 columns.
+bool few_enough(const Rows& r, int cols) {
+  return row_tiles(r, r.cap, 16) * ceil_div(cols, 16) <= INT32_MAX;
 }
 
 // Offsets inside an expert's sub-blocks have 32 bits (see descriptor()).
@@ -1068,7 +1190,9 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
     return EP_ERR_INVALID_ARG;
   const int bytes = i8 ? 1 : 2;
   const Rows r = device_rows(rows);
-  if (!fits_region(r, (int64_t)H * 2) || !fits_region(r, (int64_t)I * 2)) return EP_ERR_INVALID_ARG;
+  if (!fits_region(r, (int64_t)H * 2) || !fits_region(r, (int64_t)I * 2) ||
+      !few_enough(r, std::max(H, 2 * I)))
+    return EP_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != EP_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
@@ -1080,37 +1204,25 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
   float* sx = (float*)(hq + up(cap * I));
   float* sh = (float*)((uint8_t*)sx + up(cap * 4));
   EP_LOG("ffn experts=%d max_rows=%d H=%d I=%d int8=%d", r.E, rows->max_rows, H, I, (int)i8);
-  if (i8) {
-    rc = quantize_rows(r, rows->max_rows, a->x, H, xq, sx, st);
-    if (rc != EP_OK) return rc;
-  }
   Product p{};
   p.rows = r;
-  p.a = i8 ? xq : (const uint8_t*)a->x;
   p.b = (const uint8_t*)a->w13.data;
-  p.k = H * bytes;
-  p.a_row = p.b_row = p.k;
+  p.k = p.b_row = H * bytes;
   p.b_expert = (int64_t)2 * I * p.k;
   p.n = I;
   p.far = I;
   const StoreGate gate{(uint16_t*)h, (uint16_t*)a->gate_up, I, sx, (const float*)a->w13.scales};
-  rc = i8 ? run_rows<StoreGate, true>(p, gate, rows->max_rows, st)
-          : run_rows<StoreGate, false>(p, gate, rows->max_rows, st);
+  rc = i8 ? run_int8(p, gate, rows->max_rows, a->x, xq, sx, st)
+          : run_bf16(p, gate, rows->max_rows, a->x, st);
   if (rc != EP_OK) return rc;
-  if (i8) {
-    rc = quantize_rows(r, rows->max_rows, h, I, hq, sh, st);
-    if (rc != EP_OK) return rc;
-  }
-  p.a = i8 ? hq : h;
   p.b = (const uint8_t*)a->w2.data;
-  p.k = I * bytes;
-  p.a_row = p.b_row = p.k;
+  p.k = p.b_row = I * bytes;
   p.b_expert = (int64_t)H * p.k;
   p.n = H;
   p.far = 0;
   const StoreRows out{(uint16_t*)a->y, H, sh, (const float*)a->w2.scales};
-  return i8 ? run_rows<StoreRows, true>(p, out, rows->max_rows, st)
-            : run_rows<StoreRows, false>(p, out, rows->max_rows, st);
+  return i8 ? run_int8(p, out, rows->max_rows, h, hq, sh, st)
+            : run_bf16(p, out, rows->max_rows, h, st);
 }
 
 int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* stream) {
@@ -1121,6 +1233,9 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   const int H = a->hidden, I = a->inter;
   const Rows r = device_rows(rows);
   if (r.count && !r.offset) return EP_ERR_INVALID_ARG;   // low-latency sub-blocks
+  if (!few_enough(r, std::max(H, 2 * I)) ||
+      r.E * ceil_div(std::max(H, 2 * I), kST) * ceil_div(std::max(H, I), kST) > INT32_MAX)
+    return EP_ERR_INVALID_ARG;
   const bool any = rows->max_rows > 0;
   if (!a->w13 || !a->w2 || !a->dw13 || !a->dw2 || !aligned(a->workspace, 256) ||
       (any && (!a->x || !a->dy || !a->gate_up || !a->dx || !a->workspace)) || !aligned16(a->x) ||
@@ -1195,43 +1310,27 @@ int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* a, void* s
     return EP_ERR_INVALID_ARG;
   const Rows r = device_rows(rows);
   if (!fits_region(r, C)) return EP_ERR_INVALID_ARG;
-  const int64_t tiles_n = (O + kBN - 1) / kBN;
-  if (row_tiles(r, rows->max_rows) * tiles_n > INT32_MAX) return EP_ERR_INVALID_ARG;
+  if (!few_enough(r, O)) return EP_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != EP_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
-  const uint8_t* xq = (const uint8_t*)a->x;
-  const float* sx = a->x_scales;
-  if (!sx && fuses(r, rows->max_rows, C)) {
-    Product p{};
-    p.rows = r;
-    p.a = xq;
-    p.b = (const uint8_t*)a->w.data;
-    p.k = p.b_row = C;
-    p.a_row = 2 * C;
-    p.n = O;
-    const StoreRows out{(uint16_t*)a->y, O, nullptr, (const float*)a->w.scales};
-    return launch_few<StoreRows, true, 1, true>(p, out, (O + 31) / 32, st);
-  }
-  if (!sx) {
-    uint8_t* q = (uint8_t*)a->workspace;
-    float* s = (float*)(q + up(rows->capacity * C));
-    rc = quantize_rows(r, rows->max_rows, a->x, C, q, s, st);
-    if (rc != EP_OK) return rc;
-    xq = q;
-    sx = s;
-  }
-  EP_LOG("int8_linear experts=%d max_rows=%d cols=%d out=%d", r.E, rows->max_rows, C, O);
+  EP_LOG("integer_linear experts=%d max_rows=%d cols=%d out=%d", r.E, rows->max_rows, C, O);
   Product p{};
   p.rows = r;
-  p.a = xq;
   p.b = (const uint8_t*)a->w.data;
-  p.k = C;
-  p.a_row = p.b_row = C;
+  p.k = p.b_row = C;
   p.b_expert = (int64_t)O * C;
   p.n = O;
-  const StoreRows out{(uint16_t*)a->y, O, sx, (const float*)a->w.scales};
-  return run_rows<StoreRows, true>(p, out, rows->max_rows, st);
+  StoreRows out{(uint16_t*)a->y, O, a->x_scales, (const float*)a->w.scales};
+  if (a->x_scales) {
+    p.a = (const uint8_t*)a->x;
+    p.a_row = C;
+    return run_rows<StoreRows, true>(p, out, rows->max_rows, st);
+  }
+  uint8_t* codes = (uint8_t*)a->workspace;
+  float* scales = (float*)(codes + up(rows->capacity * C));
+  out.sx = scales;
+  return run_int8(p, out, rows->max_rows, a->x, codes, scales, st);
 }
 
 }  // extern "C"

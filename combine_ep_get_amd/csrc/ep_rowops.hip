@@ -48,12 +48,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t*
 constexpr int kPairs = 8;      // pairs of a token handled together
 constexpr int kMostWaves = 16;
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 p = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, p);
-}
-
 // A workgroup per token, with as many threads as the row has 16-byte chunks (up to 1024):
 // all loads of a token are in flight at once, and dy's row is read once for all
 // pairs.  The sums meet in LDS at the end, in a fixed order.

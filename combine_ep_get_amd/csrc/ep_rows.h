@@ -129,6 +129,15 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   }
 }
 
+[[maybe_unused]] __device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+[[maybe_unused]] __device__ __forceinline__ u32x4 pack8(const float* v) {
+  return u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+}
+
 // ---------------------------------------------------------------- rows as 8-bit integers
 // The largest magnitude of eight bf16 values as bits: they are ordered as the values are,
 // infinities and NaN last.
