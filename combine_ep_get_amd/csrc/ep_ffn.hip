@@ -132,7 +132,7 @@ struct StoreRows {
       const float s = sx[slot];
       const float* w = sw + (int64_t)e * n + c;
 #pragma unroll
-      for (int i = 0; i < 8; i++) f[i] = (float)v[i] * s * (i < left ? w[i] : 0.f);
+      for (int i = 0; i < 8; i++) f[i] = (float)v[i] * s * w[min(i, left - 1)];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++) f[i] = v[i];
@@ -687,7 +687,7 @@ __device__ __forceinline__ typename Acc4<I8>::type mfma16(u32x4 a, u32x4 b,
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-constexpr int kFuseBytes = 32768;      // codes of x in LDS
+constexpr int kFuseBytes = 32768;      // x in LDS, in bf16
 
 template <class Epi, bool I8, int TT, bool FUSE>
 __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
@@ -701,42 +701,43 @@ __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
   static_assert(kMine >= kRowsX * 32 * 4, "a wavefront's sums fit where its stages were");
 
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kMine + (FUSE ? kFuseBytes : 0)];
-  __shared__ int first_tile[EP_MAX_EXPERTS + 1];
   __shared__ int slots[kRowsX];
-  __shared__ float scale[16];
-  __shared__ uint32_t tops[4];
+  __shared__ float scale[16];            // FUSE: of each row of x
+  __shared__ RowScale scales[FUSE ? 16 : 1];
+  __shared__ uint32_t tops[16];
 
   const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
   const uint32_t mine = lds0 + w * kMine;
   const uint8_t* my = lds + w * kMine;
   const int NT = (p.n + kCols - 1) / kCols, KT = (p.k + 127) / 128, NI = (KT + 3) / 4;
-  int total = NT;
-  if constexpr (!FUSE) {
-    scan_tiles(p.rows, kRowsX, first_tile);
-    total = uniform(first_tile[p.rows.E]) * NT;
-  }
   const int64_t far = (int64_t)p.far * p.b_row;
   auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
   const int read = (l & 15) * 128 + (((l >> 4) ^ ((l >> 1) & 7)) << 4);
   const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
-  for (; tile < total; tile += G) {
+  const bool blocks = p.rows.count && !p.rows.offset;
+  for (;; tile += G) {
     int e = 0, nt = tile, nrows = p.rows.plain, slot0 = 0;
     if constexpr (!FUSE) {
-      e = find_expert(first_tile, p.rows.E, tile / NT);
-      const int f0 = uniform(first_tile[e]), mts = uniform(first_tile[e + 1]) - f0;
-      const int r = tile - f0 * NT;
-      const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, mts - f);
+      Found x;
+      if (!find_rows(p.rows, kRowsX, tile / NT, x)) break;
+      e = x.e;
+      const int r = tile - x.first * NT;
+      const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, x.tiles - f);
       const int q = r - g * kGroupM * NT;
       const int row0 = (f + q % gs) * kRowsX;
       nt = q / gs;
-      nrows = min(kRowsX, uniform(p.rows.rows_of(e)) - row0);
-      if (tid < kRowsX) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
-      slot0 = uniform(p.rows.base_slot(e, row0));
+      nrows = min(kRowsX, x.count - row0);
+      slot0 = x.slot + (blocks ? 0 : row0);
+      if (tid < kRowsX)
+        slots[tid] = tid >= nrows ? -1 : blocks ? p.rows.slot(e, row0 + tid) : slot0 + tid;
       __syncthreads();
+    } else if (tile >= NT) {
+      break;
     } else if (tid < kRowsX) {
       slots[tid] = tid < nrows ? tid : -1;
+      tops[tid] = 0;
     }
     const uint8_t* a0 = p.a + (int64_t)slot0 * p.a_row;
     const uint8_t* b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kCols * p.b_row;
@@ -769,41 +770,57 @@ __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
           load_lds<false>(to + kW + j * 1024, chunk_k(j) * 16 < p.k - at ? off_x[j] : kAbsent, d);
       }
     };
-    // x is still bf16 (FUSE): p.a_row counts its bytes, and rows of codes have p.k.  Its
-    // first row is asked for before the weights, since loads arrive in order.
-    u32x4 held[4];
-    const int chunks = p.k / 8;
-    auto take = [&](const u32x4* in) {
+    // x is still bf16 (FUSE): p.a_row counts its bytes.  It is asked for before the weights,
+    // since loads arrive in order.
+    uint8_t* const xs = lds + 4 * kMine;
+    if constexpr (FUSE) {
+      const i32x4 d = descriptor(p.a);
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        held[i] = i * 256 + tid < chunks ? in[i * 256 + tid] : u32x4{0, 0, 0, 0};
-    };
-    if constexpr (FUSE) take((const u32x4*)p.a);
+      for (int j = 0; j < kFuseBytes / 4096; j++) {
+        const int at = (j * 4 + w) * 1024;
+        load_lds<false>(lds0 + 4 * kMine + at, at + l * 16 < nrows * (int)p.a_row ? at + l * 16 : kAbsent,
+                        d);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kDepth; i++) load(i, i);
-
     if constexpr (FUSE) {
-      for (int r = 0; r < nrows; r++) {
-        const u32x4* in = (const u32x4*)(p.a + r * p.a_row);
-        if (r > 0) take(in);
-        uint32_t top = 0;
+      wait_loads<kDepth * kLoads>();
+      __syncthreads();
+      // every thread holds its chunks of all rows, so the codes may take their place
+      constexpr int kHeld = kFuseBytes / 4096;
+      const int per = p.k / 8, chunks = nrows * per;
+      u32x4 held[kHeld];
+      int row[kHeld];
 #pragma unroll
-        for (int i = 0; i < 4; i++) top = max(top, largest8(held[i]));
-        for (int c = 1024 + tid; c < chunks; c += 256) top = max(top, largest8(in[c]));
-        top = wave_max(top);
-        if (l == 0) tops[w] = top;
-        __syncthreads();
-        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-        const RowScale s(top);
-        if (tid == 0) scale[r] = s.scale;
-        u32x2* out = (u32x2*)(lds + 4 * kMine + r * p.k);
+      for (int i = 0; i < kHeld; i++) {
+        const int c = i * 256 + tid;
+        row[i] = c / per;
+        if (i * 256 >= chunks) break;
+        held[i] = *(const u32x4*)(xs + min(c, chunks - 1) * 16);
+        const uint32_t top = largest8(held[i]);
+        const int r = min(row[i], nrows - 1), r0 = uniform(r);
+        if (__all(r == r0)) {
+          const uint32_t of_row = wave_max(top);
+          if (l == 0) atomicMax(&tops[r0], of_row);
+        } else {
+          atomicMax(&tops[r], top);
+        }
+      }
+      __syncthreads();
+      if (tid < nrows) {
+        const RowScale s = RowScale::of(tops[tid]);
+        scales[tid] = s;
+        scale[tid] = s.scale;
+      }
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (i * 256 + tid < chunks) out[i * 256 + tid] = s.codes8(held[i]);
-        for (int c = 1024 + tid; c < chunks; c += 256) out[c] = s.codes8(in[c]);
-        __syncthreads();
+      for (int i = 0; i < kHeld; i++) {
+        const int c = i * 256 + tid;
+        if (c < chunks) *(u32x2*)(xs + c * 8) = scales[row[i]].codes8(held[i]);
       }
       epi.sx = scale;
+      __syncthreads();
     }
 
     acc_t acc[2][TT];
@@ -823,7 +840,7 @@ __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
         if constexpr (FUSE) {
           const int at = (i * 4 + w) * 128 + m * 64 + (l >> 4) * 16;
           fx[0][m] = (l & 15) < nrows && at < p.k
-                         ? *(const u32x4*)(lds + 4 * kMine + (l & 15) * p.k + at)
+                         ? *(const u32x4*)(xs + (l & 15) * p.k + at)
                          : u32x4{0, 0, 0, 0};
         } else {
 #pragma unroll
@@ -889,20 +906,12 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
   constexpr int kOp = 8192, kSmallStage = 2 * kOp, kMine = 2 * kSmallStage, kLoads = 16;
 
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kMine];
-  __shared__ int first_tile[EP_MAX_EXPERTS + 1];
   __shared__ int slots[kST];
 
   const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
   const uint32_t mine = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds + w * kMine;
   const uint8_t* my = lds + w * kMine;
   const int NT = (p.n + kST - 1) / kST, MT = (p.m + kST - 1) / kST;
-  int total;
-  if constexpr (KIND == kOuter) {
-    total = p.rows.E * MT * NT;
-  } else {
-    scan_tiles(p.rows, kST, first_tile);
-    total = uniform(first_tile[p.rows.E]) * NT;
-  }
   // chunk c of row r at c ^ (r / 2 & 7); where k is slow, of 128 bytes of a k at c ^ 4 (k / 2 & 1)
   auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
   const int chunk_n = (l & 7) ^ (((l >> 4) & 1) << 2);
@@ -925,10 +934,12 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
 
   const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
-  for (; tile < total; tile += G) {
+  const bool blocks = p.rows.count && !p.rows.offset;
+  for (;; tile += G) {
     int e, nt, nrows, row0, slot0, k_a, k_b, KT;
     const uint8_t *a0, *b0;
     if constexpr (KIND == kOuter) {
+      if (tile >= p.rows.E * MT * NT) break;
       e = tile / (MT * NT);
       const int r = tile - e * MT * NT;
       row0 = r / NT * kST;
@@ -940,14 +951,16 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
       a0 = p.a + (int64_t)slot0 * p.a_row + (int64_t)row0 * 2;
       b0 = p.b + (int64_t)slot0 * p.b_row + (int64_t)nt * kST * 2;
     } else {
-      e = find_expert(first_tile, p.rows.E, tile / NT);
-      const int f0 = uniform(first_tile[e]);
-      const int r = tile - f0 * NT;
+      Found x;
+      if (!find_rows(p.rows, kST, tile / NT, x)) break;
+      e = x.e;
+      const int r = tile - x.first * NT;
       row0 = r / NT * kST;
       nt = r % NT;
-      nrows = min(kST, uniform(p.rows.rows_of(e)) - row0);
-      if (tid < kST) slots[tid] = tid < nrows ? p.rows.slot(e, row0 + tid) : -1;
-      slot0 = uniform(p.rows.base_slot(e, row0));
+      nrows = min(kST, x.count - row0);
+      slot0 = x.slot + (blocks ? 0 : row0);
+      if (tid < kST)
+        slots[tid] = tid >= nrows ? -1 : blocks ? p.rows.slot(e, row0 + tid) : slot0 + tid;
       a0 = p.a + (int64_t)slot0 * p.a_row;
       b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kST * 2;
       k_a = p.k;
@@ -1057,9 +1070,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t row_tiles(const Rows& r, int max_rows, int tile) { return (int64_t)max_rows / tile + r.E; }
 
 // 256 by 256 tiles, `tiles` of them, `steps` of 128 bytes of the contraction: a step takes
-// 0.86 us on half a tile's rows, 1.3 on a whole tile's, 1.25 where all CUs stream weights.
+// 0.86 us on half a tile's rows, 1.3 on a whole tile's, 1.2 where all CUs stream weights.
 double wide_us(int64_t tiles, int64_t steps, double rows) {
-  if (tiles >= 200) return 4 + (double)ceil_div(tiles, 256) * ((double)steps * 1.25 + 6);
+  if (tiles >= 200) return 4 + (double)ceil_div(tiles, 256) * ((double)steps * 1.2 + 6);
   return 10 + (double)steps * (rows > 128 ? 1.3 : 0.86);
 }
 
@@ -1073,8 +1086,8 @@ int launch_few(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t 
 
 // Activations by a weight's rows.  Measured, few rows against wide tiles (us): one row by
 // 7168 x 7168 int8 11 : 53, 64 rows 20 : 64, 256 rows 63 : 80, 512 rows 118 : 82; 512 rows by
-// 512 x 7168 19 : 73; 32 experts of 4 rows each, bf16, both products of the block 414 : 472,
-// of 32 rows 526 : 477.
+// 512 x 7168 19 : 73; 32 experts of about 16 rows, bf16, 4096 x 7168 313 : 281 and 7168 x 2048
+// 168 : 218.
 template <class Epi, bool I8>
 int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E, wide = Epi::gate ? 128 : kBN;
@@ -1084,7 +1097,7 @@ int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const double few_tiles = E * std::max(1.0, rows <= few ? rows / few + 0.5 : rows / few + 0.25);
   const double bytes = few_tiles * cols * p.k;             // of weights, for each row tile again
   const double rounds = std::max(1.0, few_tiles * (cols / 32) / 512);
-  const double few_us = 4 + std::max(bytes / (few == 16 ? 7.0e6 : 6.5e6),
+  const double few_us = 4 + std::max(bytes / (few == 16 ? 7.0e6 : 6.2e6),
                                      rounds * ((double)ceil_div(steps, 4) * 0.35 + 1));
   const int64_t wide_tiles = E * std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5)) *
                              ceil_div(p.n, wide);
@@ -1123,7 +1136,7 @@ int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
 
 // Whether every workgroup rounds x to integers by itself.
 bool fuses(const Rows& r, int max_rows, int cols) {
-  return !r.count && max_rows <= 16 && (int64_t)max_rows * cols <= kFuseBytes;
+  return !r.count && max_rows <= 16 && (int64_t)max_rows * cols * 2 <= kFuseBytes;
 }
 
 // Rows of bf16 by an 8-bit weight: rounded by the product itself, or before it into

@@ -72,15 +72,41 @@ __device__ __forceinline__ void scan(T* v, int n) {
   }
 }
 
-// first[e] = row tiles of the experts before e, first[E] of all; by the whole workgroup.
-[[maybe_unused]] __device__ __forceinline__ void scan_tiles(const Rows& rows, int tile,
-                                                            int* first) {
-  for (int e = threadIdx.x; e < rows.E; e += blockDim.x)
-    first[e + 1] = (rows.rows_of(e) + tile - 1) / tile;
-  if (threadIdx.x == 0) first[0] = 0;
-  __syncthreads();
-  if (threadIdx.x < 64) scan(first, rows.E);
-  __syncthreads();
+// The expert whose row tiles hold tile i, by every wavefront for itself.  One round of loads
+// for up to 64 experts and no barrier: a table in LDS, and a search in it, made small
+// calls about 3 us longer.
+struct Found {
+  int e, first, tiles;       // the expert, the row tiles before its own, its own
+  int count, slot;           // its rows, the slot of its first
+};
+[[maybe_unused]] __device__ __forceinline__ bool find_rows(const Rows& rows, int tile, int i,
+                                                           Found& f) {
+  const int l = threadIdx.x & 63;
+  int before = 0;
+  for (int base = 0; base < rows.E; base += 64) {
+    const int e = base + l;
+    const int n = e < rows.E ? rows.rows_of(e) : 0;
+    const int slot = e < rows.E ? rows.base_slot(e, 0) : 0;
+    const int tiles = (n + tile - 1) / tile;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(sum, d);
+      if (l >= d) sum += o;
+    }
+    const uint64_t beyond = __ballot(before + sum > i);
+    if (beyond != 0) {
+      const int at = __builtin_ctzll(beyond);
+      f.e = base + at;
+      f.tiles = __builtin_amdgcn_readlane(tiles, at);
+      f.first = before + __builtin_amdgcn_readlane(sum, at) - f.tiles;
+      f.count = __builtin_amdgcn_readlane(n, at);
+      f.slot = __builtin_amdgcn_readlane(slot, at);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
 }
 
 // What a workgroup that walks over many tiles keeps of the experts: their rows and first
@@ -162,15 +188,17 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 struct RowScale {
   float scale, s, inv, up;
   bool finite, tiny;
-  __device__ __forceinline__ explicit RowScale(uint32_t top) {
+  static __device__ __forceinline__ RowScale of(uint32_t top) {
+    RowScale r;
     const float amax = __builtin_bit_cast(float, top << 16);
-    finite = top < 0x7F80u;
-    tiny = amax < 0x1p-100f && top != 0;
-    up = tiny ? 0x1p64f : 1.f;
-    scale = top == 0 ? 1.f : amax / 127.f;
-    s = scale * up;
-    inv = 1.f / s;
-    if (!finite) scale = __builtin_bit_cast(float, 0x7FC00000u);
+    r.finite = top < 0x7F80u;
+    r.tiny = amax < 0x1p-100f && top != 0;
+    r.up = r.tiny ? 0x1p64f : 1.f;
+    r.scale = top == 0 ? 1.f : amax / 127.f;
+    r.s = r.scale * r.up;
+    r.inv = 1.f / r.s;
+    if (!r.finite) r.scale = __builtin_bit_cast(float, 0x7FC00000u);
+    return r;
   }
   __device__ __forceinline__ u32x2 codes8(u32x4 raw) const {
     constexpr float kMagic = 12582912.f;
