@@ -10,6 +10,16 @@ raises -- there is no fallback of any kind.
     recv_x, recv_scales, recv_src_idx, recv_w = dispatch(x, topk_weights, lay, use_fp8)
     y = combine(expert_out, lay, topk_weights)
 
+Between dispatch and combine: ``expert_ffn`` is the gated feed-forward block of every
+expert on its rows, bf16 or 8-bit integer weights (``Int8Weight``), and
+``int8_linear`` one 8-bit product; for training ``expert_ffn_backward`` and
+``combine_backward`` are the gradients (dispatch's is combine with unit weights).
+
+    gate_up = recv_x.new_empty((len(recv_x), 2 * inter))
+    expert_out = expert_ffn(recv_x, w13, w2, layout=lay, gate_up=gate_up)
+    d_expert_out, d_weights = combine_backward(dy, expert_out, lay, topk_weights)
+    d_recv_x, dw13, dw2 = expert_ffn_backward(d_expert_out, recv_x, gate_up, w13, w2, layout=lay)
+
 Around them: ``route`` decides ``topk_idx`` and ``topk_weights`` from gate
 logits; ``moe_layer`` is the whole expert layer for a few tokens (up to 256),
 without dispatch and combine, on bf16 or 4-bit expert weights
@@ -878,10 +888,10 @@ def _rows(x, layout, lead, name):
     E = layout.num_experts
     if lead != (E,):
         raise ValueError(f"{name}: need the {E} experts of the layout, got {tuple(lead)}")
+    if cap < layout.capacity:
+        raise ValueError(f"x: need the {layout.capacity} rows of the layout, got {cap}")
     most = layout.num_tokens * layout.num_topk
     if isinstance(layout, LLLayout):
-        if cap < layout.capacity:
-            raise ValueError(f"x: need the {layout.capacity} rows of the layout, got {cap}")
         R = layout.num_ranks
         _arg(layout.recv_count, torch.int32, (E, R), "recv_count", x)
         return _ROWS(0, layout.recv_count.data_ptr(), cap, E, R, layout.max_tokens_per_rank, most)

@@ -1057,6 +1057,7 @@ int launch(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
   // one workgroup per CU at most: each takes more than half of a CU's LDS
   // (twice the tiles: they may be taken by halves)
   const int grid = (int)(tiles < 128 ? 2 * tiles : 256);
+  EP_LOG("  wide tiles: up to %lld", (long long)tiles);
   product_kernel<KIND, Epi, I8><<<dim3(grid), dim3(512), 0, st>>>(p, epi);
   return check_launch("ep_ffn product");
 }
@@ -1080,6 +1081,8 @@ template <class Epi, bool I8, int TT, bool FUSE>
 int launch_few(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t st) {
   const int64_t tiles = row_tiles * ceil_div(p.n, Epi::gate ? 16 : 32);
   const int grid = (int)(tiles < 512 ? tiles : 512);       // two workgroups per CU
+  EP_LOG("  few rows: %d rows a tile%s, %lld tiles", 16 * TT, FUSE ? " of bf16" : "",
+         (long long)tiles);
   few_kernel<Epi, I8, TT, FUSE><<<dim3(grid), dim3(256), 0, st>>>(p, epi);
   return check_launch("ep_ffn few rows");
 }
@@ -1126,6 +1129,7 @@ int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   if (small_us < wide_us(tiles(kBM), steps, KIND == kOuter ? kBM : rows)) {
     const int64_t n = KIND == kOuter ? tiles(kST)
                                      : row_tiles(p.rows, max_rows, kST) * ceil_div(p.n, kST);
+    EP_LOG("  small tiles: up to %lld", (long long)n);
     small_kernel<KIND, Epi><<<dim3((int)(n < 256 ? n : 256)), dim3(256), 0, st>>>(p, epi);
     return check_launch("ep_ffn small product");
   }
@@ -1202,6 +1206,11 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
       !aligned(a->workspace, 256))
     return EP_ERR_INVALID_ARG;
   const int bytes = i8 ? 1 : 2;
+  const int64_t cap = rows->capacity;
+  if (overlap(a->gate_up, cap * 4 * I, a->x, cap * 2 * H) ||
+      overlap(a->gate_up, cap * 4 * I, a->y, cap * 2 * H) || !aligned(a->w13.scales, i8 ? 4 : 1) ||
+      !aligned(a->w2.scales, i8 ? 4 : 1))
+    return EP_ERR_INVALID_ARG;
   const Rows r = device_rows(rows);
   if (!fits_region(r, (int64_t)H * 2) || !fits_region(r, (int64_t)I * 2) ||
       !few_enough(r, std::max(H, 2 * I)))
@@ -1209,7 +1218,6 @@ int ep_ffn(const ep_rows_t* rows, const ep_ffn_args_t* a, void* stream) {
   rc = check_device();
   if (rc != EP_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
-  const int64_t cap = rows->capacity;
   uint8_t* ws = (uint8_t*)a->workspace;
   uint8_t* h = ws;
   uint8_t* xq = h + up(cap * 2 * I);
@@ -1246,6 +1254,13 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   const int H = a->hidden, I = a->inter;
   const Rows r = device_rows(rows);
   if (r.count && !r.offset) return EP_ERR_INVALID_ARG;   // low-latency sub-blocks
+  const int64_t cap = rows->capacity, w13_bytes = (int64_t)r.E * 4 * I * H;
+  const struct { const void* p; int64_t n; } in[] = {{a->dy, cap * 2 * H}, {a->x, cap * 2 * H},
+      {a->gate_up, cap * 4 * I}, {a->w13, w13_bytes}, {a->w2, w13_bytes / 2}},
+      out[] = {{a->dx, cap * 2 * H}, {a->dw13, w13_bytes}, {a->dw2, w13_bytes / 2}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (overlap(o.p, o.n, i.p, i.n)) return EP_ERR_INVALID_ARG;
   if (!few_enough(r, std::max(H, 2 * I)) ||
       r.E * ceil_div(std::max(H, 2 * I), kST) * ceil_div(std::max(H, I), kST) > INT32_MAX)
     return EP_ERR_INVALID_ARG;
@@ -1319,7 +1334,9 @@ int ep_integer_linear(const ep_rows_t* rows, const ep_integer_args_t* a, void* s
   if (rows->max_rows == 0) return EP_OK;
   const int C = a->cols, O = a->out_rows;
   if (!a->x || !a->y || !a->w.data || !a->w.scales || !aligned16(a->x) || !aligned16(a->y) ||
-      !aligned16(a->w.data) || !aligned(a->workspace, 256) || (!a->x_scales && !a->workspace))
+      !aligned16(a->w.data) || !aligned(a->workspace, 256) || (!a->x_scales && !a->workspace) ||
+      !aligned(a->w.scales, 4) || !aligned(a->x_scales, 4) ||
+      overlap(a->y, rows->capacity * 2 * O, a->x, rows->capacity * C * (a->x_scales ? 1 : 2)))
     return EP_ERR_INVALID_ARG;
   const Rows r = device_rows(rows);
   if (!fits_region(r, C)) return EP_ERR_INVALID_ARG;

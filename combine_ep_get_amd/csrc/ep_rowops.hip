@@ -6,14 +6,16 @@
 namespace {
 
 // ---------------------------------------------------------------- 8-bit integers
-constexpr int kHeld = 16;      // 16-byte chunks per lane that stay in registers: 8192 columns
-
-// A wavefront per row; blocks (segment, part): segments are the experts, or the sub-blocks
-// of ep_ll_dispatch, whose rows are shared out over the parts.
-template <int CH>
+// A row by WAVES wavefronts, which hold up to CH 16-byte chunks per lane in registers (of a
+// longer row the rest is read twice); blocks (segment, part): segments are the experts, or the
+// sub-blocks of ep_ll_dispatch, whose rows are shared out over the parts.  4096 rows of
+// 7168: 18 us, one wavefront per row 24.
+template <int WAVES, int CH>
 __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t* x, int cols,
                                                        uint8_t* codes, float* scales) {
-  const int seg = blockIdx.x, l = threadIdx.x & 63;
+  __shared__ uint32_t tops[2][4];
+  constexpr int kRows = 4 / WAVES, kLanes = 64 * WAVES;
+  const int seg = blockIdx.x, l = threadIdx.x % kLanes;
   int first, n;
   if (rows.count && !rows.offset) {
     first = seg * rows.M;
@@ -23,24 +25,33 @@ __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t*
     n = rows.rows_of(seg);
   }
   const int chunks = cols / 8;
-  for (int64_t j = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); j < n; j += gridDim.y * 4) {
+  int turn = 0;                          // rows alternate between two sets of maxima
+  for (int64_t j = (int64_t)blockIdx.y * kRows + threadIdx.x / kLanes; j < n;
+       j += gridDim.y * kRows) {
     const int64_t slot = first + j;
     const u32x4* in = (const u32x4*)(x + slot * cols * 2);
     u32x2* out = (u32x2*)(codes + slot * cols);
     u32x4 held[CH];
 #pragma unroll
     for (int i = 0; i < CH; i++)
-      held[i] = i * 64 + l < chunks ? in[i * 64 + l] : u32x4{0, 0, 0, 0};
+      held[i] = i * kLanes + l < chunks ? in[i * kLanes + l] : u32x4{0, 0, 0, 0};
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < CH; i++) top = max(top, largest8(held[i]));
-    for (int c = CH * 64 + l; c < chunks; c += 64) top = max(top, largest8(in[c]));
-    const RowScale s = RowScale::of(wave_max(top));
+    for (int c = CH * kLanes + l; c < chunks; c += kLanes) top = max(top, largest8(in[c]));
+    top = wave_max(top);
+    if constexpr (WAVES == 4) {          // the whole workgroup has the same rows
+      if ((l & 63) == 0) tops[turn][l >> 6] = top;
+      __syncthreads();
+      top = max(max(tops[turn][0], tops[turn][1]), max(tops[turn][2], tops[turn][3]));
+      turn ^= 1;
+    }
+    const RowScale s = RowScale::of(top);
     if (l == 0) scales[slot] = s.scale;
 #pragma unroll
     for (int i = 0; i < CH; i++)
-      if (i * 64 + l < chunks) out[i * 64 + l] = s.codes8(held[i]);
-    for (int c = CH * 64 + l; c < chunks; c += 64) out[c] = s.codes8(in[c]);
+      if (i * kLanes + l < chunks) out[i * kLanes + l] = s.codes8(held[i]);
+    for (int c = CH * kLanes + l; c < chunks; c += kLanes) out[c] = s.codes8(in[c]);
   }
 }
 
@@ -110,18 +121,19 @@ namespace ep {
 int quantize_rows(const Rows& rows, int max_rows, const void* x, int cols, void* codes,
                   float* scales, hipStream_t st) {
   const int segments = rows.count && !rows.offset ? rows.E * rows.R : rows.E;
-  // four rows per workgroup and pass, at most about 16 workgroups per CU; at least twice
-  // the average segment, so that an uneven one takes few passes
+  // at most about 16 workgroups per CU; at least twice the average segment, so that an
+  // uneven one takes few passes
+  const int rows_per = cols <= 2048 ? 4 : 1;
   const int64_t per = ((int64_t)max_rows / segments + 1) * 2;
-  int64_t parts = (per + 3) / 4;
+  int64_t parts = (per + rows_per - 1) / rows_per;
   const int64_t most = segments >= 4096 ? 1 : 4096 / segments;
   if (parts > most) parts = most;
   const dim3 grid(segments, (int)parts);
   const uint8_t* in = (const uint8_t*)x;
   if (cols <= 2048)
-    quantize_kernel<4><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
+    quantize_kernel<1, 4><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
   else
-    quantize_kernel<kHeld><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
+    quantize_kernel<4, 4><<<grid, 256, 0, st>>>(rows, in, cols, (uint8_t*)codes, scales);
   return check_launch("quantize_rows");
 }
 
@@ -134,7 +146,8 @@ int ep_quantize_rows(int64_t num_rows, int32_t cols, const void* x, int8_t* code
   if (num_rows < 0 || num_rows > INT32_MAX || !valid_width(cols, EP_WEIGHT_INT8))
     return EP_ERR_INVALID_ARG;
   if (num_rows == 0) return EP_OK;
-  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned(scales, 4))
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned(scales, 4) ||
+      overlap(codes, num_rows * cols, x, num_rows * cols * 2))
     return EP_ERR_INVALID_ARG;
   int rc = check_device();
   if (rc != EP_OK) return rc;
@@ -155,6 +168,10 @@ int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* exper
   if (!dy || !slot_of || !topk_weights || !d_topk_weights ||
       (recv_capacity > 0 && (!expert_out || !d_expert_out)) || !aligned16(dy) ||
       !aligned16(expert_out) || !aligned16(d_expert_out))
+    return EP_ERR_INVALID_ARG;
+  const int64_t rows = recv_capacity * 2 * H, own = (int64_t)N * 2 * H;
+  if (overlap(d_expert_out, rows, dy, own) ||
+      (d_expert_out != expert_out && overlap(d_expert_out, rows, expert_out, rows)))
     return EP_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != EP_OK) return rc;

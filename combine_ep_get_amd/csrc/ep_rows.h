@@ -242,6 +242,12 @@ struct RowScale {
 [[maybe_unused]] bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 [[maybe_unused]] bool aligned16(const void* p) { return aligned(p, 16); }
 
+// Whether n bytes at p and m bytes at q share any (NULL: none).
+[[maybe_unused]] bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
+}
+
 [[maybe_unused]] int validate_rows(const ep_rows_t* r) {
   if (!r || r->capacity < 0 || r->capacity > INT32_MAX || r->max_rows < 0 || r->num_experts < 1 ||
       r->num_experts > EP_MAX_EXPERTS || r->num_sources < 1 || r->num_sources > EP_MAX_RANKS)
@@ -254,7 +260,7 @@ struct RowScale {
     return EP_ERR_INVALID_ARG;
   }
   if (!r->count && (r->num_experts != 1 || r->max_rows > r->capacity)) return EP_ERR_INVALID_ARG;
-  if (((uintptr_t)r->offset | (uintptr_t)r->count) & 3) return EP_ERR_INVALID_ARG;
+  if (!aligned(r->offset, 4) || !aligned(r->count, 4)) return EP_ERR_INVALID_ARG;
   return EP_OK;
 }
 

@@ -478,9 +478,9 @@ enum { EP_WEIGHT_INT8 = 3 };
  *   w13        [E][2*inter][hidden]: rows 0..inter-1 are Wg, the rest Wu; bf16 or
  *              EP_WEIGHT_INT8
  *   w2         [E][hidden][inter], in the same format
- *   y          [capacity][hidden] bf16 out; must not overlap x
+ *   y          [capacity][hidden] bf16 out; may be x
  *   gate_up    [capacity][2*inter] bf16 out, g and u (rounded) for
- *              ep_ffn_backward, or NULL
+ *              ep_ffn_backward, or NULL; must not overlap x or y
  *   workspace  ep_ffn_workspace_bytes (backward = 0); 256-byte aligned; no
  *              initialisation; calls that overlap need their own
  *   hidden, inter  % 8 == 0 (bf16) or % 16 == 0 (int8), at most EP_MAX_CONTRACTION
@@ -534,7 +534,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* args, void*
  * keep what they held.  Deterministic.  (Dispatch's own gradient is ep_combine of
  * the rows' gradients with unit weights.)
  *   dy            [N][H] bf16;  expert_out [recv_capacity][H] bf16
- *   d_expert_out  [recv_capacity][H] bf16 out; may be expert_out
+ *   d_expert_out  [recv_capacity][H] bf16 out; may be expert_out, apart otherwise
  *   d_topk_weights [N][K] float32 out
  * hidden, num_tokens, num_topk as for ep_combine; use_fp8 and cu_budget are only
  * checked. */
