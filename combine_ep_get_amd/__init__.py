@@ -609,7 +609,7 @@ def _call(fn, name, t, *args):
     """fn(*args, stream) on t's device and its current stream there."""
     import torch
     dev = t.get_device()
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -621,8 +621,9 @@ def _call(fn, name, t, *args):
 def _arg(t, dtype, shape, name, ref):
     """_need for arguments of small calls: the same check, the message made only
     on failure; on ref's device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous() \
-            or t.get_device() != ref.get_device():
+    dev = ref.get_device()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 \
+            or not t.is_contiguous():
         _need(t, dtype, shape, name)
         raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
 
@@ -876,29 +877,28 @@ class Int8Weight:
         return self.desc
 
 
-def _rows(x, layout, lead, name):
-    """ep_rows_t of x's rows as bytes: of a Layout, an LLLayout, or (None) a plain matrix.
-    ``lead`` is the weight's leading shape: (E,), or () for a plain matrix."""
+def _rows(x, layout):
+    """ep_rows_t of x's rows as bytes: of a Layout, an LLLayout, or (None) a plain matrix."""
     import torch
     cap = x.shape[0]
     if layout is None:
-        if lead != ():
-            raise ValueError(f"{name}: without a layout it has no expert axis")
         return _ROWS(0, 0, cap, 1, 1, 0, cap)
-    E = layout.num_experts
-    if lead != (E,):
-        raise ValueError(f"{name}: need the {E} experts of the layout, got {tuple(lead)}")
     if cap < layout.capacity:
         raise ValueError(f"x: need the {layout.capacity} rows of the layout, got {cap}")
-    most = layout.num_tokens * layout.num_topk
+    E, most = layout.num_experts, layout.num_tokens * layout.num_topk
     if isinstance(layout, LLLayout):
-        R = layout.num_ranks
-        _arg(layout.recv_count, torch.int32, (E, R), "recv_count", x)
-        return _ROWS(0, layout.recv_count.data_ptr(), cap, E, R, layout.max_tokens_per_rank, most)
-    _arg(layout.expert_slot_offset, torch.int32, (E + 1,), "expert_slot_offset", x)
-    _arg(layout.num_recv_per_expert, torch.int32, (E,), "num_recv_per_expert", x)
-    return _ROWS(layout.expert_slot_offset.data_ptr(), layout.num_recv_per_expert.data_ptr(), cap,
-                 E, 1, 0, most)
+        R, count = layout.num_ranks, layout.recv_count
+        _arg(count, torch.int32, (E, R), "recv_count", x)
+        return _ROWS(0, count.data_ptr(), cap, E, R, layout.max_tokens_per_rank, most)
+    offset, count = layout.expert_slot_offset, layout.num_recv_per_expert
+    _arg(offset, torch.int32, (E + 1,), "expert_slot_offset", x)
+    _arg(count, torch.int32, (E,), "num_recv_per_expert", x)
+    return _ROWS(offset.data_ptr(), count.data_ptr(), cap, E, 1, 0, most)
+
+
+def _of_experts(layout, *shape):
+    """The shape of a weight: a stack with a layout, a matrix without."""
+    return shape if layout is None else (layout.num_experts, *shape)
 
 
 def _workspace(workspace, need, ref):
@@ -938,17 +938,20 @@ def alloc_ffn_workspace(rows, hidden, inter, int8=False, backward=False, device=
 
 
 def _ffn_weight(w, name, shape, ref):
-    """(leading shape, descriptor) of one of the block's weights [*lead, *shape]."""
+    """The descriptor of one of the block's weights."""
     import torch
-    lead, got = tuple(w.shape[:-2]), tuple(w.shape[-2:])
-    if got != shape:
-        raise ValueError(f"{name}: need [..., {shape[0]}, {shape[1]}], got {tuple(w.shape)}")
     if isinstance(w, Int8Weight):
-        if w.get_device() != ref.get_device():
-            raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
-        return lead, w.checked_desc()
-    _arg(w, torch.bfloat16, w.shape, name, ref)
-    return lead, (w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0)
+        return _int8_weight(w, name, shape, ref)
+    _arg(w, torch.bfloat16, shape, name, ref)
+    return w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0
+
+
+def _int8_weight(w, name, shape, ref):
+    if w.shape != shape:
+        raise ValueError(f"{name}: need {shape}, got {w.shape}")
+    if w.get_device() != ref.get_device():
+        raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
+    return w.checked_desc()
 
 
 def expert_ffn(x, w13, w2, layout=None, out=None, gate_up=None, workspace=None):
@@ -966,11 +969,9 @@ def expert_ffn(x, w13, w2, layout=None, out=None, gate_up=None, workspace=None):
     if int8 != isinstance(w2, Int8Weight):
         raise ValueError("w13 and w2: need the same kind of weight")
     _arg(x, torch.bfloat16, (cap, H), "x", x)
-    lead, d13 = _ffn_weight(w13, "w13", (2 * I, H), x)
-    lead2, d2 = _ffn_weight(w2, "w2", (H, I), x)
-    if lead2 != lead:
-        raise ValueError(f"w2: need {lead} experts, got {lead2}")
-    rows = _rows(x, layout, lead, "w13")
+    d13 = _ffn_weight(w13, "w13", _of_experts(layout, 2 * I, H), x)
+    d2 = _ffn_weight(w2, "w2", _of_experts(layout, H, I), x)
+    rows = _rows(x, layout)
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -998,14 +999,11 @@ def expert_ffn_backward(dy, x, gate_up, w13, w2, layout=None, out=None, workspac
     _arg(x, torch.bfloat16, (cap, H), "x", x)
     _arg(dy, torch.bfloat16, (cap, H), "dy", x)
     _arg(gate_up, torch.bfloat16, (cap, 2 * I), "gate_up", x)
-    for w, name in ((w13, "w13"), (w2, "w2")):
-        if isinstance(w, Int8Weight):
-            raise ValueError(f"{name}: need a bf16 tensor")
-    lead, _ = _ffn_weight(w13, "w13", (2 * I, H), x)
-    lead2, _ = _ffn_weight(w2, "w2", (H, I), x)
-    if lead2 != lead:
-        raise ValueError(f"w2: need {lead} experts, got {lead2}")
-    rows = _rows(x, layout, lead, "w13")
+    if isinstance(w13, Int8Weight) or isinstance(w2, Int8Weight):
+        raise ValueError("w13 and w2: need bf16 tensors")
+    _arg(w13, torch.bfloat16, _of_experts(layout, 2 * I, H), "w13", x)
+    _arg(w2, torch.bfloat16, _of_experts(layout, H, I), "w2", x)
+    rows = _rows(x, layout)
     if out is None:
         out = torch.empty_like(x), torch.empty_like(w13), torch.empty_like(w2)
     dx, dw13, dw2 = out
@@ -1078,11 +1076,8 @@ def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
         raise ValueError("w: need an Int8Weight")
     cap, C = x.shape
     O = w.shape[-2]
-    if w.shape[-1] != C:
-        raise ValueError(f"w: need [..., {C}], got {w.shape}")
-    if w.get_device() != x.get_device():
-        raise ValueError(f"w is on {w.device}, expected {x.device}")
-    rows = _rows(x, layout, w.shape[:-2], "w")
+    desc = _int8_weight(w, "w", _of_experts(layout, O, C), x)
+    rows = _rows(x, layout)
     if x_scales is None:
         _arg(x, torch.bfloat16, (cap, C), "x", x)
         workspace = _workspace(workspace, _int8_bytes(cap, C), x)
@@ -1096,7 +1091,7 @@ def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
         _arg(out, torch.bfloat16, (cap, O), "y", x)
     _call(lib().ep_integer_linear, "ep_integer_linear", x, rows,
           _INT8_ARGS(x.data_ptr(), 0 if x_scales is None else x_scales.data_ptr(),
-                     *w.checked_desc(), out.data_ptr(),
+                     *desc, out.data_ptr(),
                      0 if workspace is None else workspace.data_ptr(), C, O))
     return out
 

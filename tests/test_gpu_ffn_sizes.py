@@ -142,3 +142,31 @@ def test_larger_buffers_and_workspaces():
     with pytest.raises(ValueError):                      # rows of 60: no whole 16 bytes
         ep.expert_ffn(x[:, :60].contiguous(), w13[:, :, :60].contiguous(),
                       w2[:, :60].contiguous(), layout=lay)
+
+
+def test_most_experts_on_wide_tiles():
+    """1024 experts with about 128 rows each, none in some."""
+    g = gen(30)
+    E, N, H, I = 1024, 131072, 256, 64
+    idx = torch.randint(0, E, (N, 1), generator=g, device="cuda").to(torch.int32)
+    idx[idx % 101 == 7] = -1
+    lay = ep.get_layout(idx, E, 1, 1)
+    where = ref.slots_of(lay, lay.capacity)
+    at = torch.cat([s for _, s in where]).cuda()
+    x, dy, gu = (torch.zeros((lay.capacity, n), dtype=BF, device="cuda") for n in (H, H, 2 * I))
+    for t in (x, dy, gu):
+        t[at] = normal(g, len(at), t.shape[1])
+    w13, w2 = normal(g, E, 2 * I, H, scale=H ** -0.5), normal(g, E, H, I, scale=I ** -0.5)
+    y = ep.expert_ffn(x, w13, w2, layout=lay)
+    dx, dw13, dw2 = ep.expert_ffn_backward(dy, x, gu, w13, w2, layout=lay)
+    for e, s in where[::53] + where[7::101] + where[-1:]:
+        s = s.cuda()
+        if len(s) == 0:
+            assert not bool(dw13[e].any()) and not bool(dw2[e].any())
+            continue
+        a = [t.double() for t in (x[s], w13[e], w2[e])]
+        want, bound, _, _ = ref.ffn(*a)
+        ref.check(y[s], want, bound, f"y of expert {e}")
+        want = ref.ffn_grad(dy[s].double(), a[0], gu[s].double(), a[1], a[2])
+        for got, (v, b), what in zip((dx[s], dw13[e], dw2[e]), want, ("dx", "dw13", "dw2")):
+            ref.check(got, v, b, f"{what} of expert {e}")
