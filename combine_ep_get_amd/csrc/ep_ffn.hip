@@ -103,9 +103,28 @@ __device__ __forceinline__ i32x4 descriptor(const uint8_t* p) {
   return d;
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+// With the hardware's reciprocal, one ulp off: a whole quotient would be most of a gate's
+// epilogue (ten instructions for each of its 32768 values).
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-g));
+}
+
+// Waits for loads into v here, whatever is done with it later: a wait that the compiler
+// leaves to a path behind a branch comes back in the main loop as a wait for everything.
+__device__ __forceinline__ void arrive(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void arrive(f32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void arrive(u32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---------------------------------------------------------------- epilogues
+// Four values from p[c] on, of n (those behind the last are the last again).
+__device__ __forceinline__ f32x4 load4(const float* p, int c, int n) {
+  if ((n & 3) == 0) return *(const f32x4*)(p + min(c, n - 4));
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r[j] = p[min(c + j, n - 1)];
+  return r;
+}
+
 // What becomes of eight neighbouring columns of a row of D; put: of eight that are rounded
 // to bf16 already (bf16 products, where that comes first, with n % 8 == 0).  `slot` is the row's slot
 // (kOuter: its row of the expert's matrix), `e` the expert, `c` the first column.
@@ -121,31 +140,34 @@ struct StoreRows {
   static constexpr bool rounds = true;
   __device__ __forceinline__ void put(int, int slot, int c, u32x4 r, int more) const {
     c += more;
-    if (c < n) *(u32x4*)(y + (int64_t)slot * n + c) = r;
-  }
-  template <class T>
-  __device__ __forceinline__ void operator()(int e, int slot, int c, const T* v, const T*) const {
     if (c >= n) return;
-    float f[8];
-    const int left = n - c;
-    if constexpr (std::is_same_v<T, int>) {
-      const float s = sx[slot];
-      const float* w = sw + (int64_t)e * n + c;
-#pragma unroll
-      for (int i = 0; i < 8; i++) f[i] = (float)v[i] * s * w[min(i, left - 1)];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; i++) f[i] = v[i];
-    }
-    const u32x4 r = pack8(f);
     uint16_t* to = y + (int64_t)slot * n + c;
     if ((n & 7) == 0) {
       *(u32x4*)to = r;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++)
-        if (i < left) to[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+        if (c + i < n) to[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
     }
+  }
+  // scales of four columns (whatever behind the last one)
+  __device__ __forceinline__ f32x4 scales(int e, int c, int half) const {
+    return load4(sw + (int64_t)e * n, c + half * 128, n);
+  }
+  template <class T>
+  __device__ __forceinline__ void operator()(int e, int slot, int c, const T* v, const T*) const {
+    if (c >= n) return;
+    float f[8];
+    if constexpr (std::is_same_v<T, int>) {
+      const float s = sx[slot];
+      const f32x4 w[2] = {scales(e, c, 0), scales(e, c + 4, 0)};
+#pragma unroll
+      for (int i = 0; i < 8; i++) f[i] = (float)v[i] * s * w[i >> 2][i & 3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) f[i] = v[i];
+    }
+    put(e, slot, c, pack8(f), 0);
   }
 };
 
@@ -181,6 +203,9 @@ struct StoreGate {
     if (c >= inter) return;
     if (what == 0) *(u32x4*)(h + (int64_t)slot * inter + c) = r;
     else *(u32x4*)(gu + (int64_t)slot * 2 * inter + (what - 1) * inter + c) = r;
+  }
+  __device__ __forceinline__ f32x4 scales(int e, int c, int half) const {
+    return load4(sw + ((int64_t)e * 2 + half) * inter, c, inter);
   }
   template <class T>
   __device__ __forceinline__ void operator()(int e, int slot, int c, const T* g, const T* u) const {
@@ -222,13 +247,20 @@ struct StoreGateGrad {
   uint16_t* dgu;           // [slot][2 inter]
   uint16_t* h;             // [slot][inter]
   int inter;
-  __device__ __forceinline__ void operator()(int, int slot, int c, const float* v,
-                                             const float*) const {
+  struct Ahead {           // what it reads, asked for before v is there
+    u32x4 g, u;
+  };
+  __device__ __forceinline__ Ahead ahead(int slot, int c) const {
+    const int64_t at = (int64_t)slot * 2 * inter + min(c, inter - 8);
+    return Ahead{*(const u32x4*)(gu + at), *(const u32x4*)(gu + at + inter)};
+  }
+  __device__ __forceinline__ void operator()(const Ahead& x, int slot, int c,
+                                             const float* v) const {
     if (c >= inter) return;
     const int64_t at = (int64_t)slot * 2 * inter + c;
     float g[8], u[8], dg[8], du[8], hh[8];
-    unpack8(*(const u32x4*)(gu + at), g);
-    unpack8(*(const u32x4*)(gu + at + inter), u);
+    unpack8(x.g, g);
+    unpack8(x.u, u);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float s = sigmoid(g[i]), silu = g[i] * s;
@@ -239,6 +271,10 @@ struct StoreGateGrad {
     *(u32x4*)(dgu + at) = pack8(dg);
     *(u32x4*)(dgu + at + inter) = pack8(du);
     *(u32x4*)(h + (int64_t)slot * inter + c) = pack8(hh);
+  }
+  __device__ __forceinline__ void operator()(int, int slot, int c, const float* v,
+                                             const float*) const {
+    (*this)(ahead(slot, c), slot, c, v);
   }
 };
 
@@ -600,14 +636,48 @@ void product_kernel(Product p, Epi epi) {
                             : cur.slot0 + r;
     };
     const int c0 = cur.nt * (Epi::gate ? 128 : kBN) + wn * 32 + (v & 3) * 8;
+    // all scales of 8-bit products at once: loaded where each block needs them, one latency
+    // after the other made a tile's epilogue 22 us long instead of 8
+    float row_scale[4];
+    f32x4 scales[2][4];
+    if constexpr (I8) {
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+      for (int i = 0; i < 4; i++) {
+        const int r = (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + (v & 31);
+        row_scale[i] = r < cur.nrows ? epi.sx[row_at(r)] : 0.f;
+      }
 #pragma unroll
-      for (int mb = 0; mb < 2; mb++) {
-        const int r0 = h * 128 + wm * 64 + mb * 32;
-        if (r0 >= cur.nrows) continue;
-        if constexpr (Epi::rounds && !I8) {
+      for (int half = 0; half < 2; half++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          scales[half][i] = epi.scales(cur.e, cur.nt * (Epi::gate ? 128 : kBN) + wn * 32 +
+                                                  8 * i + 4 * (v >> 5), half);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        arrive(row_scale[i]);
+        arrive(scales[0][i]);
+        arrive(scales[1][i]);
+      }
+    }
+    if constexpr (Epi::rounds) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int mb = 0; mb < 2; mb++) {
+          const int r0 = h * 128 + wm * 64 + mb * 32;
+          if (r0 >= cur.nrows) continue;
           // `what` is turned and stored by epi.put (a gate: h, and g and u where asked for)
+          auto values = [&](int half) {
+            f32x16 x;
+            if constexpr (I8) {
+#pragma unroll
+              for (int j = 0; j < 16; j++)
+                x[j] = (float)acc[h][half][mb][j] * row_scale[h * 2 + mb] * scales[half][j >> 2][j & 3];
+            } else {
+              x = acc[h][half][mb];
+            }
+            return x;
+          };
           auto put = [&](const f32x16& x, int what) {
             turn16(x);
             const u32x4 q[2] = {take16(0), take16(1)};
@@ -617,42 +687,54 @@ void product_kernel(Product p, Epi epi) {
               if (r < cur.nrows) epi.put(cur.e, row_at(r), c0, q[it], what);
             }
           };
+          const f32x16 a = values(0), b = values(1);
           if constexpr (Epi::gate) {
             f32x16 x;
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const float g = acc[h][0][mb][j];
-              x[j] = g * sigmoid(g) * acc[h][1][mb][j];
-            }
+            for (int j = 0; j < 16; j++) x[j] = a[j] * sigmoid(a[j]) * b[j];
             put(x, 0);
             if (epi.gu) {
-              put(acc[h][0][mb], 1);
-              put(acc[h][1][mb], 2);
+              put(a, 1);
+              put(b, 2);
             }
           } else {
-            put(acc[h][0][mb], 0);
-            put(acc[h][1][mb], 128);
-          }
-        } else {
-#pragma unroll
-          for (int qn = 0; qn < (Epi::gate ? 1 : 2); qn++) {
-            val_t x[2][8], u[2][8];
-            turn(acc[h][qn][mb]);
-            take(0, x[0]);
-            take(1, x[1]);
-            if constexpr (Epi::gate) {
-              turn(acc[h][1][mb]);
-              take(0, u[0]);
-              take(1, u[1]);
-            }
-#pragma unroll
-            for (int it = 0; it < 2; it++) {
-              const int r = r0 + it * 16 + (v >> 2);
-              if (r < cur.nrows) epi(cur.e, row_at(r), c0 + qn * 128, x[it], u[it]);
-            }
+            put(a, 0);
+            put(b, 128);
           }
         }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; b++) {
+        const int r0 = (b >> 1) * 128 + wm * 64 + (b & 1) * 32;
+        if (r0 >= cur.nrows) continue;
+        // a block's operands together, one latency instead of four (rows behind the last:
+        // the last again)
+        typename Epi::Ahead ahead[4];
+        int row[2];
+#pragma unroll
+        for (int it = 0; it < 2; it++) {
+          row[it] = row_at(min(r0 + it * 16 + (v >> 2), cur.nrows - 1));
+          ahead[it] = epi.ahead(row[it], c0);
+          ahead[2 + it] = epi.ahead(row[it], c0 + 128);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          arrive(ahead[i].g);
+          arrive(ahead[i].u);
+        }
+#pragma unroll
+        for (int qn = 0; qn < 2; qn++) {
+          val_t x[2][8];
+          turn(acc[b >> 1][qn][b & 1]);
+          take(0, x[0]);
+          take(1, x[1]);
+#pragma unroll
+          for (int it = 0; it < 2; it++)
+            if (r0 + it * 16 + (v >> 2) < cur.nrows)
+              epi(ahead[qn * 2 + it], row[it], c0 + qn * 128, x[it]);
+        }
       }
+    }
     tile += G;
     if (tile >= total) break;
     // whole tiles store the same number of times, and so do the ones behind this here
