@@ -750,6 +750,8 @@ def _weight_desc(w, shape, name, ref):
         if w.get_device() != ref.get_device():
             raise ValueError(f"{name} is on {w.device}, expected {ref.device}")
         return w.checked_desc()
+    if isinstance(w, Int8Weight):
+        raise ValueError(f"{name}: need a bf16 tensor or a QuantWeight")
     _arg(w, torch.bfloat16, shape, name, ref)
     return w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0
 
@@ -942,6 +944,8 @@ def _ffn_weight(w, name, shape, ref):
     import torch
     if isinstance(w, Int8Weight):
         return _int8_weight(w, name, shape, ref)
+    if isinstance(w, QuantWeight):
+        raise ValueError(f"{name}: need a bf16 tensor or an Int8Weight")
     _arg(w, torch.bfloat16, shape, name, ref)
     return w.data_ptr(), 0, 0, EP_WEIGHT_BF16, 0
 
@@ -999,8 +1003,9 @@ def expert_ffn_backward(dy, x, gate_up, w13, w2, layout=None, out=None, workspac
     _arg(x, torch.bfloat16, (cap, H), "x", x)
     _arg(dy, torch.bfloat16, (cap, H), "dy", x)
     _arg(gate_up, torch.bfloat16, (cap, 2 * I), "gate_up", x)
-    if isinstance(w13, Int8Weight) or isinstance(w2, Int8Weight):
-        raise ValueError("w13 and w2: need bf16 tensors")
+    for w in (w13, w2):
+        if isinstance(w, (Int8Weight, QuantWeight)):
+            raise ValueError("w13 and w2: need bf16 tensors")
     _arg(w13, torch.bfloat16, _of_experts(layout, 2 * I, H), "w13", x)
     _arg(w2, torch.bfloat16, _of_experts(layout, H, I), "w2", x)
     rows = _rows(x, layout)

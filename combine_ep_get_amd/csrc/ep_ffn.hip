@@ -1,5 +1,29 @@
 // ep_ffn.hip -- the experts' feed-forward block on dispatched rows, its gradient, and
 // products in 8-bit integers (include/ep_get.h states the contracts).
+//
+// All of it is D = A B^T over a contraction, for the rows of every expert in one launch
+// (the counts are on the device, so each workgroup finds its tiles itself):
+//   block      h = silu(x Wg^T) * (x Wu^T), y = h W2^T      activations by a weight's rows
+//   gradient   dh = dy W2 (dg, du and h in its epilogue), dx = [dg du] W13
+//                                                           ... by its columns
+//              dW13 = [dg du]^T x, dW2 = dy^T h             k runs over an expert's rows
+//   integers   the same first form on bytes, the sums exact in 32 bits
+// gate and up meet in one tile (128 columns of each), so that h leaves the kernel and 2 *
+// inter values per row never do, unless a gradient will ask for them.
+//
+// Three kernels, chosen by run_rows and run_grad:
+//   product_kernel  256 by 256 tiles, 8 wavefronts, one workgroup per CU that walks over
+//                   tiles.  A tile's step (128 bytes of the contraction) is 2048 cycles of
+//                   MFMA on each SIMD and 64 KiB of operands, which go straight to LDS two
+//                   steps deep and are read with no bank conflict.  Bound by the MFMAs and,
+//                   with them, by the card's power: at 8192 rows by 8192 x 4096 in bf16
+//                   1310 TFLOP/s (a large library product: 1260 to 1550 here) and 2050
+//                   TOP/s at 8192^3 int8 (2060 to 2120), at 1.75 GHz with the MFMAs busy 78 %
+//                   of the cycles; without any load they are 82 %, the rest is barriers.
+//                   With few rows per expert it is bound by HBM: 6.8 TB/s of weights.
+//   few_kernel      few rows: weights as a stream, the contraction split over wavefronts
+//   small_kernel    gradients of few rows and small matrices
+// One workgroup computes a value from one fixed order of sums: the same bits on every run.
 #include "ep_host.h"
 #include "ep_rows.h"
 
@@ -299,8 +323,8 @@ __device__ __forceinline__ typename Acc<I8>::type mfma(u32x4 a, u32x4 b,
 // One operand's half tile in LDS: rows by 128 bytes of k (16-byte chunk c of row r at
 // c ^ (r / 2 & 7)), or, where k is the slow axis, 64 k by 128 columns (256 bytes; chunk c of
 // row k at c ^ 4 (k & 3)): no two lanes that LDS serves together share a bank.  (It
-// serves lanes 0-3, 12-15 and 20-27 of a 16-byte read together: with c ^ (r & 7) half of
-// the time went into conflicts.)
+// serves lanes 0-3, 12-15 and 20-27 of a 16-byte read together: with c ^ (r & 7) conflicts
+// were half of its busy cycles.)
 template <bool SLOW_K>
 __device__ __forceinline__ u32x4 fragment(const uint8_t* half, int lane_off, int ks) {
   if constexpr (SLOW_K) {
@@ -755,7 +779,10 @@ void product_kernel(Product p, Epi epi) {
 // bytes of the contraction, each with loads of its own running ahead in LDS of its own, so
 // that there is no barrier before the sums meet at the end.
 // FUSE: at most 16 rows of x in bf16, which every workgroup rounds to 8-bit integers
-// itself while its first weights are on their way.
+// itself while its first weights are on their way (51 MB of weights: 14 us; rounded by a
+// launch before it, 4 + 11).
+// Bound by HBM from about 50 MB of weights on (7168 x 2048 for 32 experts of 16 rows: 5.5
+// TB/s), below that by the latency of counts, weights and sums one after the other: 5 us.
 template <bool I8>
 struct Acc4 {
   using type = std::conditional_t<I8, i32x4, f32x4>;
@@ -1359,7 +1386,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   if (rc != EP_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
   uint8_t* h = (uint8_t*)a->workspace;
-  uint8_t* dgu = h + up(rows->capacity * 2 * I);
+  uint8_t* dgu = any ? h + up(cap * 2 * I) : nullptr;
   EP_LOG("ffn_backward experts=%d max_rows=%d H=%d I=%d", r.E, rows->max_rows, H, I);
   Product p{};
   p.rows = r;

@@ -199,6 +199,9 @@ def test_binding_refuses(monkeypatch):
     q = ep.Int8Weight(torch.zeros((64, 64), dtype=torch.int8), torch.zeros(64))
     q2 = ep.Int8Weight(torch.zeros((64, 32), dtype=torch.int8), torch.zeros(64))
     ll = ep.LLLayout(4, 2, 2, 1, 4, 8, torch.zeros((2, 1)), None, None)
+    q3 = ep.Int8Weight(torch.zeros((3, 64, 64), dtype=torch.int8), torch.zeros((3, 64)))
+    four = ep.QuantWeight(torch.zeros((64, 32), dtype=torch.uint8), torch.zeros((64, 1), dtype=bf),
+                          group=64)
     stack = torch.zeros((3, 64, 64), dtype=bf), torch.zeros((3, 64, 32), dtype=bf)
     for call in (lambda: ep.expert_ffn(x, w13, q2), lambda: ep.expert_ffn(x, q, w2),
                  lambda: ep.expert_ffn(x, w13[:62], w2), lambda: ep.expert_ffn(x, w13, w2[:32]),
@@ -209,6 +212,9 @@ def test_binding_refuses(monkeypatch):
                  lambda: ep.expert_ffn(x, w13, w2, workspace=torch.zeros(8, dtype=torch.uint8)),
                  lambda: ep.expert_ffn_backward(x, x, x, q, q2),
                  lambda: ep.expert_ffn_backward(x, x, x, w13, w2, layout=ll),
+                 lambda: ep.expert_ffn(x, w13, four), lambda: ep.expert_ffn(x, four, w2),
+                 lambda: ep.expert_ffn_backward(x, x, x, w13, four),
+                 lambda: ep.moe_layer(x, x[:, :2].int(), x[:, :2], q3, q3),
                  lambda: ep.int8_linear(x[:, :32], q), lambda: ep.int8_linear(x, q, layout=ll),
                  lambda: ep.Int8Weight(torch.zeros((4, 24), dtype=torch.int8), torch.zeros(4)),
                  lambda: ep.Int8Weight(torch.zeros(16, dtype=torch.int8), torch.zeros(1))):
