@@ -22,7 +22,7 @@
 //                   of the cycles; without any load they are 82 %, the rest is barriers.
 //                   With few rows per expert it is bound by HBM: 6.8 TB/s of weights.
 //   few_kernel      few rows: weights as a stream, the contraction split over wavefronts
-//   small_kernel    gradients of few rows and small matrices
+//   small_kernel    what lies between: 64 by 64 tiles on many CUs
 // One workgroup computes a value from one fixed order of sums: the same bits on every run.
 #include "ep_host.h"
 #include "ep_rows.h"
@@ -168,6 +168,10 @@ struct StoreRows {
     uint16_t* to = y + (int64_t)slot * n + c;
     if ((n & 7) == 0) {
       *(u32x4*)to = r;
+    } else if ((n & 1) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (c + 2 * i < n) *(uint32_t*)(to + 2 * i) = r[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++)
@@ -1006,15 +1010,18 @@ __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
 }
 
 // ---------------------------------------------------------------- small products
-// Gradients whose 256 by 256 tiles would leave most CUs idle: 64 by 64 tiles, each
+// Products whose 256 by 256 tiles would leave most CUs idle: 64 by 64 tiles, each
 // wavefront all of a tile over every fourth step of the contraction, with loads of its own
 // in LDS of its own, as above.
 constexpr int kST = 64;                // rows and columns of a tile
 
-template <int KIND, class Epi>
+template <int KIND, class Epi, bool I8>
 __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
-  constexpr bool kSlowA = KIND == kOuter;
-  static_assert(KIND != kRowsT && !Epi::gate);
+  constexpr bool kSlowA = KIND == kOuter, kSlowB = KIND != kRowsT;
+  constexpr int kCols = Epi::gate ? kST / 2 : kST;         // of gate, and as many of up
+  using acc_t = typename Acc<I8>::type;
+  using val_t = typename Acc<I8>::scalar;
+  typedef val_t val4 __attribute__((ext_vector_type(4)));
   constexpr int kOp = 8192, kSmallStage = 2 * kOp, kMine = 2 * kSmallStage, kLoads = 16;
 
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kMine];
@@ -1023,7 +1030,7 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
   const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
   const uint32_t mine = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds + w * kMine;
   const uint8_t* my = lds + w * kMine;
-  const int NT = (p.n + kST - 1) / kST, MT = (p.m + kST - 1) / kST;
+  const int NT = (p.n + kCols - 1) / kCols, MT = (p.m + kST - 1) / kST;
   // chunk c of row r at c ^ (r / 2 & 7); where k is slow, of 128 bytes of a k at c ^ 4 (k / 2 & 1)
   auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
   const int chunk_n = (l & 7) ^ (((l >> 4) & 1) << 2);
@@ -1074,14 +1081,14 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
       if (tid < kST)
         slots[tid] = tid >= nrows ? -1 : blocks ? p.rows.slot(e, row0 + tid) : slot0 + tid;
       a0 = p.a + (int64_t)slot0 * p.a_row;
-      b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kST * 2;
+      b0 = p.b + (int64_t)e * p.b_expert + (int64_t)nt * kCols * (kSlowB ? 2 : p.b_row);
       k_a = p.k;
-      k_b = p.k / 2;
+      k_b = kSlowB ? p.k / 2 : p.k;
       KT = (p.k + 127) / 128;
       __syncthreads();
     }
-    const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = 64 * p.b_row;
-    int off_a[8];
+    const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
+    int off_a[8], off_b[8];
     const bool in_a = chunk_n * 8 < nrows, in_b = nt * kST + chunk_n * 8 < p.n;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -1091,23 +1098,32 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
         const int s = slots[j * 8 + (l >> 3)];
         off_a[j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
       }
+      if constexpr (kSlowB) {
+        off_b[j] = in_b ? (j * 8 + (l >> 3)) * (int)p.b_row + chunk_n * 16 : kAbsent;
+      } else {
+        const int r = (Epi::gate ? j & 3 : j) * 8 + (l >> 3);
+        off_b[j] = nt * kCols + r < p.n ? r * (int)p.b_row + chunk_k(j) * 16 : kAbsent;
+      }
     }
+    const int64_t far = (int64_t)p.far * p.b_row;
     auto load = [&](int i, int stage) {
       const int64_t t = i * 4 + w;
       const uint32_t to = mine + stage * kSmallStage;
       const i32x4 da = descriptor(a0 + t * step_a), db = descriptor(b0 + t * step_b);
+      const i32x4 du = Epi::gate ? descriptor(b0 + far + t * step_b) : db;
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const int k = j * 8 + (l >> 3);
         const bool ok = kSlowA ? k < k_a - t * 64 : chunk_k(j) * 16 < k_a - t * 128;
         load_lds<false>(to + j * 1024, ok ? off_a[j] : kAbsent, da);
-        load_lds<false>(to + kOp + j * 1024,
-                        in_b && k < k_b - t * 64 ? k * (int)p.b_row + chunk_n * 16 : kAbsent, db);
+        const bool ok_b = kSlowB ? k < k_b - t * 64 : chunk_k(j) * 16 < k_b - t * 128;
+        load_lds<false>(to + kOp + j * 1024, ok_b ? off_b[j] : kAbsent,
+                        Epi::gate && j >= 4 ? du : db);
       }
     };
-    f32x16 acc[2][2];
+    acc_t acc[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i >> 1][i & 1] = f32x16{};
+    for (int i = 0; i < 4; i++) acc[i >> 1][i & 1] = acc_t{};
     load(0, 0);
     load(1, 1);
     for (int i = 0; i * 4 < KT; i++) {
@@ -1120,7 +1136,8 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
         for (int b = 0; b < 2; b++) {
           if constexpr (kSlowA) fa[b][ks] = slow(st, b, ks);
           else fa[b][ks] = fast(st, b, ks);
-          fb[b][ks] = slow(st + kOp, b, ks);
+          if constexpr (kSlowB) fb[b][ks] = slow(st + kOp, b, ks);
+          else fb[b][ks] = fast(st + kOp, b, ks);
         }
       wait_lds();
       load(i + 2, i & 1);
@@ -1128,7 +1145,7 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
       for (int ks = 0; ks < 4; ks++)
 #pragma unroll
         for (int b = 0; b < 4; b++)
-          acc[b >> 1][b & 1] = mfma<false>(fb[b >> 1][ks], fa[b & 1][ks], acc[b >> 1][b & 1]);
+          acc[b >> 1][b & 1] = mfma<I8>(fb[b >> 1][ks], fa[b & 1][ks], acc[b >> 1][b & 1]);
     }
     wait_loads<0>();
 
@@ -1138,27 +1155,32 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int r = (b & 1) * 32 + (l & 31), c = (b >> 1) * 8 + 2 * i + (l >> 5);
-        f32x4 v;
+        val4 v;
 #pragma unroll
         for (int j = 0; j < 4; j++) v[j] = acc[b >> 1][b & 1][i * 4 + j];
-        *(f32x4*)(lds + w * kMine + r * 256 + ((c ^ (r & 15)) << 4)) = v;
+        *(val4*)(lds + w * kMine + r * 256 + ((c ^ (r & 15)) << 4)) = v;
       }
     __syncthreads();
+    constexpr int kChunks = kCols / 8;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int r = h * 32 + (tid >> 3), c = tid & 7;
+    for (int h = 0; h < kST * kChunks / 256; h++) {
+      const int r = h * (256 / kChunks) + tid / kChunks, c = tid % kChunks;
       if (r >= nrows) continue;
-      float v[8];
+      val_t v[8], u[8];
+      auto sum = [&](int chunk, val_t* to) {
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        f32x4 t = {};
+        for (int q = 0; q < 2; q++) {
+          val4 t = {};
 #pragma unroll
-        for (int o = 0; o < 4; o++)
-          t += *(const f32x4*)(lds + o * kMine + r * 256 + (((2 * c + q) ^ (r & 15)) << 4));
+          for (int o = 0; o < 4; o++)
+            t += *(const val4*)(lds + o * kMine + r * 256 + (((chunk + q) ^ (r & 15)) << 4));
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[q * 4 + j] = t[j];
-      }
-      epi(e, KIND == kOuter ? row0 + r : slots[r], nt * kST + c * 8, v, v);
+          for (int j = 0; j < 4; j++) to[q * 4 + j] = t[j];
+        }
+      };
+      sum(2 * c, v);
+      if constexpr (Epi::gate) sum(8 + 2 * c, u);
+      epi(e, KIND == kOuter ? row0 + r : slots[r], nt * kCols + c * 8, v, u);
     }
     __syncthreads();
   }
@@ -1183,10 +1205,26 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t row_tiles(const Rows& r, int max_rows, int tile) { return (int64_t)max_rows / tile + r.E; }
 
 // 256 by 256 tiles, `tiles` of them, `steps` of 128 bytes of the contraction: a step takes
-// 0.86 us on half a tile's rows, 1.3 on a whole tile's, 1.2 where all CUs stream weights.
-double wide_us(int64_t tiles, int64_t steps, double rows) {
-  if (tiles >= 200) return 4 + (double)ceil_div(tiles, 256) * ((double)steps * 1.2 + 6);
-  return 10 + (double)steps * (rows > 128 ? 1.3 : 0.86);
+// 0.86 us on half a tile's rows, 1.3 on a whole tile's, 1.2 where all CUs stream weights; rows
+// of columns that are no whole 16 bytes are stored in parts.
+double wide_us(int64_t tiles, int64_t steps, double rows, int cols) {
+  const double parts = cols % 8 ? 5 : 0;
+  if (tiles >= 200) return 4 + (double)ceil_div(tiles, 256) * ((double)steps * 1.2 + 6 + parts);
+  return 10 + (double)steps * (rows > 128 ? 1.3 : 0.86) + parts;
+}
+
+// 64 by 64 tiles: a step of a workgroup's four wavefronts is 64 KiB from the caches, which all
+// CUs together get at 12 TB/s (4.8 where it is weights from HBM), or 0.55 us of one alone.
+double small_us(double tiles, int64_t steps, double weight_bytes) {
+  const double rounds = std::max(1.0, tiles / 256),
+               step = std::max(0.55, 1.37 * std::min(1.0, tiles / 256));
+  return 3.5 + std::max(rounds * ((double)ceil_div(steps, 4) * step + 2.8), weight_bytes / 4.8e6);
+}
+
+// How many tiles of t rows the experts' rows are on average.
+double row_tiles_mean(int experts, double rows, int t) {
+  if (experts == 1) return (double)ceil_div((int64_t)rows, t);
+  return experts * std::max(1.0, rows / t + (rows > t ? 0.5 : rows > t / 2 ? 0.25 : 0));
 }
 
 template <class Epi, bool I8, int TT, bool FUSE>
@@ -1199,24 +1237,37 @@ int launch_few(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t 
   return check_launch("ep_ffn few rows");
 }
 
-// Activations by a weight's rows.  Measured, few rows against wide tiles (us): one row by
-// 7168 x 7168 int8 11 : 53, 64 rows 20 : 64, 256 rows 63 : 80, 512 rows 118 : 82; 512 rows by
-// 512 x 7168 19 : 73; 32 experts of about 16 rows, bf16, 4096 x 7168 313 : 281 and 7168 x 2048
-// 168 : 218.
+template <int KIND, class Epi, bool I8>
+int launch_small(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t st) {
+  const int64_t tiles = row_tiles * ceil_div(p.n, Epi::gate ? kST / 2 : kST);
+  EP_LOG("  small tiles: up to %lld", (long long)tiles);
+  small_kernel<KIND, Epi, I8><<<dim3((int)(tiles < 256 ? tiles : 256)), dim3(256), 0, st>>>(p, epi);
+  return check_launch("ep_ffn small product");
+}
+
+// Activations by a weight's rows.  Measured, wide, few, small (us), 8-bit, rows x columns of the
+// weight: 1 row by 7168 x 7168 53, 11, -; 16 rows 53, 12, 14; 64 rows 63, 20, 17; 256 rows 68, 66,
+// 41; 980 rows by 861 x 7120 92, 52, 23; 4000 by 4000 x 512 23, 114, 70; 33 by 1237 x 2000 23, 6,
+// 9.  Both products of a bf16 block: 512 rows, 2048 x 1024 64, 35, 25; 2048 rows 67, 124, 80; 32
+// experts of about 16 rows, 7168 x 2048: first 281, 313, second 218, 168.
 template <class Epi, bool I8>
 int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E, wide = Epi::gate ? 128 : kBN;
   const double rows = (double)max_rows / E, cols = Epi::gate ? 2.0 * p.n : p.n;
   const int64_t steps = ceil_div(p.k, 128);
+  const double weight = cols * p.k;                        // bytes of one expert
   const int few = rows <= 8 ? 16 : 32;
-  const double few_tiles = E * std::max(1.0, rows <= few ? rows / few + 0.5 : rows / few + 0.25);
-  const double bytes = few_tiles * cols * p.k;             // of weights, for each row tile again
-  const double rounds = std::max(1.0, few_tiles * (cols / 32) / 512);
-  const double few_us = 4 + std::max(bytes / (few == 16 ? 7.0e6 : 6.2e6),
-                                     rounds * ((double)ceil_div(steps, 4) * 0.35 + 1));
+  const double few_tiles = row_tiles_mean(E, rows, few);
+  const double few_rounds = few_tiles * (cols / 32) / 512, few_steps = (double)ceil_div(steps, 4);
+  const double few_us =
+      3.5 + std::max(few_tiles * weight / (few == 16 ? 7.0e6 : 6.2e6),
+                     few_rounds <= 1 ? few_steps * 0.35 + 0.5 : few_rounds * (few_steps * 0.45 + 2.7));
+  const double small = small_us(row_tiles_mean(E, rows, kST) * cols / kST, steps, E * weight);
   const int64_t wide_tiles = E * std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5)) *
                              ceil_div(p.n, wide);
-  if (few_us < wide_us(wide_tiles, steps, rows)) {
+  if (std::min(few_us, small) < wide_us(wide_tiles, steps, rows, p.n)) {
+    if (small < few_us)
+      return launch_small<kRowsT, Epi, I8>(p, epi, row_tiles(p.rows, max_rows, kST), st);
     if (few == 16) return launch_few<Epi, I8, 1, false>(p, epi, row_tiles(p.rows, max_rows, 16), st);
     return launch_few<Epi, I8, 2, false>(p, epi, row_tiles(p.rows, max_rows, 32), st);
   }
@@ -1225,29 +1276,25 @@ int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
 }
 
 // A gradient.  Measured, small tiles against wide ones: 12 experts of 88 rows, 1000 x 344: dh
-// 14 : 39, dx 16 : 20, dw13 33 : 15; one matrix of 1024 rows, 2048 x 1024, all four 88 : 149; 8
+// 13 : 39, dx 16 : 20, dw13 33 : 15; one matrix of 1024 rows, 2048 x 1024, all four 88 : 149; 8
 // experts of 512 rows, 1024 x 1024, all four 187 : 126.
 template <int KIND, class Epi>
 int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E;
   const double rows = (double)max_rows / E;
-  auto tiles = [&](int t) {
-    const int64_t m = KIND == kOuter ? ceil_div(p.m, t) : std::max<int64_t>(1, (int64_t)(rows / t + 0.5));
-    return E * m * ceil_div(p.n, t);
-  };
   const int64_t steps = KIND == kOuter ? (int64_t)(rows / 64) + 1 : ceil_div(p.k, 128);
-  const double small_us =
-      5 + (double)ceil_div(tiles(kST), 256) * ((double)ceil_div(steps, 4) * 1.8 + 1.5);
-  if (small_us < wide_us(tiles(kBM), steps, KIND == kOuter ? kBM : rows)) {
-    const int64_t n = KIND == kOuter ? tiles(kST)
-                                     : row_tiles(p.rows, max_rows, kST) * ceil_div(p.n, kST);
-    EP_LOG("  small tiles: up to %lld", (long long)n);
-    small_kernel<KIND, Epi><<<dim3((int)(n < 256 ? n : 256)), dim3(256), 0, st>>>(p, epi);
-    return check_launch("ep_ffn small product");
-  }
-  const int64_t n = KIND == kOuter ? tiles(kBM)
-                                   : row_tiles(p.rows, max_rows, kBM) * ceil_div(p.n, kBN);
-  return launch<KIND, Epi, false>(p, epi, n, st);
+  const double small_tiles = KIND == kOuter ? (double)E * ceil_div(p.m, kST)
+                                            : row_tiles_mean(E, rows, kST);
+  const int64_t wide_rows = KIND == kOuter ? ceil_div(p.m, kBM)
+                                           : std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5));
+  const double weight = KIND == kOuter ? 0 : (double)E * p.n * p.k;
+  if (small_us(small_tiles * ceil_div(p.n, kST), steps, weight) <
+      wide_us(E * wide_rows * ceil_div(p.n, kBN), steps, KIND == kOuter ? kBM : rows, p.n))
+    return launch_small<KIND, Epi, false>(
+        p, epi, KIND == kOuter ? E * ceil_div(p.m, kST) : row_tiles(p.rows, max_rows, kST), st);
+  return launch<KIND, Epi, false>(
+      p, epi, (KIND == kOuter ? E * ceil_div(p.m, kBM) : row_tiles(p.rows, max_rows, kBM)) *
+                  ceil_div(p.n, kBN), st);
 }
 
 // Whether every workgroup rounds x to integers by itself.
