@@ -18,7 +18,15 @@ MANY = [
 ]
 
 
-@pytest.mark.parametrize("shape", MANY, ids=ident)
+# on 64-row tiles
+MIDDLE = [
+    dict(N=512, K=1, E=0, A=1, H=2048, I=1024),
+    dict(N=333, K=1, E=0, A=1, H=2008, I=1032),
+    dict(N=300, K=3, E=6, A=8, H=1544, I=776, skew=0.7),
+]
+
+
+@pytest.mark.parametrize("shape", MANY + MIDDLE, ids=ident)
 def test_forward(shape):
     c = Case(21, **shape)
     y, gu = c.full(c.H), c.full(2 * c.I)
@@ -58,6 +66,9 @@ def test_backward(shape):
     dict(N=4096, K=1, E=0, A=1, H=1024, I=512),
     dict(N=6000, K=1, E=0, A=1, H=1008, I=528),
     dict(N=3000, K=3, E=4, A=16, H=1008, I=528, skew=1.0),
+    dict(N=512, K=1, E=0, A=1, H=4096, I=2048),                       # 64-row tiles
+    dict(N=333, K=1, E=0, A=1, H=4080, I=2064),
+    dict(N=300, K=3, E=6, A=8, H=3088, I=1552, skew=0.7),
 ], ids=ident)
 def test_int8_ffn(shape):
     c = Case(23, int8=True, **shape)
@@ -67,15 +78,18 @@ def test_int8_ffn(shape):
 
 
 @pytest.mark.parametrize("int8", [False, True])
-def test_low_latency_many_rows(int8):
+@pytest.mark.parametrize("shape", [dict(N=4000, K=2, E=8, R=8, ll=500, H=1008, I=528),
+                                   dict(N=400, K=2, E=4, R=4, ll=100, H=2064, I=1040)], ids=ident)
+def test_low_latency_many_rows(int8, shape):
     """Row tiles that cross the sources' sub-blocks."""
-    c = Case(24, N=4000, K=2, E=8, A=1, H=1008, I=528, R=8, ll=500, drop=0.2, int8=int8)
+    c = Case(24, A=1, drop=0.2, int8=int8, **shape)
     y = ep.expert_ffn(c.x, c.w13, c.w2, layout=c.layout, out=c.full(c.H))
     c.untouched(y)
     (check_int8_ffn if int8 else check_ffn)(c, y)
 
 
-@pytest.mark.parametrize("N,C,O", [(4096, 512, 1024), (4111, 1040, 1237), (5000, 16, 3001)])
+@pytest.mark.parametrize("N,C,O", [(4096, 512, 1024), (4111, 1040, 1237), (5000, 16, 3001),
+                                   (980, 7120, 861), (700, 4096, 1022)])
 def test_int8_linear(N, C, O):
     g = gen(25)
     codes = torch.randint(-128, 128, (O, C), generator=g, device="cuda").to(torch.int8)
