@@ -650,15 +650,16 @@ void product_kernel(Product p, Epi epi) {
         for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)x[j]);
       }
     };
-    // the same for values that are rounded to bf16 already: half the bytes
-    auto turn16 = [&](const f32x16& x) {
+    // the same for values that are rounded to bf16 already: half the bytes, so that two
+    // blocks can be under way
+    auto turn16 = [&](const f32x16& x, uint8_t* mine) {
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        *(u32x2*)(mine0 + (v & 31) * 64 + ((i ^ ((v >> 2) & 3)) << 4) + (v >> 5) * 8) =
+        *(u32x2*)(mine + (v & 31) * 64 + ((i ^ ((v >> 2) & 3)) << 4) + (v >> 5) * 8) =
             u32x2{pack2(x[i * 4], x[i * 4 + 1]), pack2(x[i * 4 + 2], x[i * 4 + 3])};
     };
-    auto take16 = [&](int it) {
-      return *(const u32x4*)(mine0 + it * 1024 + (v >> 2) * 64 +
+    auto take16 = [&](int it, const uint8_t* mine) {
+      return *(const u32x4*)(mine + it * 1024 + (v >> 2) * 64 +
                              (((v & 3) ^ ((v >> 4) & 3)) << 4));
     };
     auto row_at = [&](int r) {
@@ -697,7 +698,7 @@ void product_kernel(Product p, Epi epi) {
         for (int mb = 0; mb < 2; mb++) {
           const int r0 = h * 128 + wm * 64 + mb * 32;
           if (r0 >= cur.nrows) continue;
-          // `what` is turned and stored by epi.put (a gate: h, and g and u where asked for)
+          // what is turned is stored by epi.put (a gate: h, and g and u where asked for)
           auto values = [&](int half) {
             f32x16 x;
             if constexpr (I8) {
@@ -709,9 +710,8 @@ void product_kernel(Product p, Epi epi) {
             }
             return x;
           };
-          auto put = [&](const f32x16& x, int what) {
-            turn16(x);
-            const u32x4 q[2] = {take16(0), take16(1)};
+          auto put = [&](const uint8_t* mine, int what) {
+            const u32x4 q[2] = {take16(0, mine), take16(1, mine)};
 #pragma unroll
             for (int it = 0; it < 2; it++) {
               const int r = r0 + it * 16 + (v >> 2);
@@ -723,14 +723,19 @@ void product_kernel(Product p, Epi epi) {
             f32x16 x;
 #pragma unroll
             for (int j = 0; j < 16; j++) x[j] = a[j] * sigmoid(a[j]) * b[j];
-            put(x, 0);
+            turn16(x, mine0);
+            put(mine0, 0);
             if (epi.gu) {
-              put(a, 1);
-              put(b, 2);
+              turn16(a, mine0);
+              turn16(b, mine1);
+              put(mine0, 1);
+              put(mine1, 2);
             }
           } else {
-            put(a, 0);
-            put(b, 128);
+            turn16(a, mine0);
+            turn16(b, mine1);
+            put(mine0, 0);
+            put(mine1, 128);
           }
         }
     } else {
