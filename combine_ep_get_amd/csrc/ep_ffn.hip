@@ -48,6 +48,7 @@ constexpr int kHalf = 16384;           // bytes of half of either operand's tile
 constexpr int kStage = 4 * kHalf;      // a's two halves, b's two halves
 constexpr int kSteps = 2;              // stages in LDS
 constexpr int kGroupM = 8;             // row tiles that are neighbours in the order of tiles
+constexpr int kLastTile = INT32_MAX - 1024;    // strides behind it are in 32 bits still
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -838,7 +839,7 @@ __global__ __launch_bounds__(256) void few_kernel(Product p, Epi epi) {
   const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
   const bool blocks = p.rows.count && !p.rows.offset;
-  for (;; tile += G) {
+  for (; tile <= kLastTile; tile += G) {
     int e = 0, nt = tile, nrows = p.rows.plain, slot0 = 0;
     if constexpr (!FUSE) {
       Found x;
@@ -1059,7 +1060,7 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
   const int G = gridDim.x;
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
   const bool blocks = p.rows.count && !p.rows.offset;
-  for (;; tile += G) {
+  for (; tile <= kLastTile; tile += G) {
     int e, nt, nrows, row0, slot0, k_a, k_b, KT;
     const uint8_t *a0, *b0;
     if constexpr (KIND == kOuter) {
@@ -1329,9 +1330,13 @@ int run_bf16(Product p, const Epi& epi, int max_rows, const void* x, hipStream_t
   return run_rows<Epi, false>(p, epi, max_rows, st);
 }
 
-// Tiles are counted in 32 bits, the smallest of them of 16 rows by 16 columns.
+// Tiles are counted in 32 bits, the smallest of them of 16 rows by 16 columns.  Regions that
+// overlap (counts that nobody wrote, say) may be the whole buffer for every expert: then
+// row tiles and wide tiles still fit, and few_kernel and small_kernel stop at the last that does.
 bool few_enough(const Rows& r, int cols) {
-  return row_tiles(r, r.cap, 16) * ceil_div(cols, 16) <= INT32_MAX;
+  const int64_t most = (int64_t)r.E * r.cap;
+  return row_tiles(r, r.cap, 16) * ceil_div(cols, 16) <= INT32_MAX &&
+         most / 16 + r.E <= INT32_MAX && (most / kBM + r.E) * ceil_div(cols, 128) <= kLastTile;
 }
 
 // Offsets inside an expert's sub-blocks have 32 bits (see descriptor()).

@@ -123,6 +123,17 @@ def test_backward_refuses_sub_blocks():
     assert grad(blocks()) == INVALID
 
 
+@no_gpu
+def test_tiles_of_overlapping_regions_fit():
+    assert accepted(ffn(rows(capacity=1 << 20, num_experts=1024)))
+
+
+def test_tiles_beyond_32_bits():
+    """Counts that give every expert the whole buffer must leave the tiles countable."""
+    big = rows(capacity=1 << 27, num_experts=1024)
+    assert ffn(big) == INVALID and integer(big, y=1 << 46) == INVALID
+
+
 def test_sub_blocks_beyond_32_bits():
     """Offsets inside an expert's sub-blocks have 32 bits: larger ones are refused."""
     big = blocks(capacity=1 << 30, num_experts=1, num_sources=64, rows_per_source=1 << 16)
