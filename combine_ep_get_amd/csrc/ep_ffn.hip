@@ -58,6 +58,12 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 //   kOuter  A [k][row], B [k][column]     a weight's gradient: k runs over an expert's rows
 enum { kRowsT, kRows, kOuter };
 
+struct Outer {
+  const uint8_t *a, *b;
+  int64_t a_row, b_row;
+  int m, n;
+};
+
 struct Product {            // kernel argument
   Rows rows;
   const uint8_t* a;
@@ -67,6 +73,7 @@ struct Product {            // kernel argument
   int k;                    // contraction: bytes of a row of a (kRowsT, kRows)
   int m, n;                 // D's rows (kOuter) and columns
   int far;                  // > 0: column j of a tile's second half is b's row far + n0/2 + j
+  Outer also;               // kOuter: a second product over the same rows
 };
 
 // 16 bytes per lane from global memory straight to LDS, lane l's at base + 16 l.  In asm,
@@ -158,7 +165,7 @@ __device__ __forceinline__ f32x4 load4(const float* p, int c, int n) {
 struct StoreRows {
   static constexpr bool gate = false;
   static constexpr int stores = 16;
-  __device__ __forceinline__ int columns() const { return n; }
+  __device__ __forceinline__ int columns(int) const { return n; }
   uint16_t* y;
   int n;
   const float *sx, *sw;    // 8-bit products: scales per slot and per expert and column
@@ -200,21 +207,23 @@ struct StoreRows {
   }
 };
 
-struct StoreMatrix {       // kOuter: [e][m][n]
+// kOuter: [e][m][n], and of a second product where e is `experts` more
+struct StoreMatrix {
   static constexpr bool gate = false;
   static constexpr int stores = 16;
-  __device__ __forceinline__ int columns() const { return n; }
-  uint16_t* y;
-  int m, n;
+  uint16_t *y, *also;
+  int experts, m, n, also_m, also_n;
+  __device__ __forceinline__ int columns(int e) const { return e < experts ? n : also_n; }
   static constexpr bool rounds = true;
   __device__ __forceinline__ void put(int e, int row, int c, u32x4 r, int more) const {
+    const bool first = e < experts;
+    const int width = first ? n : also_n, of = first ? e * m : (e - experts) * also_m;
     c += more;
-    if (c < n) *(u32x4*)(y + ((int64_t)e * m + row) * n + c) = r;
+    if (c < width) *(u32x4*)((first ? y : also) + ((int64_t)of + row) * width + c) = r;
   }
   __device__ __forceinline__ void operator()(int e, int row, int c, const float* v,
                                              const float*) const {
-    if (c >= n) return;
-    *(u32x4*)(y + ((int64_t)e * m + row) * n + c) = pack8(v);
+    put(e, row, c, pack8(v), 0);
   }
 };
 
@@ -222,7 +231,7 @@ struct StoreMatrix {       // kOuter: [e][m][n]
 struct StoreGate {
   static constexpr bool gate = true;
   static constexpr int stores = 8;
-  __device__ __forceinline__ int columns() const { return inter; }
+  __device__ __forceinline__ int columns(int) const { return inter; }
   uint16_t* h;             // [slot][inter]
   uint16_t* gu;            // [slot][2 inter] or NULL
   int inter;
@@ -271,7 +280,7 @@ struct StoreGateGrad {
   static constexpr bool gate = false;
   static constexpr int stores = 48;
   static constexpr bool rounds = false;
-  __device__ __forceinline__ int columns() const { return inter; }
+  __device__ __forceinline__ int columns(int) const { return inter; }
   const uint16_t* gu;      // [slot][2 inter]
   uint16_t* dgu;           // [slot][2 inter]
   uint16_t* h;             // [slot][inter]
@@ -358,7 +367,7 @@ void product_kernel(Product p, Epi epi) {
   const int wm = w >> 2, wn = w & 3;     // rows wm*64.., columns wn*32.. of each half
   const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
   const int NT = KIND == kRowsT && p.far ? (p.n + 127) / 128 : (p.n + kBN - 1) / kBN;
-  const int MT = (p.m + kBM - 1) / kBM;                    // kOuter
+  const int MT = (p.m + kBM - 1) / kBM;                    // kOuter, of its first product
   const bool blocks = p.rows.count && !p.rows.offset;      // rows of several sub-blocks
   experts.fill(p.rows, kBM);
   // Tiles, those of over 128 rows, and those of them that are taken as two halves of 128 rows:
@@ -366,7 +375,8 @@ void product_kernel(Product p, Epi epi) {
   // less time.  Half a tile takes about 0.6 of a tile's.  16 experts of 512 rows on average:
   // dh, 264 tall and 48 short tiles, 392 us without halves, 355 with them.
   const int G = gridDim.x;
-  int total = p.rows.E * MT * NT, tall = 0, halved = 0;
+  const int NT2 = (p.also.n + kBN - 1) / kBN, MT2 = (p.also.m + kBM - 1) / kBM;
+  int total = p.rows.E * (MT * NT + MT2 * NT2), tall = 0, halved = 0;
   if constexpr (KIND != kOuter) {
     tall = uniform(experts.first[p.rows.E]) * NT;
     total = tall + uniform(experts.first_short[p.rows.E]) * NT;
@@ -403,7 +413,7 @@ void product_kernel(Product p, Epi epi) {
   int k_a = 0, k_b = 0;        // contraction of a and b in what their tail counts
   int off_a[2][2], off_b[2][2];
   const int64_t far = (int64_t)p.far * p.b_row;
-  const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
+  int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
 
   // step t of the operand at `at`; TAIL: its last bytes may be behind the contraction's end
   auto load_a = [&](auto tail, const uint8_t* at, int t, int stage, int h) {
@@ -443,18 +453,30 @@ void product_kernel(Product p, Epi epi) {
     x.KT = 2;
     k_a = k_b = 0;
     if (tile >= total) return;
+    int64_t a_row = p.a_row, b_row = p.b_row;
+    int n = p.n;
     if constexpr (KIND == kOuter) {
-      x.e = tile / (MT * NT);
-      const int r = tile - x.e * MT * NT;
-      const int g = r / (kGroupM * NT), f = g * kGroupM, gs = min(kGroupM, MT - f);
-      const int q = r - g * kGroupM * NT;
+      const bool first = tile < p.rows.E * MT * NT;
+      const int nts = first ? NT : NT2, mts = first ? MT : MT2;
+      if (!first) {
+        tile -= p.rows.E * MT * NT;
+        a_row = p.also.a_row;
+        b_row = p.also.b_row;
+        n = p.also.n;
+      }
+      const int e = tile / (mts * nts), r = tile - e * mts * nts;
+      const int g = r / (kGroupM * nts), f = g * kGroupM, gs = min(kGroupM, mts - f);
+      const int q = r - g * kGroupM * nts;
+      x.e = first ? e : e + p.rows.E;
       x.row0 = (f + q % gs) * kBM;
       x.nt = q / gs;
-      x.nrows = min(kBM, p.m - x.row0);
-      k_a = k_b = uniform(experts.count[x.e]);
-      x.slot0 = uniform(experts.slot[x.e]);
-      a0 = p.a + (int64_t)x.slot0 * p.a_row + (int64_t)x.row0 * 2;
-      b0 = p.b + (int64_t)x.slot0 * p.b_row + (int64_t)x.nt * kBN * 2;
+      x.nrows = min(kBM, (first ? p.m : p.also.m) - x.row0);
+      k_a = k_b = uniform(experts.count[e]);
+      x.slot0 = uniform(experts.slot[e]);
+      a0 = (first ? p.a : p.also.a) + (int64_t)x.slot0 * a_row + (int64_t)x.row0 * 2;
+      b0 = (first ? p.b : p.also.b) + (int64_t)x.slot0 * b_row + (int64_t)x.nt * kBN * 2;
+      step_a = 64 * a_row;
+      step_b = 64 * b_row;
       x.KT = max(2, (k_a + 63) / 64);
     } else {
       // the short ones last: they take half the time, and a workgroup whose share was all
@@ -499,7 +521,7 @@ void product_kernel(Product p, Epi epi) {
         const int r = w * 16 + j * 8 + (l >> 3), k = w * 8 + j * 4 + (l >> 4);
         const int c = h * 128 + chunk_n * 8;
         if constexpr (kSlowA) {
-          off_a[h][j] = c < x.nrows ? k * (int)p.a_row + c * 2 : kAbsent;
+          off_a[h][j] = c < x.nrows ? k * (int)a_row + c * 2 : kAbsent;
         } else {
           int s = h * 128 + r;               // slots behind slot0
           const bool in = s < x.nrows;
@@ -507,7 +529,7 @@ void product_kernel(Product p, Epi epi) {
           off_a[h][j] = in ? s * (int)p.a_row + chunk_k(j) * 16 : kAbsent;
         }
         if constexpr (kSlowB)
-          off_b[h][j] = x.nt * kBN + c < p.n ? k * (int)p.b_row + c * 2 : kAbsent;
+          off_b[h][j] = x.nt * kBN + c < n ? k * (int)b_row + c * 2 : kAbsent;
         else if (p.far)
           off_b[h][j] = x.nt * 128 + r < p.n ? r * (int)p.b_row + chunk_k(j) * 16 : kAbsent;
         else
@@ -775,7 +797,7 @@ void product_kernel(Product p, Epi epi) {
     tile += G;
     if (tile >= total) break;
     // whole tiles store the same number of times, and so do the ones behind this here
-    stores = cur.nrows == kBM && (cur.nt + 1) * (Epi::gate ? 128 : kBN) <= epi.columns();
+    stores = cur.nrows == kBM && (cur.nt + 1) * (Epi::gate ? 128 : kBN) <= epi.columns(cur.e);
     wait_lds();
     cur = next;
   }
@@ -1037,6 +1059,7 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
   const uint32_t mine = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds + w * kMine;
   const uint8_t* my = lds + w * kMine;
   const int NT = (p.n + kCols - 1) / kCols, MT = (p.m + kST - 1) / kST;
+  const int NT2 = (p.also.n + kST - 1) / kST, MT2 = (p.also.m + kST - 1) / kST;    // kOuter
   // chunk c of row r at c ^ (r / 2 & 7); where k is slow, of 128 bytes of a k at c ^ 4 (k / 2 & 1)
   auto chunk_k = [&](int j) { return (l & 7) ^ (((j & 1) << 2) + (l >> 4)); };
   const int chunk_n = (l & 7) ^ (((l >> 4) & 1) << 2);
@@ -1061,20 +1084,29 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
   const bool blocks = p.rows.count && !p.rows.offset;
   for (; tile <= kLastTile; tile += G) {
-    int e, nt, nrows, row0, slot0, k_a, k_b, KT;
+    int e, nt, nrows, row0, slot0, k_a, k_b, KT, n = p.n;
+    int64_t a_row = p.a_row, b_row = p.b_row;
     const uint8_t *a0, *b0;
     if constexpr (KIND == kOuter) {
-      if (tile >= p.rows.E * MT * NT) break;
-      e = tile / (MT * NT);
-      const int r = tile - e * MT * NT;
-      row0 = r / NT * kST;
-      nt = r % NT;
-      nrows = min(kST, p.m - row0);
-      k_a = k_b = uniform(p.rows.rows_of(e));
+      const int before = p.rows.E * MT * NT;
+      if (tile >= before + p.rows.E * MT2 * NT2) break;
+      const bool first = tile < before;
+      const int nts = first ? NT : NT2, per = first ? MT * NT : MT2 * NT2;
+      if (!first) {
+        a_row = p.also.a_row;
+        b_row = p.also.b_row;
+        n = p.also.n;
+      }
+      const int at = first ? tile : tile - before, of = at / per, r = at - of * per;
+      e = first ? of : of + p.rows.E;
+      row0 = r / nts * kST;
+      nt = r % nts;
+      nrows = min(kST, (first ? p.m : p.also.m) - row0);
+      k_a = k_b = uniform(p.rows.rows_of(of));
       KT = (k_a + 63) / 64;
-      slot0 = uniform(p.rows.first_slot(e));
-      a0 = p.a + (int64_t)slot0 * p.a_row + (int64_t)row0 * 2;
-      b0 = p.b + (int64_t)slot0 * p.b_row + (int64_t)nt * kST * 2;
+      slot0 = uniform(p.rows.first_slot(of));
+      a0 = (first ? p.a : p.also.a) + (int64_t)slot0 * a_row + (int64_t)row0 * 2;
+      b0 = (first ? p.b : p.also.b) + (int64_t)slot0 * b_row + (int64_t)nt * kST * 2;
     } else {
       Found x;
       if (!find_rows(p.rows, kST, tile / NT, x)) break;
@@ -1093,22 +1125,22 @@ __global__ __launch_bounds__(256) void small_kernel(Product p, Epi epi) {
       KT = (p.k + 127) / 128;
       __syncthreads();
     }
-    const int64_t step_a = kSlowA ? 64 * p.a_row : 128, step_b = kSlowB ? 64 * p.b_row : 128;
+    const int64_t step_a = kSlowA ? 64 * a_row : 128, step_b = kSlowB ? 64 * b_row : 128;
     int off_a[8], off_b[8];
-    const bool in_a = chunk_n * 8 < nrows, in_b = nt * kST + chunk_n * 8 < p.n;
+    const bool in_a = chunk_n * 8 < nrows, in_b = nt * kST + chunk_n * 8 < n;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       if constexpr (kSlowA) {
-        off_a[j] = in_a ? (j * 8 + (l >> 3)) * (int)p.a_row + chunk_n * 16 : kAbsent;
+        off_a[j] = in_a ? (j * 8 + (l >> 3)) * (int)a_row + chunk_n * 16 : kAbsent;
       } else {
         const int s = slots[j * 8 + (l >> 3)];
-        off_a[j] = s >= 0 ? (int)((s - slot0) * p.a_row) + chunk_k(j) * 16 : kAbsent;
+        off_a[j] = s >= 0 ? (int)((s - slot0) * a_row) + chunk_k(j) * 16 : kAbsent;
       }
       if constexpr (kSlowB) {
-        off_b[j] = in_b ? (j * 8 + (l >> 3)) * (int)p.b_row + chunk_n * 16 : kAbsent;
+        off_b[j] = in_b ? (j * 8 + (l >> 3)) * (int)b_row + chunk_n * 16 : kAbsent;
       } else {
         const int r = (Epi::gate ? j & 3 : j) * 8 + (l >> 3);
-        off_b[j] = nt * kCols + r < p.n ? r * (int)p.b_row + chunk_k(j) * 16 : kAbsent;
+        off_b[j] = nt * kCols + r < n ? r * (int)b_row + chunk_k(j) * 16 : kAbsent;
       }
     }
     const int64_t far = (int64_t)p.far * p.b_row;
@@ -1244,8 +1276,7 @@ int launch_few(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t 
 }
 
 template <int KIND, class Epi, bool I8>
-int launch_small(const Product& p, const Epi& epi, int64_t row_tiles, hipStream_t st) {
-  const int64_t tiles = row_tiles * ceil_div(p.n, Epi::gate ? kST / 2 : kST);
+int launch_small(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st) {
   EP_LOG("  small tiles: up to %lld", (long long)tiles);
   small_kernel<KIND, Epi, I8><<<dim3((int)(tiles < 256 ? tiles : 256)), dim3(256), 0, st>>>(p, epi);
   return check_launch("ep_ffn small product");
@@ -1273,7 +1304,8 @@ int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
                              ceil_div(p.n, wide);
   if (std::min(few_us, small) < wide_us(wide_tiles, steps, rows, p.n)) {
     if (small < few_us)
-      return launch_small<kRowsT, Epi, I8>(p, epi, row_tiles(p.rows, max_rows, kST), st);
+      return launch_small<kRowsT, Epi, I8>(
+          p, epi, row_tiles(p.rows, max_rows, kST) * ceil_div(p.n, Epi::gate ? kST / 2 : kST), st);
     if (few == 16) return launch_few<Epi, I8, 1, false>(p, epi, row_tiles(p.rows, max_rows, 16), st);
     return launch_few<Epi, I8, 2, false>(p, epi, row_tiles(p.rows, max_rows, 32), st);
   }
@@ -1281,26 +1313,31 @@ int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
                                  st);
 }
 
-// A gradient.  Measured, small tiles against wide ones: 12 experts of 88 rows, 1000 x 344: dh
-// 13 : 39, dx 16 : 20, dw13 33 : 15; one matrix of 1024 rows, 2048 x 1024, all four 88 : 149; 8
-// experts of 512 rows, 1024 x 1024, all four 187 : 126.
+// A gradient, or the two of the weights in one launch.  Measured, small tiles against wide ones: 12
+// experts of 88 rows, 1000 x 344: dh 13 : 39, dx 16 : 20, dw13 33 : 15; one matrix of 1024 rows,
+// 2048 x 1024, all four 88 : 149; 8 experts of 512 rows, 1024 x 1024, all four 187 : 126.
 template <int KIND, class Epi>
 int run_grad(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E;
   const double rows = (double)max_rows / E;
-  const int64_t steps = KIND == kOuter ? (int64_t)(rows / 64) + 1 : ceil_div(p.k, 128);
-  const double small_tiles = KIND == kOuter ? (double)E * ceil_div(p.m, kST)
-                                            : row_tiles_mean(E, rows, kST);
-  const int64_t wide_rows = KIND == kOuter ? ceil_div(p.m, kBM)
-                                           : std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5));
-  const double weight = KIND == kOuter ? 0 : (double)E * p.n * p.k;
-  if (small_us(small_tiles * ceil_div(p.n, kST), steps, weight) <
-      wide_us(E * wide_rows * ceil_div(p.n, kBN), steps, KIND == kOuter ? kBM : rows, p.n))
-    return launch_small<KIND, Epi, false>(
-        p, epi, KIND == kOuter ? E * ceil_div(p.m, kST) : row_tiles(p.rows, max_rows, kST), st);
-  return launch<KIND, Epi, false>(
-      p, epi, (KIND == kOuter ? E * ceil_div(p.m, kBM) : row_tiles(p.rows, max_rows, kBM)) *
-                  ceil_div(p.n, kBN), st);
+  if constexpr (KIND == kOuter) {
+    auto tiles = [&](int t) {
+      return E * (ceil_div(p.m, t) * ceil_div(p.n, t) + ceil_div(p.also.m, t) * ceil_div(p.also.n, t));
+    };
+    const int64_t steps = (int64_t)(rows / 64) + 1;
+    if (small_us((double)tiles(kST), steps, 0) < wide_us(tiles(kBM), steps, kBM, p.n))
+      return launch_small<KIND, Epi, false>(p, epi, tiles(kST), st);
+    return launch<KIND, Epi, false>(p, epi, tiles(kBM), st);
+  } else {
+    const int64_t steps = ceil_div(p.k, 128),
+                  wide_rows = std::max<int64_t>(1, (int64_t)(rows / kBM + 0.5));
+    if (small_us(row_tiles_mean(E, rows, kST) * ceil_div(p.n, kST), steps, (double)E * p.n * p.k) <
+        wide_us(E * wide_rows * ceil_div(p.n, kBN), steps, rows, p.n))
+      return launch_small<KIND, Epi, false>(
+          p, epi, row_tiles(p.rows, max_rows, kST) * ceil_div(p.n, kST), st);
+    return launch<KIND, Epi, false>(p, epi,
+                                    row_tiles(p.rows, max_rows, kBM) * ceil_div(p.n, kBN), st);
+  }
 }
 
 // Whether every workgroup rounds x to integers by itself.
@@ -1431,7 +1468,7 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
     for (const auto& i : in)
       if (overlap(o.p, o.n, i.p, i.n)) return EP_ERR_INVALID_ARG;
   if (!few_enough(r, std::max(H, 2 * I)) ||
-      r.E * ceil_div(std::max(H, 2 * I), kST) * ceil_div(std::max(H, I), kST) > INT32_MAX)
+      r.E * (ceil_div(2 * I, kST) + ceil_div(I, kST)) * ceil_div(H, kST) > kLastTile)
     return EP_ERR_INVALID_ARG;
   const bool any = rows->max_rows > 0;
   if (!a->w13 || !a->w2 || !a->dw13 || !a->dw2 || !aligned(a->workspace, 256) ||
@@ -1476,17 +1513,9 @@ int ep_ffn_backward(const ep_rows_t* rows, const ep_ffn_grad_args_t* a, void* st
   p.b_row = 2 * H;
   p.m = 2 * I;
   p.n = H;
-  const StoreMatrix w13{(uint16_t*)a->dw13, 2 * I, H};
-  rc = run_grad<kOuter>(p, w13, rows->max_rows, st);
-  if (rc != EP_OK) return rc;
-  p.a = (const uint8_t*)a->dy;
-  p.b = h;
-  p.a_row = 2 * H;
-  p.b_row = 2 * I;
-  p.m = H;
-  p.n = I;
-  const StoreMatrix w2{(uint16_t*)a->dw2, H, I};
-  return run_grad<kOuter>(p, w2, rows->max_rows, st);
+  p.also = Outer{(const uint8_t*)a->dy, h, 2 * H, 2 * I, H, I};
+  const StoreMatrix out_w{(uint16_t*)a->dw13, (uint16_t*)a->dw2, r.E, 2 * I, H, H, I};
+  return run_grad<kOuter>(p, out_w, rows->max_rows, st);
 }
 
 int64_t ep_integer_workspace_bytes(const ep_rows_t* rows, int32_t cols) {
