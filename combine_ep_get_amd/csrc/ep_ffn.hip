@@ -353,6 +353,228 @@ __device__ __forceinline__ u32x4 fragment(const uint8_t* half, int lane_off, int
   }
 }
 
+// The scales of 8-bit products for store_block, of N times 64 rows, 128 apart: all at once.  Loaded
+// where each block needs them, one latency after the other made a tile's epilogue 22 us long
+// instead of 8.
+template <int N, class Epi, class RowAt>
+__device__ __forceinline__ void load_scales(const Epi& epi, int e, int r0, int nrows, int c0, int v,
+                                            RowAt row_at, float (&row)[N][2], f32x4 (&col)[2][4]) {
+#pragma unroll
+  for (int i = 0; i < 2 * N; i++) {
+    const int r = r0 + (i >> 1) * 128 + (i & 1) * 32 + (v & 31);
+    row[i >> 1][i & 1] = r < nrows ? epi.sx[row_at(r)] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    col[i >> 2][i & 3] = epi.scales(e, c0 + 8 * (i & 3) + 4 * (v >> 5), i >> 2);
+#pragma unroll
+  for (int i = 0; i < 8; i++) arrive(col[i >> 2][i & 3]);
+#pragma unroll
+  for (int i = 0; i < 2 * N; i++) arrive(row[i >> 1][i & 1]);
+}
+
+// A wavefront's 64 rows (from r0 on, of nrows) by 32 columns of either half (from c0 on): blocks
+// of 32 by 32, rounded to bf16, through 2 KiB of its own LDS at mine0 and at mine1, where a
+// lane's four columns of a row become eight of another: stores of 64 bytes of a row.  Two
+// blocks are under way.
+template <class Epi, bool I8, class RowAt>
+__device__ __forceinline__ void store_block(const Epi& epi, int e, int r0, int nrows, int c0,
+                                            const typename Acc<I8>::type (&acc)[2][2],
+                                            const float (&row_scale)[2], const f32x4 (&scales)[2][4],
+                                            uint8_t* mine0, uint8_t* mine1, int v, RowAt row_at) {
+  auto turn16 = [&](const f32x16& x, uint8_t* mine) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      *(u32x2*)(mine + (v & 31) * 64 + ((i ^ ((v >> 2) & 3)) << 4) + (v >> 5) * 8) =
+          u32x2{pack2(x[i * 4], x[i * 4 + 1]), pack2(x[i * 4 + 2], x[i * 4 + 3])};
+  };
+#pragma unroll
+  for (int mb = 0; mb < 2; mb++) {
+    const int first = r0 + mb * 32;
+    if (first >= nrows) continue;
+    auto values = [&](int half) {
+      f32x16 x;
+      if constexpr (I8) {
+#pragma unroll
+        for (int j = 0; j < 16; j++)
+          x[j] = (float)acc[half][mb][j] * row_scale[mb] * scales[half][j >> 2][j & 3];
+      } else {
+        x = acc[half][mb];
+      }
+      return x;
+    };
+    auto put = [&](const uint8_t* mine, int what) {
+      u32x4 q[2];
+#pragma unroll
+      for (int it = 0; it < 2; it++)
+        q[it] = *(const u32x4*)(mine + it * 1024 + (v >> 2) * 64 +
+                                (((v & 3) ^ ((v >> 4) & 3)) << 4));
+#pragma unroll
+      for (int it = 0; it < 2; it++) {
+        const int r = first + it * 16 + (v >> 2);
+        if (r < nrows) epi.put(e, row_at(r), c0 + (v & 3) * 8, q[it], what);
+      }
+    };
+    const f32x16 a = values(0), b = values(1);
+    if constexpr (Epi::gate) {
+      f32x16 x;
+#pragma unroll
+      for (int j = 0; j < 16; j++) x[j] = a[j] * sigmoid(a[j]) * b[j];
+      turn16(x, mine0);
+      put(mine0, 0);
+      if (epi.gu) {
+        turn16(a, mine0);
+        turn16(b, mine1);
+        put(mine0, 1);
+        put(mine1, 2);
+      }
+    } else {
+      turn16(a, mine0);
+      turn16(b, mine1);
+      put(mine0, 0);
+      put(mine1, 128);
+    }
+  }
+}
+
+// Tiles of at most 128 rows by a weight's rows, which come from HBM: 48 KiB a step, three stages
+// in LDS and all wavefronts in the same phase, so that two whole steps (96 KiB per CU) are on
+// their way where the wide tiles' loop has one.  A workgroup takes them after its wide ones,
+// from tile `tile` on; those before `wide` are wide.  Both products for 32 experts of 64 rows,
+// 7168 x 2048: 495 us, with the wide tiles' loop 533; of 128 rows 546 : 582; of 64 in 8 bits 289 : 319.
+constexpr int kStreamM = 128, kStream = 3 * kHalf;      // rows; bytes of a stage
+
+template <class Epi, bool I8>
+__device__ __forceinline__ void stream(const Product& p, const Epi& epi, uint8_t* lds,
+                                       const Experts& experts, int tile, int wide, int total) {
+  using acc_t = typename Acc<I8>::type;
+  constexpr int kCols = Epi::gate ? 128 : kBN;
+  const int tid = threadIdx.x, l = tid & 63, w = uniform(tid >> 6);
+  const int wm = w >> 2, wn = w & 3;     // rows wm*64.., columns wn*32.. of each half
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(EP_LDS uint8_t*)lds;
+  const int NT = (p.n + kCols - 1) / kCols, G = gridDim.x;
+  const bool blocks = p.rows.count && !p.rows.offset;
+  auto chunk_k = [&](int j) { return (l & 7) ^ ((j << 2) + (l >> 4)); };
+  const int read_k = (l & 31) * 128 + (((l >> 5) ^ ((l >> 1) & 7)) << 4);
+  const int read_a = wm * 64 * 128 + read_k, read_b = kHalf + wn * 32 * 128 + read_k;
+
+  struct Tile {
+    int e, nt, nrows, row0, slot0;
+  };
+  const uint8_t *a0 = nullptr, *b0 = nullptr;
+  int left = 0;                          // contraction of what is loaded
+  int off_a[2], off_b[2][2];
+  const int64_t far = Epi::gate ? (int64_t)p.far * p.b_row : 0;
+  const int KT = max(2, (p.k + 127) / 128);
+
+  // step t, whose last bytes may be behind the contraction's end
+  auto load = [&](int t, int stage) {
+    int a[2], b[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const bool in = chunk_k(j) * 16 < left - t * 128;
+      a[j] = in ? off_a[j] : kAbsent;
+      b[0][j] = in ? off_b[0][j] : kAbsent;
+      b[1][j] = in ? off_b[1][j] : kAbsent;
+    }
+    const uint32_t to = lds0 + stage * kStream + w * 2048;
+    const uint8_t* from = b0 + (int64_t)t * 128;
+    load_lds2<true>(to + kHalf, b[0][0], b[0][1], descriptor(from));
+    load_lds2<true>(to + 2 * kHalf, b[1][0], b[1][1], descriptor(from + far));
+    load_lds2<false>(to, a[0], a[1], descriptor(a0 + (int64_t)t * 128));
+  };
+  // Finds tile `tile` and turns the loads to it; behind the last one they load zeros.
+  auto locate = [&](int tile, Tile& x) {
+    left = 0;
+    if (tile >= total) return;
+    const int at = (tile - wide) / NT;
+    x.e = find_expert(experts.first_short, p.rows.E, at);
+    x.nt = tile - wide - at * NT;
+    x.row0 = (uniform(experts.first[x.e + 1]) - uniform(experts.first[x.e])) * kBM;
+    x.nrows = uniform(experts.count[x.e]) - x.row0;
+    x.slot0 = uniform(experts.slot[x.e]) + (blocks ? 0 : x.row0);
+    a0 = p.a + (int64_t)x.slot0 * p.a_row;
+    b0 = p.b + (int64_t)x.e * p.b_expert + (int64_t)x.nt * kCols * p.b_row;
+    left = p.k;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const int r = w * 16 + j * 8 + (l >> 3), c = chunk_k(j) * 16;
+      int s = r;                         // slots behind slot0
+      if (blocks && s < x.nrows) s = p.rows.slot(x.e, x.row0 + s) - x.slot0;
+      off_a[j] = r < x.nrows ? s * (int)p.a_row + c : kAbsent;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int col = Epi::gate ? r : h * 128 + r;
+        off_b[h][j] = x.nt * kCols + col < p.n ? col * (int)p.b_row + c : kAbsent;
+      }
+    }
+  };
+
+  Tile cur, next;
+  locate(tile, cur);
+  next = cur;
+  load(0, 0);
+  load(1, 1);
+  int stage = 0, ahead = 2;
+  bool stores = false;         // the last epilogue surely sent kStores of them
+  constexpr int kStores = Epi::stores / 2;
+  for (;;) {
+    acc_t acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[i >> 1][i & 1] = acc_t{};
+    const bool any = wm * 64 < cur.nrows;
+    for (int t = 0; t < KT; t++) {
+      // this step's loads have arrived and the last one's stage is read by all: it is loaded
+      // again.  Behind an epilogue its stores stay under way for two steps.
+      if (t < 2 && stores) wait_loads<6 + kStores>();
+      else wait_loads<6>();
+      barrier();
+      if (t == KT - 2) locate(tile + G, next);
+      load(t + 2 < KT ? t + 2 : t + 2 - KT, ahead);
+      if (any) {
+        const uint8_t* st = lds + stage * kStream;
+        u32x4 fa[2][4], fb[2][4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            fa[i][ks] = fragment<false>(st + i * 4096, read_a, ks);
+            fb[i][ks] = fragment<false>(st + i * kHalf, read_b, ks);
+          }
+        wait_lds();
+#pragma unroll
+        for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            acc[i >> 1][i & 1] = mfma<I8>(fb[i >> 1][ks], fa[i & 1][ks], acc[i >> 1][i & 1]);
+      }
+      stage = stage == 2 ? 0 : stage + 1;
+      ahead = ahead == 2 ? 0 : ahead + 1;
+    }
+    // ---- results, through the stage that was read last, each wavefront where its own next
+    // loads go
+    barrier();
+    uint8_t* const mine0 = lds + ahead * kStream + w * 2048;
+    uint8_t* const mine1 = mine0 + kHalf;
+    auto row_at = [&](int r) {
+      return blocks ? p.rows.slot(cur.e, cur.row0 + r) : cur.slot0 + r;
+    };
+    const int c0 = cur.nt * kCols + wn * 32;
+    float row_scale[1][2];
+    f32x4 scales[2][4];
+    if constexpr (I8)
+      load_scales(epi, cur.e, wm * 64, cur.nrows, c0, l, row_at, row_scale, scales);
+    store_block<Epi, I8>(epi, cur.e, wm * 64, cur.nrows, c0, acc, row_scale[0], scales, mine0, mine1, l,
+                         row_at);
+    tile += G;
+    if (tile >= total) break;
+    stores = cur.nrows == kStreamM && (cur.nt + 1) * kCols <= epi.columns(cur.e);
+    wait_lds();
+    cur = next;
+  }
+  wait_loads<0>();             // zeros behind the last tile
+}
+
 template <int KIND, class Epi, bool I8>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void product_kernel(Product p, Epi epi) {
@@ -376,7 +598,7 @@ void product_kernel(Product p, Epi epi) {
   // dh, 264 tall and 48 short tiles, 392 us without halves, 355 with them.
   const int G = gridDim.x;
   const int NT2 = (p.also.n + kBN - 1) / kBN, MT2 = (p.also.m + kBM - 1) / kBM;
-  int total = p.rows.E * (MT * NT + MT2 * NT2), tall = 0, halved = 0;
+  int total = p.rows.E * (MT * NT + MT2 * NT2), tall = 0, halved = 0, all = 0;
   if constexpr (KIND != kOuter) {
     tall = uniform(experts.first[p.rows.E]) * NT;
     total = tall + uniform(experts.first_short[p.rows.E]) * NT;
@@ -386,6 +608,8 @@ void product_kernel(Product p, Epi epi) {
       halved = rest;
       total += rest;
     }
+    all = total;
+    if constexpr (KIND == kRowsT) total = tall + halved;   // the short ones: stream()
   }
 
   // where this lane's bytes of a load go (a wavefront sends two loads per half: rows
@@ -481,7 +705,7 @@ void product_kernel(Product p, Epi epi) {
     } else {
       // the short ones last: they take half the time, and a workgroup whose share was all
       // tall ones would keep the others waiting
-      const bool is_short = tile >= tall + halved;
+      const bool is_short = KIND != kRowsT && tile >= tall + halved;
       const int half = tile - (tall - halved);               // of a halved one
       const int at = is_short ? tile - (tall + halved) : half >= 0 ? tall - halved + half / 2 : tile;
       x.e = is_short ? find_expert(experts.first_short, p.rows.E, at / NT)
@@ -540,7 +764,14 @@ void product_kernel(Product p, Epi epi) {
 
   // workgroup ids go round robin over the 8 XCDs: give each XCD neighbouring tiles
   int tile = G % 8 == 0 ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
-  if (tile >= total) return;
+  if constexpr (KIND == kRowsT) {
+    if (tile >= total) {
+      if (tile < all) stream<Epi, I8>(p, epi, lds, experts, tile, total, all);
+      return;
+    }
+  } else if (tile >= total) {
+    return;
+  }
   Tile cur, next;
   locate(tile, cur);
   next = cur;
@@ -642,9 +873,8 @@ void product_kernel(Product p, Epi epi) {
     }
 
     // ---- this tile's results are in registers, the next one's first loads under way.
-    // Blocks of 32 by 32 through LDS, where a lane's four columns of a row become eight
-    // of another: stores of 64 bytes of a row.  The first 16 rows lie where this
-    // wavefront's own next load goes, so that no other one is waited for.
+    // They go through LDS: half of it where this wavefront's own next load goes, so that
+    // no other one is waited for.
     uint8_t* const mine0 = lds + (stage ^ 1) * kStage + kHalf + w * 2048;
     uint8_t* const mine1 = lds + kSteps * kStage + w * 2048;
     // this lane as a value of its own: what follows from it is computed here, not before
@@ -654,6 +884,7 @@ void product_kernel(Product p, Epi epi) {
     const int swizzle = (v >> 1) & 7;        // of row v % 32, that is v % 16
     uint8_t* const to_row = (v & 16 ? mine1 : mine0) + (v & 15) * 128;
     const int take_at = (v >> 2) * 128, take_swizzle = (v >> 3) & 7;
+    // blocks in 32 bits, for an epilogue that does not round first
     auto turn = [&](const acc_t& x) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
@@ -673,94 +904,21 @@ void product_kernel(Product p, Epi epi) {
         for (int j = 0; j < 4; j++) to[q * 4 + j] = __builtin_bit_cast(val_t, (uint32_t)x[j]);
       }
     };
-    // the same for values that are rounded to bf16 already: half the bytes, so that two
-    // blocks can be under way
-    auto turn16 = [&](const f32x16& x, uint8_t* mine) {
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        *(u32x2*)(mine + (v & 31) * 64 + ((i ^ ((v >> 2) & 3)) << 4) + (v >> 5) * 8) =
-            u32x2{pack2(x[i * 4], x[i * 4 + 1]), pack2(x[i * 4 + 2], x[i * 4 + 3])};
-    };
-    auto take16 = [&](int it, const uint8_t* mine) {
-      return *(const u32x4*)(mine + it * 1024 + (v >> 2) * 64 +
-                             (((v & 3) ^ ((v >> 4) & 3)) << 4));
-    };
     auto row_at = [&](int r) {
       return KIND == kOuter ? cur.row0 + r
              : blocks       ? p.rows.slot(cur.e, cur.row0 + r)
                             : cur.slot0 + r;
     };
-    const int c0 = cur.nt * (Epi::gate ? 128 : kBN) + wn * 32 + (v & 3) * 8;
-    // all scales of 8-bit products at once: loaded where each block needs them, one latency
-    // after the other made a tile's epilogue 22 us long instead of 8
-    float row_scale[4];
-    f32x4 scales[2][4];
-    if constexpr (I8) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int r = (i >> 1) * 128 + wm * 64 + (i & 1) * 32 + (v & 31);
-        row_scale[i] = r < cur.nrows ? epi.sx[row_at(r)] : 0.f;
-      }
-#pragma unroll
-      for (int half = 0; half < 2; half++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          scales[half][i] = epi.scales(cur.e, cur.nt * (Epi::gate ? 128 : kBN) + wn * 32 +
-                                                  8 * i + 4 * (v >> 5), half);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        arrive(row_scale[i]);
-        arrive(scales[0][i]);
-        arrive(scales[1][i]);
-      }
-    }
+    const int c00 = cur.nt * (Epi::gate ? 128 : kBN) + wn * 32, c0 = c00 + (v & 3) * 8;
     if constexpr (Epi::rounds) {
+      float row_scale[2][2];
+      f32x4 scales[2][4];
+      if constexpr (I8)
+        load_scales(epi, cur.e, wm * 64, cur.nrows, c00, v, row_at, row_scale, scales);
 #pragma unroll
       for (int h = 0; h < 2; h++)
-#pragma unroll
-        for (int mb = 0; mb < 2; mb++) {
-          const int r0 = h * 128 + wm * 64 + mb * 32;
-          if (r0 >= cur.nrows) continue;
-          // what is turned is stored by epi.put (a gate: h, and g and u where asked for)
-          auto values = [&](int half) {
-            f32x16 x;
-            if constexpr (I8) {
-#pragma unroll
-              for (int j = 0; j < 16; j++)
-                x[j] = (float)acc[h][half][mb][j] * row_scale[h * 2 + mb] * scales[half][j >> 2][j & 3];
-            } else {
-              x = acc[h][half][mb];
-            }
-            return x;
-          };
-          auto put = [&](const uint8_t* mine, int what) {
-            const u32x4 q[2] = {take16(0, mine), take16(1, mine)};
-#pragma unroll
-            for (int it = 0; it < 2; it++) {
-              const int r = r0 + it * 16 + (v >> 2);
-              if (r < cur.nrows) epi.put(cur.e, row_at(r), c0, q[it], what);
-            }
-          };
-          const f32x16 a = values(0), b = values(1);
-          if constexpr (Epi::gate) {
-            f32x16 x;
-#pragma unroll
-            for (int j = 0; j < 16; j++) x[j] = a[j] * sigmoid(a[j]) * b[j];
-            turn16(x, mine0);
-            put(mine0, 0);
-            if (epi.gu) {
-              turn16(a, mine0);
-              turn16(b, mine1);
-              put(mine0, 1);
-              put(mine1, 2);
-            }
-          } else {
-            turn16(a, mine0);
-            turn16(b, mine1);
-            put(mine0, 0);
-            put(mine1, 128);
-          }
-        }
+        store_block<Epi, I8>(epi, cur.e, h * 128 + wm * 64, cur.nrows, c00, acc[h], row_scale[h],
+                             scales, mine0, mine1, v, row_at);
     } else {
 #pragma unroll
       for (int b = 0; b < 4; b++) {
@@ -803,6 +961,13 @@ void product_kernel(Product p, Epi epi) {
   }
   wait_loads<0>();             // zeros behind the last tile
   if (wm == 0) barrier();
+  if constexpr (KIND == kRowsT) {
+    if (tile < all) {
+      wait_lds();
+      barrier();
+      stream<Epi, I8>(p, epi, lds, experts, tile, total, all);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- few rows
