@@ -18,6 +18,26 @@ MANY = [
 ]
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("H,I", [(272, 144), (128, 64)])     # several steps; the fewest
+def test_tall_tiles_then_short_ones(int8, H, I, monkeypatch):
+    """Row counts around a tile's ends, so many that a workgroup takes both kinds."""
+    counts = torch.tensor([0, 1, 64, 65, 127, 128, 129, 192, 255, 256, 257, 384, 385] * 25)
+    idx = torch.repeat_interleave(torch.arange(len(counts)), counts)
+    idx = idx[torch.randperm(len(idx), generator=torch.Generator().manual_seed(31))]
+    idx = idx.to(torch.int32).view(-1, 1).cuda()
+    monkeypatch.setattr("tests.test_gpu_ffn.routing", lambda *a: idx)
+    c = Case(31, N=len(idx), K=1, E=len(counts), A=1, H=H, I=I, int8=int8)
+    assert [len(s) for _, s in c.where] == counts.tolist()
+    y = ep.expert_ffn(c.x, c.w13, c.w2, layout=c.layout, out=c.full(H))
+    c.untouched(y)
+    c.where = c.where[:26] + c.where[-13:]
+    (check_int8_ffn if int8 else check_ffn)(c, y)
+    for _ in range(3):
+        again = ep.expert_ffn(c.x, c.w13, c.w2, layout=c.layout)
+        assert torch.equal(again[c.at], y[c.at])
+
+
 # on 64-row tiles
 MIDDLE = [
     dict(N=512, K=1, E=0, A=1, H=2048, I=1024),
