@@ -15,12 +15,13 @@
 //   product_kernel  256 by 256 tiles, 8 wavefronts, one workgroup per CU that walks over
 //                   tiles.  A tile's step (128 bytes of the contraction) is 2048 cycles of
 //                   MFMA on each SIMD and 64 KiB of operands, which go straight to LDS two
-//                   steps deep and are read with no bank conflict.  Bound by the MFMAs and,
+//                   steps deep and are read with few bank conflicts.  Bound by the MFMAs and,
 //                   with them, by the card's power: at 8192 rows by 8192 x 4096 in bf16
 //                   1310 TFLOP/s (a large library product: 1260 to 1550 here) and 2050
 //                   TOP/s at 8192^3 int8 (2060 to 2120), at 1.75 GHz with the MFMAs busy 78 %
 //                   of the cycles; without any load they are 82 %, the rest is barriers.
-//                   With few rows per expert it is bound by HBM: 6.8 TB/s of weights.
+//                   Tiles of at most 128 rows have a loop of their own (stream): bound by
+//                   HBM, 6.9 TB/s of weights at 16 rows an expert.
 //   few_kernel      few rows: weights as a stream, the contraction split over wavefronts
 //   small_kernel    what lies between: 64 by 64 tiles on many CUs
 // One workgroup computes a value from one fixed order of sums: the same bits on every run.
@@ -1451,7 +1452,7 @@ int launch_small(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st
 // weight: 1 row by 7168 x 7168 53, 11, -; 16 rows 53, 12, 14; 64 rows 63, 20, 17; 256 rows 68, 66,
 // 41; 980 rows by 861 x 7120 92, 52, 23; 4000 by 4000 x 512 23, 114, 70; 33 by 1237 x 2000 23, 6,
 // 9.  Both products of a bf16 block: 512 rows, 2048 x 1024 64, 35, 25; 2048 rows 67, 124, 80; 32
-// experts of about 16 rows, 7168 x 2048: first 281, 313, second 218, 168.
+// experts of about 16 rows, 7168 x 2048: first 273, 313, second 183, 171.
 template <class Epi, bool I8>
 int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E, wide = Epi::gate ? 128 : kBN;
