@@ -3,6 +3,8 @@
 #include "ep_host.h"
 #include "ep_rows.h"
 
+#include <algorithm>
+
 namespace {
 
 // ---------------------------------------------------------------- 8-bit integers
@@ -57,6 +59,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t*
 
 // ---------------------------------------------------------------- combine's gradient
 constexpr int kMostWaves = 16, kPairs = 4;
+// A grid has less than 2^32 threads along an axis (with more, the count wraps and tokens
+// stay undone without an error), 2^22 workgroups of 1024: more tokens take several launches.
+constexpr int kTokensPerLaunch = 1 << 21;
 
 // A workgroup per token and four of its pairs, a thread per 16-byte chunk of the row (or
 // per several): all loads of a chunk are in flight at once, and dy's row is read once
@@ -178,11 +183,17 @@ int ep_combine_backward(const ep_problem_t* p, const void* dy, const void* exper
   EP_LOG("combine_backward N=%d H=%d K=%d cap=%lld", N, H, p->num_topk, (long long)recv_capacity);
   const int K = p->num_topk, q = (H / 8 + 63) / 64;
   const int passes = (q + kMostWaves - 1) / kMostWaves, waves = (q + passes - 1) / passes;
-  combine_backward_kernel<<<dim3(N, (K + kPairs - 1) / kPairs), dim3(64 * waves), 0,
-                            (hipStream_t)stream>>>(
-      (const u32x4*)dy, (const u32x4*)expert_out, slot_of, topk_weights, (u32x4*)d_expert_out,
-      d_topk_weights, H / 8, K, (int)recv_capacity);
-  return check_launch("combine_backward");
+  for (int64_t t = 0; t < N; t += kTokensPerLaunch) {
+    const int n = (int)std::min<int64_t>(N - t, kTokensPerLaunch);
+    combine_backward_kernel<<<dim3(n, (K + kPairs - 1) / kPairs), dim3(64 * waves), 0,
+                              (hipStream_t)stream>>>(
+        (const u32x4*)dy + t * (H / 8), (const u32x4*)expert_out, slot_of + t * K,
+        topk_weights + t * K, (u32x4*)d_expert_out, d_topk_weights + t * K, H / 8, K,
+        (int)recv_capacity);
+    rc = check_launch("combine_backward");
+    if (rc != EP_OK) return rc;
+  }
+  return EP_OK;
 }
 
 }  // extern "C"
