@@ -14,10 +14,14 @@ struct Rows {            // kernel argument
   int E, R, M;           // R sub-blocks of M rows per expert where there are no offsets
   int plain;             // rows of the one expert where there are no counts either
 
-  // Rows of expert e; counts and offsets are cut off where they leave the buffer.
+  // Rows of expert e: its region's, cut off at the ends of the buffer.  Of one that starts
+  // before the buffer the first rows are lost, not the last.
   __device__ __forceinline__ int rows_of(int e) const {
     if (!count) return plain;
-    if (offset) return max(0, min(count[e], cap - first_slot(e)));
+    if (offset) {
+      const int64_t end = min((int64_t)offset[e] + count[e], (int64_t)cap);
+      return (int)max((int64_t)0, end - first_slot(e));
+    }
     int n = 0;
     for (int s = 0; s < R; s++) n += max(0, min(count[e * R + s], M));
     return n;
