@@ -91,7 +91,7 @@ struct Found {
     const int e = base + l;
     const int n = e < rows.E ? rows.rows_of(e) : 0;
     const int slot = e < rows.E ? rows.base_slot(e, 0) : 0;
-    const int tiles = (n + tile - 1) / tile;
+    const int tiles = n / tile + (n % tile != 0);          // n may be all that an int holds
     int sum = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
