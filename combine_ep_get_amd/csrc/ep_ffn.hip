@@ -158,6 +158,21 @@ __device__ __forceinline__ f32x4 load4(const float* p, int c, int n) {
   return r;
 }
 
+// A sum of codes (at most 2^30) times a row's scale and a column's.  The first product would
+// pass float32's range with scales of 2^96 on (rows near bf16's largest) though the result need
+// not: those are taken 2^64 times smaller and the result larger again, both exact.
+struct RowFactor {
+  float s, back;
+  __device__ __forceinline__ explicit RowFactor(float scale) {
+    const bool large = fabsf(scale) >= 0x1p96f;
+    s = large ? scale * 0x1p-64f : scale;
+    back = large ? 0x1p64f : 1.f;
+  }
+  __device__ __forceinline__ float operator()(int sum, float column) const {
+    return (float)sum * s * column * back;
+  }
+};
+
 // What becomes of eight neighbouring columns of a row of D; put: of eight that are rounded
 // to bf16 already (bf16 products, where that comes first, with n % 8 == 0).  `slot` is the row's slot
 // (kOuter: its row of the expert's matrix), `e` the expert, `c` the first column.
@@ -196,10 +211,10 @@ struct StoreRows {
     if (c >= n) return;
     float f[8];
     if constexpr (std::is_same_v<T, int>) {
-      const float s = sx[slot];
+      const RowFactor row(sx[slot]);
       const f32x4 w[2] = {scales(e, c, 0), scales(e, c + 4, 0)};
 #pragma unroll
-      for (int i = 0; i < 8; i++) f[i] = (float)v[i] * s * w[i >> 2][i & 3];
+      for (int i = 0; i < 8; i++) f[i] = row(v[i], w[i >> 2][i & 3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++) f[i] = v[i];
@@ -251,12 +266,12 @@ struct StoreGate {
     if (c >= inter) return;
     float a[8], b[8], r[8];
     if constexpr (std::is_same_v<T, int>) {
-      const float s = sx[slot];
+      const RowFactor row(sx[slot]);
       const float* w = sw + (int64_t)e * 2 * inter + c;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        a[i] = (float)g[i] * s * w[i];
-        b[i] = (float)u[i] * s * w[inter + i];
+        a[i] = row(g[i], w[i]);
+        b[i] = row(u[i], w[inter + i]);
       }
     } else {
 #pragma unroll
@@ -396,9 +411,9 @@ __device__ __forceinline__ void store_block(const Epi& epi, int e, int r0, int n
     auto values = [&](int half) {
       f32x16 x;
       if constexpr (I8) {
+        const RowFactor row(row_scale[mb]);
 #pragma unroll
-        for (int j = 0; j < 16; j++)
-          x[j] = (float)acc[half][mb][j] * row_scale[mb] * scales[half][j >> 2][j & 3];
+        for (int j = 0; j < 16; j++) x[j] = row(acc[half][mb][j], scales[half][j >> 2][j & 3]);
       } else {
         x = acc[half][mb];
       }
