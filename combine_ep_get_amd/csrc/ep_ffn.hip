@@ -149,9 +149,11 @@ __device__ __forceinline__ void arrive(f32x4& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void arrive(u32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---------------------------------------------------------------- epilogues
-// Four values from p[c] on, of n (those behind the last are the last again).
+// Four values from p[c] on, of n (those behind the last are the last again).  Scales are
+// aligned to 4 bytes only, which is enough for a load of 16.
+typedef float f32x4_at_4 __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ f32x4 load4(const float* p, int c, int n) {
-  if ((n & 3) == 0) return *(const f32x4*)(p + min(c, n - 4));
+  if ((n & 3) == 0) return *(const f32x4_at_4*)(p + min(c, n - 4));
   f32x4 r;
 #pragma unroll
   for (int j = 0; j < 4; j++) r[j] = p[min(c + j, n - 1)];

@@ -53,3 +53,25 @@ def test_largest_rows_of_a_block(N, H, I):
     assert 1e-3 < float(want[0].abs().max()) < 1e6
     ref.check(gu, want, ONCE * want.abs(), "gate_up")
     assert bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("N", [3, 40, 700, 4096])
+def test_scales_at_any_float(N, off):
+    """Scales that start at any multiple of 4 bytes, of an even and of an odd width."""
+    g = gen(63)
+
+    def moved(w):
+        s = torch.empty((w.scales.numel() + off,), device="cuda")[off:].view(w.scales.shape)
+        assert s.data_ptr() % 16 == 4 * off
+        return ep.Int8Weight(w.codes, s.copy_(w.scales))
+
+    for O in (512, 333):
+        w, x = weight(g, O, 1024, 1e-2), normal(g, N, 1024)
+        assert torch.equal(ep.int8_linear(x, moved(w)), ep.int8_linear(x, w))
+    w13, w2 = weight(g, 1056, 1024, 1e-3), weight(g, 1024, 528, 1e-3)
+    assert torch.equal(ep.expert_ffn(x, moved(w13), moved(w2)), ep.expert_ffn(x, w13, w2))
+    codes, scales = ep.quantize_int8(x)
+    s = torch.empty((N + off,), device="cuda")[off:]
+    assert torch.equal(ep.int8_linear(codes, w13, x_scales=s.copy_(scales)),
+                       ep.int8_linear(codes, w13, x_scales=scales))
