@@ -451,7 +451,18 @@ int ep_quant_linear(int32_t num_rows, int32_t cols, int32_t out_rows, const void
  *                    launch shapes; more rows than that are computed just the same,
  *                    except that 0 launches nothing
  * Counts and offsets come from the device as they are: what reaches outside of
- * [0, capacity) (or of M) is cut off there. */
+ * [0, capacity) (or of M) is cut off there.
+ * Tiles, and offsets inside an expert's sub-blocks, are counted in 32 bits, also
+ * where counts that nobody wrote give every expert the whole buffer.  Calls beyond
+ * that return EP_ERR_INVALID_ARG (divisions by 16 and 256 round down, ceil up):
+ *   (capacity/16 + E) * ceil(cols/16)         <= 2^31 - 1
+ *   E*capacity/16 + E                         <= 2^31 - 1
+ *   (E*capacity/256 + E) * ceil(cols/128)     <= 2^31 - 1025
+ *       E = num_experts, cols = max(hidden, 2*inter), out_rows of ep_integer_linear
+ *   E * (ceil(2*inter/64) + ceil(inter/64)) * ceil(hidden/64) <= 2^31 - 1025
+ *       of ep_ffn_backward
+ *   R*M * row bytes < 1.5 GiB, with count alone: 2*max(hidden, inter) bytes of
+ *       ep_ffn, cols of ep_integer_linear */
 typedef struct ep_rows {
   const int32_t* offset;
   const int32_t* count;
