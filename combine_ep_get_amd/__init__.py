@@ -879,10 +879,17 @@ class Int8Weight:
         return self.desc
 
 
+def _int32(sizes, name):
+    """Refuses sizes that the C interface would cut to 32 bits."""
+    if max(sizes) > 2 ** 31 - 1 or min(sizes) < -2 ** 31:
+        raise ValueError(f"{name}: sizes {tuple(sizes)} beyond 32 bits")
+
+
 def _rows(x, layout):
     """ep_rows_t of x's rows as bytes: of a Layout, an LLLayout, or (None) a plain matrix."""
     import torch
     cap = x.shape[0]
+    _int32(x.shape, "x")
     if layout is None:
         return _ROWS(0, 0, cap, 1, 1, 0, cap)
     if cap < layout.capacity:
@@ -917,6 +924,7 @@ def _workspace(workspace, need, ref):
 
 @functools.lru_cache(maxsize=256)
 def _ffn_bytes(rows, hidden, inter, int8, backward):
+    _int32((rows, hidden, inter), "workspace")
     # its size depends on the rows of the buffers alone
     return int(lib().ep_ffn_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), hidden, inter,
                                             EP_WEIGHT_INT8 if int8 else EP_WEIGHT_BF16,
@@ -1052,6 +1060,7 @@ def quantize_int8(x, out=None):
     scale = amax / 127 (see ep_quantize_rows)."""
     import torch
     rows, cols = x.shape
+    _int32(x.shape, "x")
     _arg(x, torch.bfloat16, (rows, cols), "x", x)
     if out is None:
         out = x.new_empty((rows, cols), dtype=torch.int8), x.new_empty((rows,),
@@ -1066,6 +1075,7 @@ def quantize_int8(x, out=None):
 
 @functools.lru_cache(maxsize=256)
 def _int8_bytes(rows, cols):
+    _int32((rows, cols), "workspace")
     return int(lib().ep_integer_workspace_bytes(_ROWS(0, 0, rows, 1, 1, 0, rows), cols))
 
 
@@ -1081,6 +1091,7 @@ def int8_linear(x, w, layout=None, x_scales=None, out=None, workspace=None):
         raise ValueError("w: need an Int8Weight")
     cap, C = x.shape
     O = w.shape[-2]
+    _int32(w.shape, "w")
     desc = _int8_weight(w, "w", _of_experts(layout, O, C), x)
     rows = _rows(x, layout)
     if x_scales is None:

@@ -89,3 +89,36 @@ def test_gradients_of_weights():
     assert i < 65536 // 8
     assert accepted(grad(region(64, E), H, 8 * i))
     assert grad(region(64, E), H, 8 * (i + 1)) == INVALID
+
+
+def test_sizes_beyond_32_bits(monkeypatch):
+    """The binding refuses what ctypes would cut to 32 bits: 2^32 + 16 columns are not 16."""
+    class Matrix:                            # of any size, without memory
+        def __init__(self, *shape):
+            self.shape = shape
+
+        def get_device(self):
+            return 0
+
+        def data_ptr(self):
+            return FAR[0]
+        new_empty = checked_desc = lambda self, *a, **kw: self
+
+    monkeypatch.setattr(ep, "_arg", lambda *a: None)
+    monkeypatch.setattr(ep, "_call", lambda *a: pytest.fail("a call with sizes cut off"))
+    wide, many, x = Matrix(1, 2 ** 32 + 16), Matrix(2 ** 32 + 1, 16), Matrix(1, 16)
+    big = ep.Int8Weight.__new__(ep.Int8Weight)
+    big.__dict__.update(shape=(2 ** 32 + 16, 16), codes=x, scales=x, desc=(FAR[0], FAR[0], 0, 3, 0))
+    for call in (lambda: ep.quantize_int8(wide), lambda: ep.quantize_int8(many),
+                 lambda: ep.expert_ffn(many, Matrix(32, 16), Matrix(16, 16)),
+                 lambda: ep.expert_ffn(x, Matrix(2 ** 33 + 32, 16), Matrix(16, 2 ** 32 + 16),
+                                       out=x),
+                 lambda: ep.expert_ffn_backward(x, x, x, Matrix(2 ** 33 + 32, 16),
+                                                Matrix(16, 2 ** 32 + 16), out=(x, x, x)),
+                 lambda: ep.int8_linear(x, big, x_scales=x),
+                 lambda: ep.ffn_workspace_bytes(4, 2 ** 32 + 64, 32),
+                 lambda: ep.ffn_workspace_bytes(4, 64, -2 ** 32 + 32),
+                 lambda: ep.ffn_workspace_bytes(2 ** 32 + 4, 64, 32),
+                 lambda: ep.ep_integer_workspace_bytes(4, 2 ** 32 + 64)):
+        with pytest.raises(ValueError):
+            call()
