@@ -44,6 +44,8 @@
 
 #include "ep_host.h"
 
+#include <algorithm>
+
 // Cache policy of the streaming accesses (measured on MI355X): token rows
 // read by dispatch use ordinary loads, expert rows read by combine use
 // non-temporal loads; dispatch stores its rows non-temporally, combine writes
@@ -863,8 +865,11 @@ __device__ __forceinline__ void quant_row_fp8(const u32x4* __restrict__ row,
 // the piece is read from HBM once) gains nothing at S = 2 and loses at S = 4
 // (158.3 / 175.3 us).  Lanes past H (when H % 1024 != 0) hold whole groups:
 // they load clamped addresses, take part in the shuffles and store nothing.
-// A launch holds at most kItemLaunch items; larger problems take several.
-constexpr int64_t kItemLaunch = 1 << 30;
+// A launch holds at most kItemLaunch workgroups, of up to 256 threads: a grid has less than
+// 2^32 threads (with more, their number wraps and items stay undone without an error).
+// Larger problems take several launches.
+constexpr int64_t kItemLaunch = 1 << 23;
+static_assert(kItemLaunch * 256 < (int64_t)1 << 32, "threads of a grid");
 
 __global__ __launch_bounds__(64) void dispatch_fp8_item_kernel(
     const u32x4* __restrict__ x, const float* __restrict__ w, const int32_t* __restrict__ slot_of,
@@ -937,6 +942,7 @@ constexpr int kPieceWaves = EP_PIECE_WAVES;
 constexpr int kPieceThreads = 64 * kPieceWaves;
 constexpr int kPieceChunks = EP_PIECE_CHUNKS;
 static_assert(kPieceChunks % 64 == 0 && kPieceChunks <= kPieceThreads * 4, "piece geometry");
+static_assert(kItemLaunch * kPieceThreads < (int64_t)1 << 32, "threads of a grid");
 
 __global__ __launch_bounds__(kPieceThreads) void dispatch_piece_kernel(
     const u32x4* __restrict__ x, const float* __restrict__ w, const int32_t* __restrict__ slot_of,
@@ -980,20 +986,23 @@ __global__ __launch_bounds__(kPieceThreads) void dispatch_piece_kernel(
 // per pass) and stored to each of the token's K slots, with their scales.
 // Workgroups past the tokens do the auxiliary work.
 constexpr int kTokPerBlock = kThreads / 64;
+static_assert(kItemLaunch * kThreads < (int64_t)1 << 32, "threads of a grid");
 
 template <int NV>
 __global__ __launch_bounds__(kThreads) void dispatch_token_kernel(
     const u32x4* __restrict__ x, const float* __restrict__ xs, const float* __restrict__ w,
     const int32_t* __restrict__ slot_of, u32x4* __restrict__ recv_x,
     float* __restrict__ recv_scales, int32_t* __restrict__ recv_src, float* __restrict__ recv_w,
-    int N, int K, int H, int64_t cap, DispatchAux aux) {
-  const int tok_blocks = (N + kTokPerBlock - 1) / kTokPerBlock;
-  if ((int)blockIdx.x >= tok_blocks) {
-    aux_block<kThreads>((int64_t)blockIdx.x - tok_blocks, aux);
+    int N, int K, int H, int64_t block0, int64_t cap, DispatchAux aux) {
+  const int64_t b = block0 + blockIdx.x;
+  const int64_t tok_blocks = ((int64_t)N + kTokPerBlock - 1) / kTokPerBlock;
+  if (b >= tok_blocks) {
+    aux_block<kThreads>(b - tok_blocks, aux);
     return;
   }
-  const int t = uniform((int)blockIdx.x * kTokPerBlock + (int)(threadIdx.x >> 6));
-  if (t >= N) return;
+  const int64_t tok = b * kTokPerBlock + (threadIdx.x >> 6);
+  if (tok >= N) return;
+  const int t = uniform((int)tok);
   const int lane = threadIdx.x & 63;
   const int myslot = load_slot(slot_of, t, K, lane, cap);
   copy_row<64, NV>(x + (int64_t)t * (H >> 4), recv_x, myslot, K, H >> 4, lane);
@@ -1496,11 +1505,11 @@ Plan make_plan(const ep_problem_t* p) {
 
 template <int NV>
 void launch_dispatch_token(int grid, hipStream_t st, const ep_problem_t* p,
-                           const ep_dispatch_args_t* a, const DispatchAux& aux) {
+                           const ep_dispatch_args_t* a, const DispatchAux& aux, int64_t block0) {
   dispatch_token_kernel<NV><<<grid, kThreads, 0, st>>>(
       (const u32x4*)a->x, a->x_scales, a->topk_weights, a->slot_of, (u32x4*)a->recv_x,
       a->recv_scales, a->recv_src_idx, a->recv_topk_weights, p->num_tokens, p->num_topk,
-      p->hidden, a->recv_capacity, aux);
+      p->hidden, block0, a->recv_capacity, aux);
 }
 
 void launch_dispatch_piece(int grid, hipStream_t st, const ep_problem_t* p,
@@ -1778,14 +1787,12 @@ int ep_dispatch_ex(const ep_problem_t* p, const ep_dispatch_args_t* a, void* str
     if (items + n_aux == 0) return EP_OK;
     EP_LOG("dispatch e4m3 N=%d H=%d K=%d cap=%lld: items=%lld (pieces %d) aux items=%lld", N, H,
            K, (long long)cap, (long long)items, P, (long long)n_aux);
-    for (int64_t item0 = 0;; item0 += kItemLaunch) {
-      const int64_t left = items - item0;
-      const bool last = left <= kItemLaunch;
-      const int64_t grid = last ? left + n_aux : kItemLaunch;
-      if (grid > INT32_MAX) return EP_ERR_INVALID_ARG;
-      launch_dispatch_fp8_item((int)grid, st, p, a, aux, P, item0, items);
-      if ((rc = check_launch("dispatch")) != EP_OK || last) return rc;
+    for (int64_t item0 = 0; item0 < items + n_aux; item0 += kItemLaunch) {
+      const int grid = (int)std::min(items + n_aux - item0, kItemLaunch);
+      launch_dispatch_fp8_item(grid, st, p, a, aux, P, item0, items);
+      if ((rc = check_launch("dispatch")) != EP_OK) return rc;
     }
+    return EP_OK;
   }
   if (mode == 0) {
     // bf16: (token, 2 KiB piece) workgroups, then the auxiliary blocks
@@ -1797,34 +1804,34 @@ int ep_dispatch_ex(const ep_problem_t* p, const ep_dispatch_args_t* a, void* str
            "(tags %lld, zero rows %lld, stats %lld)", N, H, K, (long long)cap, (long long)items, P,
            (long long)n_aux, (long long)aux.tag_items, (long long)aux.zero_items,
            (long long)aux.stat_items);
-    for (int64_t item0 = 0;; item0 += kItemLaunch) {
-      const int64_t left = items - item0;
-      const bool last = left <= kItemLaunch;
-      const int64_t grid = last ? left + aux_blocks : kItemLaunch;
-      if (grid > INT32_MAX) return EP_ERR_INVALID_ARG;
-      launch_dispatch_piece((int)grid, st, p, a, aux, P, item0, items);
-      if ((rc = check_launch("dispatch")) != EP_OK || last) return rc;
+    for (int64_t item0 = 0; item0 < items + aux_blocks; item0 += kItemLaunch) {
+      const int grid = (int)std::min(items + aux_blocks - item0, kItemLaunch);
+      launch_dispatch_piece(grid, st, p, a, aux, P, item0, items);
+      if ((rc = check_launch("dispatch")) != EP_OK) return rc;
     }
+    return EP_OK;
   }
   // pre-quantised e4m3: one wavefront per token, then the auxiliary blocks
   const int64_t grid = ((int64_t)N + kTokPerBlock - 1) / kTokPerBlock +
                        (n_aux + kTokPerBlock - 1) / kTokPerBlock;
-  if (grid > INT32_MAX) return EP_ERR_INVALID_ARG;
   if (grid == 0) return EP_OK;
   EP_LOG("dispatch pre-quantised e4m3 N=%d H=%d K=%d cap=%lld: token blocks=%d aux items=%lld "
          "(tags %lld, zero rows %lld, stats %lld)", N, H, K, (long long)cap,
          (N + kTokPerBlock - 1) / kTokPerBlock, (long long)n_aux, (long long)aux.tag_items,
          (long long)aux.zero_items, (long long)aux.stat_items);
-  const int g = (int)grid;
-#define EP_DT(NV) launch_dispatch_token<NV>(g, st, p, a, aux)
-  if (q <= 1) EP_DT(1);
-  else if (q <= 2) EP_DT(2);
-  else if (q <= 4) EP_DT(4);
-  else if (q <= 7) EP_DT(7);
-  else if (q <= 8) EP_DT(8);
-  else EP_DT(16);
+  for (int64_t block0 = 0; block0 < grid; block0 += kItemLaunch) {
+    const int g = (int)std::min(grid - block0, kItemLaunch);
+#define EP_DT(NV) launch_dispatch_token<NV>(g, st, p, a, aux, block0)
+    if (q <= 1) EP_DT(1);
+    else if (q <= 2) EP_DT(2);
+    else if (q <= 4) EP_DT(4);
+    else if (q <= 7) EP_DT(7);
+    else if (q <= 8) EP_DT(8);
+    else EP_DT(16);
 #undef EP_DT
-  return check_launch("dispatch");
+    if ((rc = check_launch("dispatch")) != EP_OK) return rc;
+  }
+  return EP_OK;
 }
 
 int ep_dispatch(const ep_problem_t* p, const void* x, const float* topk_weights,
