@@ -20,6 +20,8 @@ expert on its rows, bf16 or 8-bit integer weights (``Int8Weight``), and
     d_expert_out, d_weights = combine_backward(dy, expert_out, lay, topk_weights)
     d_recv_x, dw13, dw2 = expert_ffn_backward(d_expert_out, recv_x, gate_up, w13, w2, layout=lay)
 
+None of these is connected to autograd: outputs never require a gradient.
+
 Around them: ``route`` decides ``topk_idx`` and ``topk_weights`` from gate
 logits; ``moe_layer`` is the whole expert layer for a few tokens (up to 256),
 without dispatch and combine, on bf16 or 4-bit expert weights
@@ -971,8 +973,9 @@ def expert_ffn(x, w13, w2, layout=None, out=None, gate_up=None, workspace=None):
     y = (silu(x Wg^T) * (x Wu^T)) W2^T (see ep_ffn).  ``layout`` says where the rows lie:
     a Layout (x = recv_x of dispatch), an LLLayout (of ll_dispatch), or None for a plain
     matrix, whose weights have no expert axis.  ``w13`` [E, 2*I, H] (gate rows first) and
-    ``w2`` [E, H, I] are bf16 tensors or both Int8Weight.  Slots without a row are
-    neither read nor written.  ``out`` [cap, H]; ``gate_up`` [cap, 2*I] bf16 receives
+    ``w2`` [E, H, I] are bf16 tensors or both Int8Weight.  Rows are bf16 (e4m3 rows of
+    dispatch(use_fp8=True) are not taken).  Slots without a row are neither read nor
+    written.  ``out`` [cap, H]; ``gate_up`` [cap, 2*I] bf16 receives
     what expert_ffn_backward needs; ``workspace`` from alloc_ffn_workspace."""
     import torch
     cap, H = x.shape

@@ -16,15 +16,19 @@
 //                   tiles.  A tile's step (128 bytes of the contraction) is 2048 cycles of
 //                   MFMA on each SIMD and 64 KiB of operands, which go straight to LDS two
 //                   steps deep and are read with few bank conflicts.  Bound by the MFMAs and,
-//                   with them, by the card's power: at 8192 rows by 8192 x 4096 in bf16
-//                   1310 TFLOP/s (a large library product: 1260 to 1550 here) and 2050
-//                   TOP/s at 8192^3 int8 (2060 to 2120), at 1.75 GHz with the MFMAs busy 78 %
-//                   of the cycles; without any load they are 82 %, the rest is barriers.
+//                   with them, by the card's power: gate and up of 8192 rows of 8192, 4096
+//                   columns, in bf16 1270 TFLOP/s at 1.59 GHz, the MFMAs busy 82 % of the
+//                   cycles (a large library product: 1260 to 1550); 8192^3 int8 2220 TOP/s
+//                   at 1.61 GHz, 71 % (2060 to 2120).  Not counted in the cycles: 8 % of the
+//                   time, in which a CU has no work yet or none left.
 //                   Tiles of at most 128 rows have a loop of their own (stream): bound by
 //                   HBM, 6.9 TB/s of weights at 16 rows an expert.
 //   few_kernel      few rows: weights as a stream, the contraction split over wavefronts
 //   small_kernel    what lies between: 64 by 64 tiles on many CUs
 // One workgroup computes a value from one fixed order of sums: the same bits on every run.
+// h, dg and du are rounded to bf16 between the products, whose operands they are: float32
+// operands have a sixteenth of the bf16 MFMAs' rate.  It is most of what the block's error has
+// over that of one rounding of y (0.0023 of the norm, 0.0017).
 #include "ep_host.h"
 #include "ep_rows.h"
 
@@ -175,9 +179,9 @@ struct RowFactor {
   }
 };
 
-// What becomes of eight neighbouring columns of a row of D; put: of eight that are rounded
-// to bf16 already (bf16 products, where that comes first, with n % 8 == 0).  `slot` is the row's slot
-// (kOuter: its row of the expert's matrix), `e` the expert, `c` the first column.
+// What becomes of eight neighbouring columns of a row of D; put: of eight that store_block has
+// rounded to bf16 (`rounds`).  `slot` is the row's slot (kOuter: its row of the expert's
+// matrix), `e` the expert, `c` the first column; columns from n on are dropped.
 // `stores` is how many of them a wavefront sends at least for a whole tile (16 calls, 8 of
 // a gate).
 struct StoreRows {
@@ -1469,7 +1473,10 @@ int launch_small(const Product& p, const Epi& epi, int64_t tiles, hipStream_t st
 // weight: 1 row by 7168 x 7168 53, 11, -; 16 rows 53, 12, 14; 64 rows 63, 20, 17; 256 rows 68, 66,
 // 41; 980 rows by 861 x 7120 92, 52, 23; 4000 by 4000 x 512 23, 114, 70; 33 by 1237 x 2000 23, 6,
 // 9.  Both products of a bf16 block: 512 rows, 2048 x 1024 64, 35, 25; 2048 rows 67, 124, 80; 32
-// experts of about 16 rows, 7168 x 2048: first 273, 313, second 183, 171.
+// experts of about 16 rows, 7168 x 2048: first 273, 313, second 183, 171.  Row tiles are
+// estimated as at least one for each expert, also of fewer rows than experts: counted as
+// min(experts, rows) the choice is few rows, and slower (8-bit block, 512 experts, 2048 x 512,
+// 10 rows 35 us by wide tiles, 44 by few rows; 80 rows 81 : 123; bf16 has few rows either way).
 template <class Epi, bool I8>
 int run_rows(const Product& p, const Epi& epi, int max_rows, hipStream_t st) {
   const int E = p.rows.E, wide = Epi::gate ? 128 : kBN;

@@ -11,7 +11,7 @@ namespace {
 // A row by WAVES wavefronts, which hold up to CH 16-byte chunks per lane in registers (of a
 // longer row the rest is read twice); blocks (segment, part): segments are the experts, or the
 // sub-blocks of ep_ll_dispatch, whose rows are shared out over the parts.  4096 rows of
-// 7168: 18 us, one wavefront per row 24.
+// 7168: 18.7 us over and over on the same rows, one wavefront per row 24.7; 21 on new rows.
 template <int WAVES, int CH>
 __global__ __launch_bounds__(256) void quantize_kernel(Rows rows, const uint8_t* x, int cols,
                                                        uint8_t* codes, float* scales) {
@@ -66,8 +66,9 @@ constexpr int kTokensPerLaunch = 1 << 21;
 // A workgroup per token and four of its pairs, a thread per 16-byte chunk of the row (or
 // per several): all loads of a chunk are in flight at once, and dy's row is read once
 // for these pairs.  The sums meet in LDS at the end, in a fixed order.  4096 tokens of 8
-// pairs by 7168: 188 us, 5.3 TB/s of mixed reads and writes, whatever the pairs (8: 190, 2:
-// 188, 1: 225) or wavefronts per workgroup; 128 tokens: 7.7 us, with eight pairs 10.9.
+// pairs by 7168: 189 us, 5.3 TB/s of mixed reads and writes (a copy of 1 GiB: 5.15), whatever
+// the pairs (8: 190, 2: 188, 1: 225) or wavefronts per workgroup; 128 tokens: 7.4 us, with
+// eight pairs 10.9.
 __global__ __launch_bounds__(1024) void combine_backward_kernel(
     const u32x4* dy, const u32x4* eo, const int* slot_of, const float* wts, u32x4* deo,
     float* dwts, int H8, int K, int cap) {
